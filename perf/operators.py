@@ -253,8 +253,9 @@ def prepare(case, seed):
             s["lse"] = _cache_lse(s)
     if own:
         s["cache"] = E.Cache(s["k_codes"], s["k_scales"], s["v_codes"], s["v_scales"], s["table"])
-        if op == "attend":
-            n = E.cache_workspace_size(s["q_lens"], s["kv_lens"], s["heads"], s["kv_heads"], s["d"], s["topk"])
+        if op != "append":
+            shape = (s["q_lens"], s["kv_lens"], s["heads"], s["kv_heads"], s["d"])
+            n = E.cache_workspace_size(*shape, s["topk"]) if op == "attend" else E.weights_workspace_size(*shape)
             s["ws"] = torch.empty(n, dtype=torch.uint8, device=DEV)
     return s
 
@@ -456,7 +457,7 @@ def run(s):
         return s["out"], s["lse"]
     if op == "weights":
         E.dsa_cache_weights(s["cache"], s["q"], s["lse"], s["q_lens"], s["kv_lens"], s["acc"], s["acc_out"],
-                            scale=s["scale"])
+                            scale=s["scale"], workspace=s["ws"])
         return s["acc_out"]
     E.dsa_cache_evict(s["acc"], s["table"], s["kv_lens"], s["new_lens"],
                       [(s["k"], s["k"]), (s["v"], s["v"]), (s["acc"], s["acc_out"]), (s["pos"], s["pos_out"])],
