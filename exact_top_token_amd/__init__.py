@@ -8,6 +8,9 @@ functions mirror the C entry points of include/dosa_indexer.h:
                         -> compaction -> survivor scoring -> select)
     dsa_indexer_topk    dense scoring of every visible key + streaming Top-K
     workspace_size, default_config, status_string
+    dsa_prompt_attention, dsa_cache_append, dsa_cache_read, dsa_cache_attention,
+    dsa_cache_weights, dsa_cache_evict and their workspace sizes: attention next
+    to the indexer (attention.py)
 
 Importing the package never falls back to anything: if the shared library is
 missing, :func:`lib` raises.
@@ -37,7 +40,9 @@ STATUS = {0: "DOSA_OK", -1: "DOSA_ERR_INVALID_ARG", -2: "DOSA_ERR_UNSUPPORTED", 
 
 EXPORTS = ("dosa_default_config", "dosa_workspace_size", "dosa_indexer_topk", "dsa_indexer_topk",
            "dosa_indexer_topk_noalloc", "dosa_status_string", "dosa_version", "dosa_profile_begin",
-           "dosa_profile_end")
+           "dosa_profile_end", "dsa_prompt_workspace_size", "dsa_prompt_attention", "dsa_cache_append",
+           "dsa_cache_read", "dsa_cache_workspace_size", "dsa_cache_attention", "dsa_weights_workspace_size",
+           "dsa_cache_weights", "dsa_evict_workspace_size", "dsa_cache_evict")
 
 NOALLOC_SCRATCH_BYTES = 128 << 20   # DOSA_NOALLOC_SCRATCH_BYTES
 
@@ -137,6 +142,9 @@ def lib():
         L.dosa_profile_begin.restype = ctypes.c_int
         L.dosa_profile_end.argtypes = [ctypes.POINTER(DosaKernelTime), i32]
         L.dosa_profile_end.restype = ctypes.c_int
+        from . import attention
+
+        attention.declare(L)
         _lib = L
     return _lib
 
@@ -244,3 +252,20 @@ def dosa_indexer_topk_noalloc(q, q_dtype, q_scale, w, k, k_dtype, k_scale, q_len
     if st != 0:
         raise DosaError(st, status_string(st))
     return st
+
+
+from .attention import (  # noqa: E402,F401
+    Cache,
+    DsaCache,
+    DsaEvictArray,
+    cache_workspace_size,
+    dsa_cache_append,
+    dsa_cache_attention,
+    dsa_cache_evict,
+    dsa_cache_read,
+    dsa_cache_weights,
+    dsa_prompt_attention,
+    evict_workspace_size,
+    prompt_workspace_size,
+    weights_workspace_size,
+)

@@ -12,59 +12,24 @@
 
 #include "dosa_device.h"
 #include "dosa_internal.h"
+#include "host_common.h"
 
 using namespace dosa;
 
-namespace {
+namespace dosa {
 
 thread_local std::string g_err;
-
-// ---------------------------------------------------------------------------
-// optional per-pass event timing
-// ---------------------------------------------------------------------------
-enum PassId { P_NORMS = 0, P_SCORE_SEED, P_SELECT_SEED, P_PLAN, P_BOUND, P_COMPACT, P_SURV_TILES, P_SURV_LISTS,
-              P_SCORE_DENSE, P_SELECT_FINAL, P_PREP, P_PROBE, P_SEED_EXTRA, P_COUNT };
-const char* const kPassNames[P_COUNT] = {"key_norms", "score_seed", "select_seed", "plan", "bound", "compact",
-                                         "score_survivor_tiles", "score_survivor_lists", "score_dense",
-                                         "select_final", "prep", "probe", "seed_extra"};
-
-struct Profiler {
-  bool on = false;
-  std::vector<hipEvent_t> pool;
-  size_t used = 0;
-  std::vector<std::pair<int, size_t>> recs;   // (pass, index of start event; stop = +1)
-  hipEvent_t next() {
-    if (used == pool.size()) {
-      hipEvent_t e;
-      if (hipEventCreate(&e) != hipSuccess) return nullptr;
-      pool.push_back(e);
-    }
-    return pool[used++];
-  }
-};
 thread_local Profiler g_prof;
 
-struct PassScope {
-  hipStream_t s;
-  hipEvent_t stop = nullptr;
-  PassScope(int pass, hipStream_t st) : s(st) {
-    if (!g_prof.on) return;
-    const size_t at = g_prof.used;
-    hipEvent_t a = g_prof.next(), b = g_prof.next();
-    if (!a || !b) return;
-    hipEventRecord(a, s);
-    stop = b;
-    g_prof.recs.push_back({pass, at});
-  }
-  ~PassScope() {
-    if (stop) hipEventRecord(stop, s);
-  }
-};
+}  // namespace dosa
 
-int fail_hip(hipError_t e, const char* what) {
-  g_err = std::string(what) + ": " + hipGetErrorString(e);
-  return DOSA_ERR_HIP;
-}
+namespace {
+
+const char* const kPassNames[P_COUNT] = {"key_norms", "score_seed", "select_seed", "plan", "bound", "compact",
+                                         "score_survivor_tiles", "score_survivor_lists", "score_dense",
+                                         "select_final", "prep", "probe", "seed_extra", "prompt_attention",
+                                         "cache_attention", "attention_join", "cache_append", "cache_read",
+                                         "cache_weights", "weights_join", "evict_select", "evict_move"};
 
 // ---------------------------------------------------------------------------
 // The certificate stages of a call with a probe run on a side stream of the

@@ -1,0 +1,621 @@
+// C-ABI entry points of the attention side: argument checks, the split of the
+// work over the GPU, and the launches on the caller's stream.  Lengths travel
+// as kernel arguments: no call copies to the device, allocates or waits.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <string>
+#include <vector>
+
+#include "attn_internal.h"
+#include "host_common.h"
+
+using namespace dosa;
+
+namespace {
+
+constexpr int64_t kMaxInt = (int64_t(1) << 31) - 1;
+
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+// Lengths, with a <= b for every sequence; total of each.
+int check_lens(int32_t batch, const int32_t* a, const int32_t* b, const char* an, const char* bn, int64_t* ta,
+               int64_t* tb) {
+  if (batch < 0 || (batch > 0 && (a == nullptr || b == nullptr)))
+    return fail(DOSA_ERR_INVALID_ARG, std::string("batch < 0 or ") + an + "/" + bn + " NULL");
+  *ta = *tb = 0;
+  for (int i = 0; i < batch; ++i) {
+    if (a[i] < 0 || b[i] < 0 || a[i] > b[i])
+      return fail(DOSA_ERR_INVALID_ARG, "sequence " + std::to_string(i) + ": need 0 <= " + an + " <= " + bn);
+    *ta += a[i];
+    *tb += b[i];
+  }
+  if (*ta > kMaxInt || *tb > kMaxInt) return fail(DOSA_ERR_UNSUPPORTED, "more than 2^31 - 1 tokens in a batch");
+  return DOSA_OK;
+}
+
+int check_heads(int32_t Hq, int32_t Hkv, int32_t d) {
+  if (Hq <= 0 || Hkv <= 0 || d <= 0 || Hq % Hkv != 0)
+    return fail(DOSA_ERR_INVALID_ARG, "Hq must be a positive multiple of Hkv, d positive");
+  if ((d != 64 && d != 128) || Hkv > 128 || Hq > 1024)
+    return fail(DOSA_ERR_UNSUPPORTED, "d must be 64 or 128, Hkv at most 128, Hq at most 1024");
+  return DOSA_OK;
+}
+
+int check_scale(float scale) {
+  if (!(scale > 0.f) || !std::isfinite(scale)) return fail(DOSA_ERR_INVALID_ARG, "scale must be positive and finite");
+  return DOSA_OK;
+}
+
+int check_float(int32_t dtype) {
+  if (dtype != DOSA_F32 && dtype != DOSA_BF16) return fail(DOSA_ERR_UNSUPPORTED, "dtype must be fp32 or bf16");
+  return DOSA_OK;
+}
+
+// A packed operand [tokens, H, d] with a stride between tokens: 16-byte rows,
+// offsets within 64 tokens in 31 bits.
+int check_rows(const char* name, const void* p, int64_t stride, int32_t H, int32_t d, int32_t dtype, int64_t tokens) {
+  if (tokens == 0) return DOSA_OK;
+  const int64_t size = dtype == DOSA_F32 ? 4 : 2;
+  if (p == nullptr) return fail(DOSA_ERR_INVALID_ARG, std::string(name) + " is NULL");
+  if (stride < (int64_t)H * d || (stride * size) % 16 != 0 || !aligned(p, 16))
+    return fail(DOSA_ERR_INVALID_ARG, std::string(name) + ": token rows must not overlap and must be 16-byte aligned");
+  if (stride > (int64_t(1) << 23)) return fail(DOSA_ERR_UNSUPPORTED, std::string(name) + ": token stride above 2^23");
+  return DOSA_OK;
+}
+
+int check_pages(const int32_t* table, int32_t num_pages, int32_t page_size, int32_t max_pages, int32_t batch,
+                const int32_t* kv_lens) {
+  if (page_size <= 0 || page_size % 16 != 0 || num_pages <= 0 || max_pages < 0)
+    return fail(DOSA_ERR_INVALID_ARG, "page_size must be a positive multiple of 16, num_pages positive");
+  if ((int64_t)num_pages * page_size > kMaxInt) return fail(DOSA_ERR_UNSUPPORTED, "more than 2^31 - 1 cache slots");
+  for (int b = 0; b < batch; ++b) {
+    if (kv_lens[b] > 0 && table == nullptr) return fail(DOSA_ERR_INVALID_ARG, "page_table is NULL");
+    if ((int64_t)max_pages * page_size < kv_lens[b])
+      return fail(DOSA_ERR_INVALID_ARG, "sequence " + std::to_string(b) + ": its page table row ends before its keys");
+  }
+  return DOSA_OK;
+}
+
+int check_cache(const dsa_cache* c, int32_t batch, const int32_t* kv_lens) {
+  if (c == nullptr || c->k_codes == nullptr || c->k_scales == nullptr || c->v_codes == nullptr ||
+      c->v_scales == nullptr)
+    return fail(DOSA_ERR_INVALID_ARG, "cache or one of its buffers is NULL");
+  if (!aligned(c->k_codes, 16) || !aligned(c->v_codes, 16) || !aligned(c->k_scales, 4) || !aligned(c->v_scales, 4))
+    return fail(DOSA_ERR_INVALID_ARG, "cache codes must be 16-byte and scales 4-byte aligned");
+  if (c->reserved != 0) return fail(DOSA_ERR_INVALID_ARG, "dsa_cache.reserved must be 0");
+  return check_pages(c->page_table, c->num_pages, c->page_size, c->max_pages, batch, kv_lens);
+}
+
+CacheView view(const dsa_cache* c) {
+  return CacheView{static_cast<uint8_t*>(c->k_codes), static_cast<uint8_t*>(c->k_scales),
+                   static_cast<uint8_t*>(c->v_codes), static_cast<uint8_t*>(c->v_scales),
+                   c->page_table, c->page_size, c->max_pages, c->num_pages, c->Hkv};
+}
+
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+// ---------------------------------------------------------------------------
+// Work split of the wavefront attention kernel.  A unit is one row tile of one
+// kv head over one key range.  Ranges are cut so that the launch has about
+// kTargetUnits units of equal work (two rounds of the wavefronts the GPU
+// holds at eight a CU), none shorter than kMinKeys.
+// ---------------------------------------------------------------------------
+constexpr int64_t kTargetUnits = 4096;
+constexpr int64_t kMinKeys = 128;
+
+struct AttnChunk {
+  AttnArgs a;
+  int64_t parts = 0;
+};
+
+// Sequences b0.. of the batch, at most kAttnSeqs with queries; returns the
+// sequence after the last one taken, or -1 if the launch would be too large.
+int plan_attn(AttnChunk& ch, int src, int b0, int32_t batch, const int32_t* q_lens, const int32_t* kv_lens,
+              int32_t Hq, int32_t Hkv, int32_t topk, int64_t* q_row, int64_t* k_row) {
+  AttnArgs& a = ch.a;
+  const bool sel = topk > 0;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.group = Hq / Hkv;
+  a.topk = topk;
+  a.n_seq = 0;
+  int b = b0;
+  int64_t most = 0;
+  for (; b < batch && a.n_seq < kAttnSeqs; ++b) {
+    if (q_lens[b] > 0) {
+      AttnSeq& s = a.s[a.n_seq++];
+      s = AttnSeq{};
+      s.q_row0 = (int32_t)*q_row;
+      s.q_len = q_lens[b];
+      s.kv_len = kv_lens[b];
+      s.b = b;
+      s.key_base = *k_row;
+      most = std::max<int64_t>(most, sel ? a.group : (int64_t)q_lens[b] * a.group);
+    }
+    *q_row += q_lens[b];
+    *k_row += kv_lens[b];
+  }
+  a.rt = most > 16 ? attn_max_rt(src) : 1;
+  const int64_t tile = 16 * a.rt;
+  auto tiles = [&](const AttnSeq& s) -> int64_t {
+    return sel ? (int64_t)s.q_len * ((a.group + tile - 1) / tile) : ((int64_t)s.q_len * a.group + tile - 1) / tile;
+  };
+  auto keys = [&](const AttnSeq& s) -> int64_t { return sel ? topk : s.kv_len; };
+  std::stable_sort(a.s, a.s + a.n_seq, [&](const AttnSeq& x, const AttnSeq& y) { return keys(x) > keys(y); });
+  int64_t work = 0;
+  for (int i = 0; i < a.n_seq; ++i) work += tiles(a.s[i]) * Hkv * keys(a.s[i]);
+  const int64_t len = std::max(kMinKeys, (work + kTargetUnits - 1) / kTargetUnits);
+  int64_t units = 0, join = 0, parts = 0;
+  for (int i = 0; i < a.n_seq; ++i) {
+    AttnSeq& s = a.s[i];
+    const int64_t k = keys(s), nrt = tiles(s);
+    int64_t n = std::max<int64_t>(1, (k + len - 1) / len);
+    const int64_t sl = ((k + n - 1) / n + 63) / 64 * 64;
+    n = (k + sl - 1) / sl;
+    if (nrt * n * Hkv > kMaxInt || units + nrt * n * Hkv > kMaxInt) return -1;
+    s.n_rt = (int32_t)nrt;
+    s.n_split = (int32_t)n;
+    s.split_len = (int32_t)sl;
+    s.unit0 = (int32_t)units;
+    s.join0 = (int32_t)join;
+    s.part0 = (int32_t)parts;
+    units += nrt * n * Hkv;
+    if (n > 1) {
+      join += nrt * Hkv * tile;
+      parts += nrt * n * Hkv;
+    }
+    if (join > kMaxInt) return -1;
+  }
+  a.n_units = (int32_t)units;
+  a.n_join = (int32_t)join;
+  ch.parts = parts;
+  return b;
+}
+
+size_t part_bytes(const AttnChunk& ch, int d) {
+  const size_t rows = (size_t)ch.parts * 16 * ch.a.rt;
+  return up256(rows * d * sizeof(float)) + up256(rows * 2 * sizeof(float));
+}
+
+// Bytes of partial results the call's launches need (each launch reuses them);
+// 0 if a launch would be too large.
+size_t attn_workspace(int src, int32_t batch, const int32_t* q_lens, const int32_t* kv_lens, int32_t Hq, int32_t Hkv,
+                      int32_t d, int32_t topk) {
+  size_t most = 256;
+  int64_t qr = 0, kr = 0;
+  for (int b = 0; b < batch;) {
+    AttnChunk ch;
+    b = plan_attn(ch, src, b, batch, q_lens, kv_lens, Hq, Hkv, topk, &qr, &kr);
+    if (b < 0) return 0;
+    most = std::max(most, part_bytes(ch, d));
+  }
+  return most;
+}
+
+int run_attn(int src, AttnArgs base, int32_t batch, const int32_t* q_lens, const int32_t* kv_lens, int32_t d,
+             void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  const size_t need = attn_workspace(src, batch, q_lens, kv_lens, base.Hq, base.Hkv, d, base.topk);
+  if (need == 0) return fail(DOSA_ERR_UNSUPPORTED, "too many row tiles and key ranges for one launch");
+  if (workspace == nullptr || workspace_bytes < need || !aligned(workspace, 16))
+    return fail(DOSA_ERR_WORKSPACE, "workspace needs " + std::to_string(need) + " bytes, 16-byte aligned");
+  int64_t qr = 0, kr = 0;
+  for (int b = 0; b < batch;) {
+    AttnChunk ch;
+    ch.a = base;
+    b = plan_attn(ch, src, b, batch, q_lens, kv_lens, base.Hq, base.Hkv, base.topk, &qr, &kr);
+    AttnArgs& a = ch.a;
+    const size_t rows = (size_t)ch.parts * 16 * a.rt;
+    a.part_o = static_cast<float*>(workspace);
+    a.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + up256(rows * d * sizeof(float)));
+    hipError_t e;
+    {
+      PassScope ps(src == A_F32 || src == A_BF16 ? P_PROMPT : P_ATTEND, stream);
+      e = launch_attn(src, d, a, stream);
+    }
+    if (e != hipSuccess) return fail_hip(e, "attention kernel launch");
+    {
+      PassScope ps(P_ATTEND_JOIN, stream);
+      e = launch_attn_join(src, d, a, stream);
+    }
+    if (e != hipSuccess) return fail_hip(e, "attention join launch");
+  }
+  return DOSA_OK;
+}
+
+// ---------------------------------------------------------------------------
+// Work split of the weights kernel: workgroups per 64-key tile, so that the
+// launch has about kWeightUnits of them and none is left without a row tile.
+// ---------------------------------------------------------------------------
+constexpr int64_t kWeightUnits = 1024;
+
+int plan_weights(WeightArgs& a, int64_t* parts, int b0, int32_t batch, const int32_t* q_lens, const int32_t* kv_lens,
+                 int32_t Hq, int32_t Hkv, int64_t* q_row) {
+  a.Hq = Hq;
+  a.group = Hq / Hkv;
+  a.n_seq = 0;
+  int b = b0;
+  int64_t work = 0;
+  for (; b < batch && a.n_seq < kAttnSeqs; ++b) {
+    if (q_lens[b] > 0) {
+      WeightSeq& s = a.s[a.n_seq++];
+      s = WeightSeq{};
+      s.q_row0 = (int32_t)*q_row;
+      s.q_len = q_lens[b];
+      s.kv_len = kv_lens[b];
+      s.b = b;
+      work += ((int64_t)s.kv_len + 63) / 64 * (((int64_t)s.q_len * a.group + 15) / 16 * Hkv);
+    }
+    *q_row += q_lens[b];
+  }
+  std::stable_sort(a.s, a.s + a.n_seq, [](const WeightSeq& x, const WeightSeq& y) { return x.q_len > y.q_len; });
+  int64_t units = 0, tiles = 0;
+  *parts = 0;
+  const int64_t share = std::max<int64_t>(8, (work + kWeightUnits - 1) / kWeightUnits);   // row tiles x heads a workgroup
+  for (int i = 0; i < a.n_seq; ++i) {
+    WeightSeq& s = a.s[i];
+    const int64_t nt = ((int64_t)s.kv_len + 63) / 64;
+    const int64_t w = ((int64_t)s.q_len * a.group + 15) / 16 * Hkv;
+    const int64_t np = std::min<int64_t>(64, std::max<int64_t>(1, w / share));
+    s.n_part = (int32_t)np;
+    s.unit0 = (int32_t)units;
+    s.tile0 = (int32_t)tiles;
+    s.part0 = (int32_t)*parts;
+    units += nt * np;
+    tiles += nt;
+    if (np > 1) *parts += nt * np;
+    if (units > kMaxInt) return -1;
+  }
+  a.n_units = (int32_t)units;
+  a.n_tiles = *parts > 0 ? (int32_t)tiles : 0;
+  return b;
+}
+
+size_t weights_workspace(int32_t batch, const int32_t* q_lens, const int32_t* kv_lens, int32_t Hq, int32_t Hkv) {
+  size_t most = 256;
+  int64_t qr = 0;
+  for (int b = 0; b < batch;) {
+    WeightArgs a;
+    int64_t parts;
+    b = plan_weights(a, &parts, b, batch, q_lens, kv_lens, Hq, Hkv, &qr);
+    if (b < 0) return 0;
+    most = std::max(most, up256((size_t)parts * 64 * sizeof(float)));
+  }
+  return most;
+}
+
+int cache_io(bool write, const dsa_cache* cache, void* k, int64_t k_stride, void* v, int64_t v_stride, int32_t dtype,
+             const int32_t* q_lens, const int32_t* kv_lens, int32_t batch, int32_t* pos, const int32_t* seen_lens,
+             hipStream_t stream) {
+  int64_t tq, tk;
+  int st = check_lens(batch, q_lens, kv_lens, "q_len", "kv_len", &tq, &tk);
+  if (st == DOSA_OK) st = check_cache(cache, batch, kv_lens);
+  if (st == DOSA_OK) st = check_heads(cache->Hkv, cache->Hkv, cache->d);
+  if (st == DOSA_OK) st = check_float(dtype);
+  if (st == DOSA_OK) st = check_rows("k", k, k_stride, cache->Hkv, cache->d, dtype, tq);
+  if (st == DOSA_OK) st = check_rows("v", v, v_stride, cache->Hkv, cache->d, dtype, tq);
+  if (st != DOSA_OK) return st;
+  for (int b = 0; seen_lens != nullptr && b < batch; ++b)
+    if (seen_lens[b] < kv_lens[b])
+      return fail(DOSA_ERR_INVALID_ARG, "sequence " + std::to_string(b) + ": need seen_len >= kv_len");
+  CacheIoArgs a{};
+  a.cache = view(cache);
+  a.k = k;
+  a.v = v;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.pos = pos;
+  int64_t row = 0;
+  for (int b = 0; b < batch;) {
+    a.n_seq = 0;
+    for (; b < batch && a.n_seq < kAttnSeqs; ++b) {
+      if (q_lens[b] > 0)
+        a.s[a.n_seq++] = CacheSeq{(int32_t)row, q_lens[b], kv_lens[b] - q_lens[b],
+                                  (seen_lens != nullptr ? seen_lens[b] : kv_lens[b]) - q_lens[b], b};
+      row += q_lens[b];
+    }
+    if (a.n_seq == 0) continue;
+    PassScope ps(write ? P_APPEND : P_READ, stream);
+    const hipError_t e = write ? launch_cache_append(dtype == DOSA_F32, cache->d, a, stream)
+                               : launch_cache_read(dtype == DOSA_F32, cache->d, a, stream);
+    if (e != hipSuccess) return fail_hip(e, write ? "cache append launch" : "cache read launch");
+  }
+  return DOSA_OK;
+}
+
+size_t evict_workspace(int32_t batch, const int32_t* new_lens, int32_t* stride) {
+  int64_t most = 1;
+  for (int b = 0; b < batch; ++b) most = std::max<int64_t>(most, new_lens[b]);
+  most = (most + 63) / 64 * 64;
+  *stride = (int32_t)std::min<int64_t>(most, kMaxInt);
+  return up256((size_t)std::max(batch, 1) * most * sizeof(int32_t));
+}
+
+template <class F>
+int guarded(F f) {
+  try {
+    return f();
+  } catch (...) {
+    g_err = "internal error";
+    return DOSA_ERR_HIP;
+  }
+}
+
+template <class F>
+size_t guarded_size(F f) {
+  try {
+    return f();
+  } catch (...) {
+    g_err = "internal error";
+    return 0;
+  }
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t dsa_prompt_workspace_size(int32_t batch, const int32_t* q_lens, const int32_t* kv_lens, int32_t Hq, int32_t Hkv,
+                                 int32_t d, int32_t dtype) {
+  return guarded_size([&]() -> size_t {
+    int64_t tq, tk;
+    if (check_lens(batch, q_lens, kv_lens, "q_len", "kv_len", &tq, &tk) != DOSA_OK ||
+        check_heads(Hq, Hkv, d) != DOSA_OK || check_float(dtype) != DOSA_OK)
+      return 0;
+    return attn_workspace(dtype == DOSA_F32 ? A_F32 : A_BF16, batch, q_lens, kv_lens, Hq, Hkv, d, 0);
+  });
+}
+
+int dsa_prompt_attention(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                         int64_t v_stride, int32_t dtype, const int32_t* q_lens, const int32_t* kv_lens, int32_t batch,
+                         int32_t Hq, int32_t Hkv, int32_t d, float scale, void* out, float* lse, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+  return guarded([&]() -> int {
+    int64_t tq, tk;
+    int st = check_lens(batch, q_lens, kv_lens, "q_len", "kv_len", &tq, &tk);
+    if (st == DOSA_OK) st = check_heads(Hq, Hkv, d);
+    if (st == DOSA_OK) st = check_float(dtype);
+    if (st == DOSA_OK) st = check_scale(scale);
+    if (st == DOSA_OK) st = check_rows("q", q, q_stride, Hq, d, dtype, tq);
+    if (st == DOSA_OK) st = check_rows("k", k, k_stride, Hkv, d, dtype, tq > 0 ? tk : 0);
+    if (st == DOSA_OK) st = check_rows("v", v, v_stride, Hkv, d, dtype, tq > 0 ? tk : 0);
+    if (st == DOSA_OK) st = check_rows("out", out, (int64_t)Hq * d, Hq, d, dtype, tq);
+    if (st != DOSA_OK) return st;
+    AttnArgs a{};
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.out = out;
+    a.lse = lse;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.scale = scale;
+    return run_attn(dtype == DOSA_F32 ? A_F32 : A_BF16, a, batch, q_lens, kv_lens, d, workspace, workspace_bytes,
+                    static_cast<hipStream_t>(stream));
+  });
+}
+
+int dsa_cache_append(const dsa_cache* cache, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                     int32_t dtype, const int32_t* q_lens, const int32_t* kv_lens, int32_t batch, int32_t* pos,
+                     const int32_t* seen_lens, void* stream) {
+  return guarded([&]() -> int {
+    return cache_io(true, cache, const_cast<void*>(k), k_stride, const_cast<void*>(v), v_stride, dtype, q_lens,
+                    kv_lens, batch, pos, seen_lens, static_cast<hipStream_t>(stream));
+  });
+}
+
+int dsa_cache_read(const dsa_cache* cache, void* k, int64_t k_stride, void* v, int64_t v_stride, int32_t dtype,
+                   const int32_t* q_lens, const int32_t* kv_lens, int32_t batch, void* stream) {
+  return guarded([&]() -> int {
+    return cache_io(false, cache, k, k_stride, v, v_stride, dtype, q_lens, kv_lens, batch, nullptr, nullptr,
+                    static_cast<hipStream_t>(stream));
+  });
+}
+
+size_t dsa_cache_workspace_size(int32_t batch, const int32_t* q_lens, const int32_t* kv_lens, int32_t Hq, int32_t Hkv,
+                                int32_t d, int32_t topk) {
+  return guarded_size([&]() -> size_t {
+    int64_t tq, tk;
+    if (check_lens(batch, q_lens, kv_lens, "q_len", "kv_len", &tq, &tk) != DOSA_OK ||
+        check_heads(Hq, Hkv, d) != DOSA_OK)
+      return 0;
+    if (topk < 0 || topk > (1 << 20)) return 0;
+    return std::max(attn_workspace(A_MX, batch, q_lens, kv_lens, Hq, Hkv, d, topk),
+                    attn_workspace(A_MX32, batch, q_lens, kv_lens, Hq, Hkv, d, topk));
+  });
+}
+
+int dsa_cache_attention(const dsa_cache* cache, const void* q, int64_t q_stride, int32_t q_dtype,
+                        const int32_t* q_lens, const int32_t* kv_lens, int32_t batch, int32_t Hq, const int32_t* idx,
+                        int32_t topk, float scale, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                        void* stream) {
+  return guarded([&]() -> int {
+    int64_t tq, tk;
+    int st = check_lens(batch, q_lens, kv_lens, "q_len", "kv_len", &tq, &tk);
+    if (st == DOSA_OK) st = check_cache(cache, batch, kv_lens);
+    if (st == DOSA_OK) st = check_heads(Hq, cache->Hkv, cache->d);
+    if (st == DOSA_OK) st = check_float(q_dtype);
+    if (st == DOSA_OK) st = check_scale(scale);
+    if (st == DOSA_OK) st = check_rows("q", q, q_stride, Hq, cache->d, q_dtype, tq);
+    if (st == DOSA_OK) st = check_rows("out", out, (int64_t)Hq * cache->d, Hq, cache->d, q_dtype, tq);
+    if (st != DOSA_OK) return st;
+    if (idx == nullptr ? topk != 0 : topk <= 0)
+      return fail(DOSA_ERR_INVALID_ARG, "topk must be positive with idx, 0 without");
+    if (topk > (1 << 20)) return fail(DOSA_ERR_UNSUPPORTED, "topk above 2^20");
+    AttnArgs a{};
+    a.q = q;
+    a.q_stride = q_stride;
+    a.cache = view(cache);
+    a.idx = idx;
+    a.topk = topk;
+    a.out = out;
+    a.lse = lse;
+    a.Hq = Hq;
+    a.Hkv = cache->Hkv;
+    a.scale = scale;
+    return run_attn(q_dtype == DOSA_F32 ? A_MX32 : A_MX, a, batch, q_lens, kv_lens, cache->d, workspace,
+                    workspace_bytes, static_cast<hipStream_t>(stream));
+  });
+}
+
+size_t dsa_weights_workspace_size(int32_t batch, const int32_t* q_lens, const int32_t* kv_lens, int32_t Hq,
+                                  int32_t Hkv, int32_t d) {
+  return guarded_size([&]() -> size_t {
+    int64_t tq, tk;
+    if (check_lens(batch, q_lens, kv_lens, "q_len", "kv_len", &tq, &tk) != DOSA_OK ||
+        check_heads(Hq, Hkv, d) != DOSA_OK)
+      return 0;
+    return weights_workspace(batch, q_lens, kv_lens, Hq, Hkv);
+  });
+}
+
+int dsa_cache_weights(const dsa_cache* cache, const void* q, int64_t q_stride, int32_t q_dtype, const float* lse,
+                      const int32_t* q_lens, const int32_t* kv_lens, int32_t batch, int32_t Hq, float scale,
+                      const float* acc, float* acc_out, void* workspace, size_t workspace_bytes, void* stream) {
+  return guarded([&]() -> int {
+    int64_t tq, tk;
+    int st = check_lens(batch, q_lens, kv_lens, "q_len", "kv_len", &tq, &tk);
+    if (st == DOSA_OK) st = check_cache(cache, batch, kv_lens);
+    if (st == DOSA_OK) st = check_heads(Hq, cache->Hkv, cache->d);
+    if (st == DOSA_OK) st = check_float(q_dtype);
+    if (st == DOSA_OK) st = check_scale(scale);
+    if (st == DOSA_OK) st = check_rows("q", q, q_stride, Hq, cache->d, q_dtype, tq);
+    if (st != DOSA_OK) return st;
+    if (tq > 0 && (lse == nullptr || acc_out == nullptr)) return fail(DOSA_ERR_INVALID_ARG, "lse or acc_out is NULL");
+    const size_t need = weights_workspace(batch, q_lens, kv_lens, Hq, cache->Hkv);
+    if (need == 0) return fail(DOSA_ERR_UNSUPPORTED, "too many key tiles for one launch");
+    if (workspace == nullptr || workspace_bytes < need || !aligned(workspace, 16))
+      return fail(DOSA_ERR_WORKSPACE, "workspace needs " + std::to_string(need) + " bytes, 16-byte aligned");
+    int64_t qr = 0;
+    for (int b = 0; b < batch;) {
+      WeightArgs a{};
+      int64_t parts;
+      b = plan_weights(a, &parts, b, batch, q_lens, kv_lens, Hq, cache->Hkv, &qr);
+      a.cache = view(cache);
+      a.q = q;
+      a.q_stride = q_stride;
+      a.lse = lse;
+      a.acc = acc;
+      a.acc_out = acc_out;
+      a.part = static_cast<float*>(workspace);
+      a.scale = scale;
+      hipError_t e;
+      {
+        PassScope ps(P_WEIGHTS, static_cast<hipStream_t>(stream));
+        e = launch_weights(q_dtype == DOSA_F32, cache->d, a, static_cast<hipStream_t>(stream));
+      }
+      if (e != hipSuccess) return fail_hip(e, "weights kernel launch");
+      {
+        PassScope ps(P_WEIGHTS_JOIN, static_cast<hipStream_t>(stream));
+        e = launch_weights_join(a, static_cast<hipStream_t>(stream));
+      }
+      if (e != hipSuccess) return fail_hip(e, "weights join launch");
+    }
+    return DOSA_OK;
+  });
+}
+
+size_t dsa_evict_workspace_size(int32_t batch, const int32_t* kv_lens, const int32_t* new_lens) {
+  return guarded_size([&]() -> size_t {
+    int64_t tn, tk;
+    if (check_lens(batch, new_lens, kv_lens, "new_len", "kv_len", &tn, &tk) != DOSA_OK) return 0;
+    int32_t stride;
+    return evict_workspace(batch, new_lens, &stride);
+  });
+}
+
+int dsa_cache_evict(const float* acc, const int32_t* pos, const int32_t* page_table, int32_t page_size,
+                    int32_t max_pages, int32_t num_pages, const int32_t* kv_lens, const int32_t* new_lens,
+                    const int32_t* seen_lens, int32_t batch, int32_t prefix, int32_t window,
+                    const dsa_evict_array* arrays, int32_t n_arrays, int32_t* out_src, int32_t out_stride,
+                    void* workspace, size_t workspace_bytes, void* stream) {
+  return guarded([&]() -> int {
+    int64_t tn, tk;
+    int st = check_lens(batch, new_lens, kv_lens, "new_len", "kv_len", &tn, &tk);
+    if (st == DOSA_OK) st = check_pages(page_table, num_pages, page_size, max_pages, batch, kv_lens);
+    if (st != DOSA_OK) return st;
+    if (prefix < 0 || window < 0) return fail(DOSA_ERR_INVALID_ARG, "prefix and window must not be negative");
+    if (pos == nullptr && seen_lens != nullptr)
+      return fail(DOSA_ERR_INVALID_ARG, "seen_lens without pos: without positions the keys are the whole text");
+    for (int b = 0; b < batch; ++b) {
+      if (std::min<int64_t>((int64_t)prefix + window, kv_lens[b]) > new_lens[b])
+        return fail(DOSA_ERR_INVALID_ARG, "sequence " + std::to_string(b) + ": prefix + window protect more keys than new_len");
+      if (new_lens[b] > out_stride) return fail(DOSA_ERR_INVALID_ARG, "out_stride is shorter than a new_len");
+      if (seen_lens != nullptr && seen_lens[b] < kv_lens[b])
+        return fail(DOSA_ERR_INVALID_ARG, "sequence " + std::to_string(b) + ": need seen_len >= kv_len");
+    }
+    if (n_arrays < 0 || n_arrays > kEvictArrays || (n_arrays > 0 && arrays == nullptr))
+      return fail(DOSA_ERR_INVALID_ARG, "n_arrays must be in 0.." + std::to_string(kEvictArrays) + ", with arrays");
+    if (batch == 0 || out_stride == 0) return DOSA_OK;
+    if (acc == nullptr || out_src == nullptr) return fail(DOSA_ERR_INVALID_ARG, "acc or out_src is NULL");
+    EvictMoveArgs mv{};
+    for (int i = 0; i < n_arrays; ++i) {
+      const dsa_evict_array& x = arrays[i];
+      if (x.src == nullptr || x.dst == nullptr || x.row_bytes <= 0)
+        return fail(DOSA_ERR_INVALID_ARG, "array " + std::to_string(i) + ": NULL pointer or no row bytes");
+      if (x.row_bytes > (1 << 24)) return fail(DOSA_ERR_UNSUPPORTED, "array " + std::to_string(i) + ": rows above 2^24 bytes");
+      for (int j = 0; j < n_arrays; ++j)
+        if (j != i && (arrays[j].dst == x.dst || arrays[j].src == static_cast<const void*>(x.dst)))
+          return fail(DOSA_ERR_INVALID_ARG, "array " + std::to_string(i) + " writes where another one reads or writes");
+      if (x.dst == static_cast<const void*>(acc) || (pos != nullptr && x.dst == static_cast<const void*>(pos))) {
+        // in place only from itself: the choice has read it by then
+        if (x.dst != x.src) return fail(DOSA_ERR_INVALID_ARG, "array " + std::to_string(i) + " would overwrite acc or pos");
+      }
+      int gran = 1;
+      for (int g : {16, 4})
+        if (gran == 1 && x.row_bytes % g == 0 && aligned(x.src, g) && aligned(x.dst, g)) gran = g;
+      mv.a[i] = EvictArray{static_cast<const uint8_t*>(x.src), static_cast<uint8_t*>(x.dst), (int32_t)x.row_bytes, gran};
+    }
+    EvictArgs a{};
+    const size_t need = evict_workspace(batch, new_lens, &a.move_stride);
+    if (workspace == nullptr || workspace_bytes < need || !aligned(workspace, 16))
+      return fail(DOSA_ERR_WORKSPACE, "workspace needs " + std::to_string(need) + " bytes, 16-byte aligned");
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    a.acc = acc;
+    a.pos = pos;
+    a.table = page_table;
+    a.page_size = page_size;
+    a.max_pages = max_pages;
+    a.num_pages = num_pages;
+    a.prefix = prefix;
+    a.window = window;
+    a.out_src = out_src;
+    a.out_stride = out_stride;
+    a.moves = static_cast<int32_t*>(workspace);
+    mv.out_src = out_src;
+    mv.table = page_table;
+    mv.out_stride = out_stride;
+    mv.page_size = page_size;
+    mv.max_pages = max_pages;
+    mv.num_pages = num_pages;
+    mv.n_arr = n_arrays;
+    for (int b0 = 0; b0 < batch; b0 += kEvictSeqs) {
+      a.n_seq = mv.n_seq = std::min(kEvictSeqs, batch - b0);
+      mv.max_new = 0;
+      for (int i = 0; i < a.n_seq; ++i) {
+        const int b = b0 + i;
+        a.s[i] = EvictSeq{kv_lens[b], new_lens[b], seen_lens != nullptr ? seen_lens[b] : kv_lens[b], b};
+        mv.s[i] = a.s[i];
+        mv.max_new = std::max(mv.max_new, new_lens[b]);
+      }
+      hipError_t e;
+      {
+        PassScope ps(P_EVICT_SELECT, s);
+        e = launch_evict_select(a, s);
+      }
+      if (e != hipSuccess) return fail_hip(e, "eviction select launch");
+      {
+        PassScope ps(P_EVICT_MOVE, s);
+        e = launch_evict_move(mv, s);
+      }
+      if (e != hipSuccess) return fail_hip(e, "eviction move launch");
+    }
+    return DOSA_OK;
+  });
+}
+
+}  // extern "C"

@@ -1,0 +1,143 @@
+// Declarations shared by the attention entry points' host code and kernels.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "../../include/dosa_indexer.h"
+
+namespace dosa {
+
+// Sequences of one launch.  Their records travel as kernel arguments (which a
+// captured graph keeps), so a call copies nothing to the device; a larger
+// batch takes several launches.
+constexpr int kAttnSeqs = 64;
+
+// The paged 4-bit cache as the kernels see it.
+struct CacheView {
+  uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
+  const int32_t* table;    // [batch, max_pages]
+  int32_t page_size, max_pages, num_pages, Hkv;
+};
+
+// Where an attention kernel finds its keys and values, and its queries' type:
+// contiguous fp32 or bf16 rows, or the 4-bit cache read for bf16 or for fp32
+// queries.
+enum AttnSrc : int { A_F32 = 0, A_BF16 = 1, A_MX = 2, A_MX32 = 3 };
+
+struct AttnSeq {
+  int32_t unit0;      // first unit (wavefront task) of the sequence in this launch
+  int32_t join0;      // first row of the join launch (sequences with n_split > 1)
+  int32_t part0;      // first partial result (sequences with n_split > 1)
+  int32_t q_row0;     // first query row of the packed queries
+  int32_t q_len, kv_len;
+  int32_t b;          // row of the page table / of the batch
+  int32_t n_split, split_len;   // key ranges, keys of each (a multiple of 64)
+  int32_t n_rt;       // row tiles
+  int64_t key_base;   // contiguous keys: row of the sequence's key 0
+};
+
+struct AttnArgs {
+  const void* q;
+  const void* k;      // contiguous sources
+  const void* v;
+  CacheView cache;    // cache sources
+  const int32_t* idx; // selected keys [total_q, topk], or NULL
+  void* out;          // [total_q, Hq, d] of q's type
+  float* lse;         // [total_q, Hq] or NULL
+  float* part_o;      // partial outputs [parts, 16 * row tiles, d]
+  float* part_ml;     // partial maxima and sums [parts, 16 * row tiles, 2]
+  int64_t q_stride, k_stride, v_stride;   // elements between token rows
+  int32_t topk, Hq, Hkv, group;           // group = Hq / Hkv
+  float scale;
+  int32_t n_seq, n_units, n_join, rt;     // rt: 16-row tiles per unit
+  AttnSeq s[kAttnSeqs];
+};
+
+// 16-row tiles one wavefront may hold (chosen by the host from the row count).
+inline int attn_max_rt(int src) { return src == A_MX32 ? 1 : 2; }
+
+hipError_t launch_attn(int src, int d, const AttnArgs& p, hipStream_t s);
+hipError_t launch_attn_join(int src, int d, const AttnArgs& p, hipStream_t s);
+
+// Cache write and read-back.
+struct CacheSeq {
+  int32_t row0;       // first token row of the packed tokens
+  int32_t n;          // tokens
+  int32_t pos0;       // logical position of the first
+  int32_t seen0;      // value of pos[] of the first
+  int32_t b;
+};
+struct CacheIoArgs {
+  CacheView cache;
+  void* k;            // [total, Hkv, d]
+  void* v;
+  int64_t k_stride, v_stride;
+  int32_t* pos;       // [num_pages, page_size] or NULL (write only)
+  int32_t n_seq, total;
+  CacheSeq s[kAttnSeqs];
+};
+hipError_t launch_cache_append(bool f32, int d, const CacheIoArgs& p, hipStream_t s);
+hipError_t launch_cache_read(bool f32, int d, const CacheIoArgs& p, hipStream_t s);
+
+// Accumulated attention weights.
+struct WeightSeq {
+  int32_t unit0;      // first workgroup
+  int32_t tile0;      // first 64-key tile (of all tiles of the launch)
+  int32_t part0;      // first 64-float partial of the sequence
+  int32_t q_row0, q_len, kv_len, b;
+  int32_t n_part;     // workgroups per 64-key tile
+};
+struct WeightArgs {
+  CacheView cache;
+  const void* q;
+  const float* lse;
+  const float* acc;   // or NULL
+  float* acc_out;
+  float* part;        // [parts, 64]
+  int64_t q_stride;
+  int32_t Hq, group;
+  float scale;
+  int32_t n_seq, n_units, n_tiles;
+  WeightSeq s[kAttnSeqs];
+};
+hipError_t launch_weights(bool f32, int d, const WeightArgs& p, hipStream_t s);
+hipError_t launch_weights_join(const WeightArgs& p, hipStream_t s);
+
+// Eviction.
+struct EvictSeq {
+  int32_t kv_len, new_len, seen, b;
+};
+constexpr int kEvictSeqs = 64;
+struct EvictArgs {
+  const float* acc;         // [num_pages, page_size]
+  const int32_t* pos;       // [num_pages, page_size] or NULL
+  const int32_t* table;
+  int32_t page_size, max_pages, num_pages;
+  int32_t prefix, window;
+  int32_t* out_src;         // [batch, out_stride]
+  int32_t out_stride;
+  int32_t* moves;           // workspace, move_stride ints a sequence: movers (ascending)
+  int32_t move_stride;
+  int32_t n_seq;
+  EvictSeq s[kEvictSeqs];
+};
+struct EvictArray {
+  const uint8_t* src;
+  uint8_t* dst;
+  int32_t row_bytes;
+  int32_t gran;             // bytes of one access: 16, 4 or 1
+};
+constexpr int kEvictArrays = 16;
+struct EvictMoveArgs {
+  const int32_t* out_src;
+  const int32_t* table;
+  int32_t out_stride, page_size, max_pages, num_pages;
+  int32_t n_seq, n_arr;
+  int32_t max_new;          // largest new_len
+  EvictSeq s[kEvictSeqs];
+  EvictArray a[kEvictArrays];
+};
+hipError_t launch_evict_select(const EvictArgs& p, hipStream_t s);
+hipError_t launch_evict_move(const EvictMoveArgs& p, hipStream_t s);
+
+}  // namespace dosa

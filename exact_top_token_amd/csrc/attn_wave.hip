@@ -1,0 +1,635 @@
+// Attention by independent wavefronts: each takes one 16-row tile of a kv
+// head's query rows (or two) and one range of keys, and keeps everything in
+// registers.  Rows are the queries of a sequence times the query heads that
+// share the kv head, so a single token with grouped heads still fills the
+// matrix instruction's rows.
+//
+//   s_j = q . k_j,  m = max_j s_j,  p_j = 2^((s_j - m) c),  c = scale log2(e),
+//   o = sum_j p_j v_j / sum_j p_j,  lse = scale m + ln sum_j p_j,
+//
+// in one pass over the keys with the running maximum and sum in fp32.
+//
+// Layout.  The scores are computed transposed, S^T = K Q^T: the 16x16 product
+// then leaves lane l with row l%16 and keys 4(l/16)..+3 of each 16-key tile,
+// which is what the second product, O^T = V^T P^T, wants of its right operand
+// when its reduction slots are numbered the same way.  So the weights go from
+// one product to the other without leaving their lane, and the running
+// statistics of a row sit in the lanes that hold its outputs.  V^T needs, per
+// lane, several keys of one dimension: lane n of 16 loads D/16 neighbouring
+// dimensions of its keys and swaps halves with v_perm, so value rows stay
+// row-major in memory and are read with whole-row bursts.
+//
+// 4-bit rows become bf16 in the converter (exact), 32-dimension blocks match
+// a lane's share of a key row.  The weights are rounded to bf16 before the
+// second product (2^-9 relative on average sqrt-summed over keys; the sum in
+// the denominator is taken before the rounding); with fp32 queries both the
+// queries and the weights go as three bf16 terms, which keeps fp32 products.
+#include <type_traits>
+
+#include "attn_device.h"
+
+namespace dosa {
+
+namespace {
+
+constexpr int kWaves = 8;   // largest wavefronts per workgroup
+
+template <int SRC>
+struct SrcTraits {
+  static constexpr bool MX = SRC == A_MX || SRC == A_MX32;
+  static constexpr int KT = MX ? 4 : (SRC == A_BF16 ? 2 : 1);     // 16-key tiles per step
+  static constexpr int TERMS = SRC == A_MX32 ? 3 : 1;             // bf16 terms of queries and weights
+  static constexpr bool F32IO = SRC == A_F32 || SRC == A_MX32;    // type of q and out
+};
+
+// One step's keys and values of a lane.
+template <int SRC, int D>
+struct Stage;
+
+template <int D>
+struct MxStage {
+  static constexpr int NS = D / 32;
+  uint32_t k[4][NS];    // per 16-key tile: key l%16, dims [g D/4, (g+1) D/4)
+  uint32_t v[16];       // per key 16t+4g+r: dims [n D/16, (n+1) D/16)
+  uint32_t ks, vs;      // scale bytes of key l of the step
+  uint32_t mask;        // bit 4t+r: key 16t+4g+r is not there
+};
+template <int D>
+struct Stage<A_MX, D> : MxStage<D> {};
+template <int D>
+struct Stage<A_MX32, D> : MxStage<D> {};
+template <int D>
+struct Stage<A_BF16, D> {
+  i4 k[2][D / 32];
+  uint32_t v[8][D / 32];
+};
+template <int D>
+struct Stage<A_F32, D> {
+  float k[D / 4];
+  float v[4][D / 16];
+};
+
+template <int SRC, int D, int RT, bool SEL>
+__global__ __launch_bounds__(64 * kWaves) void attn_kernel(const AttnArgs p) {
+  using T = SrcTraits<SRC>;
+  constexpr int KT = T::KT, STEP = 16 * KT, TERMS = T::TERMS;
+  constexpr int NT = D / 16, NS = D / 32;
+  constexpr bool MX = T::MX;
+  __shared__ __attribute__((aligned(16))) uint32_t lds[MX ? kWaves : 1][3][64];   // key scales, value scales, slots
+
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int unit = blockIdx.x * (int)(blockDim.x >> 6) + wave;
+  if (unit >= p.n_units) return;
+  const AttnSeq& sq = p.s[find_seq(p.s, p.n_seq, unit, [](const AttnSeq& s) { return s.unit0; })];
+  const int lane = lane64(), n = lane & 15, g = lane >> 4;
+  int t = unit - sq.unit0;
+  const int head = t % p.Hkv;
+  t /= p.Hkv;
+  // last row tile first: under the causal mask it sees the most keys
+  const int split = t % sq.n_split, rt0 = sq.n_rt - 1 - t / sq.n_split;
+
+  // rows of this unit: dense (query, group head) pairs of the sequence; with
+  // selected keys the group heads of one query
+  const int tiles_q = SEL ? (p.group + 16 * RT - 1) / (16 * RT) : 1;
+  const int q_first = SEL ? rt0 / tiles_q : 0;
+  const int row_base = (SEL ? rt0 % tiles_q : rt0) * (16 * RT);
+  const int n_rows = SEL ? p.group : sq.q_len * p.group;
+  int row_q[RT], row_h[RT], vis[RT];     // query, head, visible keys of row l%16 of each tile
+  bool row_ok[RT];
+#pragma unroll
+  for (int i = 0; i < RT; ++i) {
+    int r = row_base + 16 * i + n;
+    row_ok[i] = r < n_rows;
+    r = r < n_rows ? r : n_rows - 1;
+    row_q[i] = q_first + r / p.group;
+    row_h[i] = head * p.group + r % p.group;
+    vis[i] = sq.kv_len - sq.q_len + row_q[i] + 1;
+  }
+  const int last_row = (row_base + 16 * RT < n_rows ? row_base + 16 * RT : n_rows) - 1;
+  const int vis_last = sq.kv_len - sq.q_len + q_first + last_row / p.group + 1;
+  const int vis_first = sq.kv_len - sq.q_len + q_first + row_base / p.group + 1;
+  const int key_lo = split * sq.split_len;
+  const int all = SEL ? p.topk : vis_last;
+  const int key_hi = (int64_t)key_lo + sq.split_len < all ? key_lo + sq.split_len : all;
+
+  // queries: lane (row l%16, g) holds dims [g D/4, (g+1) D/4)
+  b8 qf[SRC == A_F32 ? 1 : RT][TERMS][NS];
+  float qs[SRC == A_F32 ? RT : 1][D / 4];
+#pragma unroll
+  for (int i = 0; i < RT; ++i) {
+    const int64_t at = (int64_t)(sq.q_row0 + row_q[i]) * p.q_stride + (int64_t)row_h[i] * D + g * (D / 4);
+    if constexpr (T::F32IO) {
+      const float* src = static_cast<const float*>(p.q) + at;
+      float x[D / 4];
+#pragma unroll
+      for (int e = 0; e < D / 16; ++e) {
+        const f4 y = reinterpret_cast<const f4*>(src)[e];
+        x[4 * e] = y[0]; x[4 * e + 1] = y[1]; x[4 * e + 2] = y[2]; x[4 * e + 3] = y[3];
+      }
+      if constexpr (SRC == A_F32) {
+#pragma unroll
+        for (int e = 0; e < D / 4; ++e) qs[i][e] = x[e];
+      } else {
+#pragma unroll
+        for (int s = 0; s < NS; ++s)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            float tt[3];
+            split3(x[8 * s + e], tt);
+#pragma unroll
+            for (int w = 0; w < TERMS; ++w) qf[i][w][s][e] = (__bf16)tt[w];
+          }
+      }
+    } else {
+      const i4* src = reinterpret_cast<const i4*>(static_cast<const uint16_t*>(p.q) + at);
+#pragma unroll
+      for (int s = 0; s < NS; ++s) qf[i][0][s] = __builtin_bit_cast(b8, src[s]);
+    }
+  }
+
+  f4 o[RT][NT];
+  float m[RT], l[RT];
+#pragma unroll
+  for (int i = 0; i < RT; ++i) {
+    m[i] = -INFINITY;
+    l[i] = 0.f;
+#pragma unroll
+    for (int j = 0; j < NT; ++j) o[i][j] = f4{0.f, 0.f, 0.f, 0.f};
+  }
+  const float c = p.scale * kLog2e;
+
+  // ---- where a step's rows are ----
+  const CacheView& cv = p.cache;
+  const int row_b = cv.Hkv * (D / 2), row_s = cv.Hkv * (D / 32);
+  // 64 consecutive keys of a step lie in one page when the page size is a
+  // multiple of 64: one table entry, constant offsets
+  const bool paged64 = MX && !SEL && (cv.page_size & 63) == 0;
+  const int64_t sel_row = SEL ? (int64_t)(sq.q_row0 + q_first) * p.topk : 0;
+
+  // logical position of entry `e` of this lane, -1 if there is none
+  auto entry = [&](int e) -> int {
+    if constexpr (SEL) {
+      const int pos = e < key_hi ? p.idx[sel_row + e] : -1;
+      return pos < vis_first ? pos : -1;
+    } else {
+      return e < key_hi ? e : -1;
+    }
+  };
+
+  auto load = [&](Stage<SRC, D>& st, int key0) {
+    if constexpr (MX) {
+      typedef uint32_t kvec __attribute__((ext_vector_type(NS)));
+      const uint8_t *kb = cv.k_codes + head * (D / 2), *vb = cv.v_codes + head * (D / 2);
+      const uint8_t *ksb = cv.k_scales + head * (D / 32), *vsb = cv.v_scales + head * (D / 32);
+      auto scale_bytes = [&](const uint8_t* a) -> uint32_t {
+        if constexpr (D == 128) return *reinterpret_cast<const uint32_t*>(a);
+        else return *reinterpret_cast<const uint16_t*>(a);
+      };
+      if (paged64) {
+        const int pg = key0 / cv.page_size;
+        int page = pg < cv.max_pages ? cv.table[(int64_t)sq.b * cv.max_pages + pg] : -1;
+        const bool bad = (uint32_t)page >= (uint32_t)cv.num_pages;
+        page = bad ? 0 : page;
+        const int64_t slot = (int64_t)page * cv.page_size + (key0 - pg * cv.page_size);
+        const uint8_t *k1 = kb + slot * row_b, *v1 = vb + slot * row_b;
+        // the scales of keys past the range are zero bytes, which keeps
+        // whatever their slots hold finite
+        const bool in = !bad && key0 + lane < key_hi;
+        st.ks = in ? scale_bytes(ksb + slot * row_s + lane * row_s) : 0u;
+        st.vs = in ? scale_bytes(vsb + slot * row_s + lane * row_s) : 0u;
+        st.mask = bad ? 0xffffu : 0u;
+#pragma unroll
+        for (int a = 0; a < KT; ++a) {
+          const kvec x = *reinterpret_cast<const kvec*>(k1 + (16 * a + n) * row_b + g * (D / 8));
+#pragma unroll
+          for (int s = 0; s < NS; ++s) st.k[a][s] = x[s];
+        }
+#pragma unroll
+        for (int a = 0; a < 16; ++a) {
+          const uint8_t* x = v1 + ((a >> 2) * 16 + 4 * g + (a & 3)) * row_b + n * (D / 32);
+          if constexpr (D == 128) st.v[a] = *reinterpret_cast<const uint32_t*>(x);
+          else st.v[a] = *reinterpret_cast<const uint16_t*>(x);
+        }
+      } else {
+        const int pos = entry(key0 + lane);
+        const int slot = pos >= 0 ? cache_slot(cv.table, sq.b, cv.max_pages, cv.page_size, cv.num_pages, pos) : -1;
+        const int64_t safe = slot < 0 ? 0 : slot;
+        st.ks = slot >= 0 ? scale_bytes(ksb + safe * row_s) : 0u;
+        st.vs = slot >= 0 ? scale_bytes(vsb + safe * row_s) : 0u;
+        wave_sync();
+        lds[wave][2][lane] = (uint32_t)slot;
+        wave_sync();
+        st.mask = 0;
+#pragma unroll
+        for (int a = 0; a < KT; ++a) {
+          const int ksl = (int)lds[wave][2][16 * a + n];
+          const kvec x = *reinterpret_cast<const kvec*>(kb + (int64_t)(ksl < 0 ? 0 : ksl) * row_b + g * (D / 8));
+#pragma unroll
+          for (int s = 0; s < NS; ++s) st.k[a][s] = x[s];
+          const i4 vsl = *reinterpret_cast<const i4*>(&lds[wave][2][16 * a + 4 * g]);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            st.mask |= vsl[r] < 0 ? 1u << (4 * a + r) : 0u;
+            const uint8_t* y = vb + (int64_t)(vsl[r] < 0 ? 0 : vsl[r]) * row_b + n * (D / 32);
+            if constexpr (D == 128) st.v[4 * a + r] = *reinterpret_cast<const uint32_t*>(y);
+            else st.v[4 * a + r] = *reinterpret_cast<const uint16_t*>(y);
+          }
+        }
+      }
+    } else {
+      // contiguous rows; rows past the range repeat its last one
+      const int last = key_hi - 1 - key0;
+      const int64_t r0 = sq.key_base + key0;
+      if constexpr (SRC == A_BF16) {
+        const uint16_t* kb = static_cast<const uint16_t*>(p.k) + r0 * p.k_stride + head * D;
+        const uint16_t* vb = static_cast<const uint16_t*>(p.v) + r0 * p.v_stride + head * D;
+#pragma unroll
+        for (int a = 0; a < KT; ++a) {
+          const int kr = 16 * a + n < last ? 16 * a + n : last;
+          const i4* x = reinterpret_cast<const i4*>(kb + kr * p.k_stride + g * (D / 4));
+#pragma unroll
+          for (int s = 0; s < NS; ++s) st.k[a][s] = x[s];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int vr = 16 * a + 4 * g + r < last ? 16 * a + 4 * g + r : last;
+            const uint16_t* y = vb + vr * p.v_stride + n * NT;
+            if constexpr (D == 128) {
+              const i4 z = *reinterpret_cast<const i4*>(y);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) st.v[4 * a + r][e] = (uint32_t)z[e];
+            } else {
+              const i2 z = *reinterpret_cast<const i2*>(y);
+#pragma unroll
+              for (int e = 0; e < 2; ++e) st.v[4 * a + r][e] = (uint32_t)z[e];
+            }
+          }
+        }
+      } else {
+        const float* kb = static_cast<const float*>(p.k) + r0 * p.k_stride + head * D;
+        const float* vb = static_cast<const float*>(p.v) + r0 * p.v_stride + head * D;
+        const int kr = n < last ? n : last;
+        const f4* x = reinterpret_cast<const f4*>(kb + kr * p.k_stride + g * (D / 4));
+#pragma unroll
+        for (int e = 0; e < D / 16; ++e) {
+          const f4 z = x[e];
+          st.k[4 * e] = z[0]; st.k[4 * e + 1] = z[1]; st.k[4 * e + 2] = z[2]; st.k[4 * e + 3] = z[3];
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int vr = 4 * g + r < last ? 4 * g + r : last;
+          const f4* y = reinterpret_cast<const f4*>(vb + vr * p.v_stride + n * NT);
+#pragma unroll
+          for (int e = 0; e < NT / 4; ++e) {
+            const f4 z = y[e];
+            st.v[r][4 * e] = z[0]; st.v[r][4 * e + 1] = z[1]; st.v[r][4 * e + 2] = z[2]; st.v[r][4 * e + 3] = z[3];
+          }
+        }
+      }
+    }
+  };
+
+  auto compute = [&](const Stage<SRC, D>& st, int key0) {
+    f4 sc[RT][KT];
+    f4 vscale[KT];
+    if constexpr (MX) {
+      wave_sync();
+      lds[wave][0][lane] = st.ks;
+      lds[wave][1][lane] = st.vs;
+      wave_sync();
+    }
+    // ---- scores ----
+#pragma unroll
+    for (int a = 0; a < KT; ++a) {
+#pragma unroll
+      for (int i = 0; i < RT; ++i) sc[i][a] = f4{0.f, 0.f, 0.f, 0.f};
+      if constexpr (MX) {
+        const float ksc = mx_scale(lds[wave][0][16 * a + n], 8 * (D == 128 ? g : g >> 1));
+        const i4 vb = *reinterpret_cast<const i4*>(&lds[wave][1][16 * a + 4 * g]);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) vscale[a][r] = mx_scale((uint32_t)vb[r], 8 * (D == 128 ? n >> 2 : n >> 3));
+#pragma unroll
+        for (int s = 0; s < NS; ++s) {
+          const b8 kf = mx8(st.k[a][s], ksc);
+#pragma unroll
+          for (int w = TERMS - 1; w >= 0; --w)
+#pragma unroll
+            for (int i = 0; i < RT; ++i) sc[i][a] = mfma_bf16(kf, qf[i][w][s], sc[i][a]);
+        }
+      } else if constexpr (SRC == A_BF16) {
+#pragma unroll
+        for (int s = 0; s < NS; ++s)
+#pragma unroll
+          for (int i = 0; i < RT; ++i) sc[i][a] = mfma_bf16(__builtin_bit_cast(b8, st.k[a][s]), qf[i][0][s], sc[i][a]);
+      } else {
+#pragma unroll
+        for (int s = 0; s < D / 4; ++s)
+#pragma unroll
+          for (int i = 0; i < RT; ++i) sc[i][a] = mfma_f32(st.k[s], qs[i][s], sc[i][a]);
+      }
+    }
+    // ---- masks: only steps that reach past some row's visible keys ----
+    if constexpr (SEL) {
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int a = 0; a < KT; ++a)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            if constexpr (MX) sc[i][a][r] = (st.mask >> (4 * a + r)) & 1u ? -INFINITY : sc[i][a][r];
+    } else {
+      const int edge = vis_first < key_hi ? vis_first : key_hi;
+      bool part = key0 + STEP > edge;
+      if constexpr (MX) part = part || __any(st.mask != 0u);
+      if (part) {
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+          const int end = vis[i] < key_hi ? vis[i] : key_hi;
+#pragma unroll
+          for (int a = 0; a < KT; ++a)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              bool hide = key0 + 16 * a + 4 * g + r >= end;
+              if constexpr (MX) hide = hide || ((st.mask >> (4 * a + r)) & 1u);
+              sc[i][a][r] = hide ? -INFINITY : sc[i][a][r];
+            }
+        }
+      }
+    }
+    // ---- running maximum and sum ----
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      float top = sc[i][0][0];
+#pragma unroll
+      for (int a = 0; a < KT; ++a)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) top = fmaxf(top, sc[i][a][r]);
+      top = max_groups(top);
+      if (__any(top > m[i])) {
+        const float m_new = fmaxf(m[i], top);
+        // a row that has seen nothing yet: weight 1 on empty sums
+        const float f = m_new == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((m[i] - m_new) * c);
+        m[i] = m_new;
+        l[i] *= f;
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) o[i][j][r] *= f;
+      }
+      const float mc = m[i] == -INFINITY ? 0.f : m[i] * c;
+#pragma unroll
+      for (int a = 0; a < KT; ++a)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float e = __builtin_amdgcn_exp2f(fmaf(sc[i][a][r], c, -mc));
+          sc[i][a][r] = e;
+          l[i] += e;
+        }
+    }
+    // ---- weighted values ----
+    if constexpr (SRC == A_F32) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int i = 0; i < RT; ++i) o[i][j] = mfma_f32(st.v[r][j], sc[i][0][r], o[i][j]);
+    } else {
+#pragma unroll
+      for (int u = 0; u < KT / 2; ++u) {
+        b8 pf[RT][TERMS];
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float x = sc[i][2 * u + (e >> 2)][e & 3];
+            if constexpr (TERMS == 1) {
+              pf[i][0][e] = (__bf16)x;
+            } else {
+              float tt[3];
+              split3(x, tt);
+#pragma unroll
+              for (int w = 0; w < TERMS; ++w) pf[i][w][e] = (__bf16)tt[w];
+            }
+          }
+        auto pair = [&](auto bsel) {
+          constexpr int B = decltype(bsel)::value;
+          uint32_t x[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            if constexpr (MX) x[e] = mx2<B>(st.v[8 * u + e], vscale[2 * u + (e >> 2)][e & 3]);
+            else x[e] = st.v[8 * u + e][B];
+          }
+          const b8 lo = __builtin_bit_cast(b8, i4{(int)lows(x[0], x[1]), (int)lows(x[2], x[3]), (int)lows(x[4], x[5]),
+                                                  (int)lows(x[6], x[7])});
+          const b8 hi = __builtin_bit_cast(b8, i4{(int)highs(x[0], x[1]), (int)highs(x[2], x[3]),
+                                                  (int)highs(x[4], x[5]), (int)highs(x[6], x[7])});
+#pragma unroll
+          for (int w = TERMS - 1; w >= 0; --w)
+#pragma unroll
+            for (int i = 0; i < RT; ++i) {
+              o[i][2 * B] = mfma_bf16(lo, pf[i][w], o[i][2 * B]);
+              o[i][2 * B + 1] = mfma_bf16(hi, pf[i][w], o[i][2 * B + 1]);
+            }
+        };
+        pair(std::integral_constant<int, 0>{});
+        pair(std::integral_constant<int, 1>{});
+        if constexpr (NT == 8) {
+          pair(std::integral_constant<int, 2>{});
+          pair(std::integral_constant<int, 3>{});
+        }
+      }
+    }
+  };
+
+  if (key_lo < key_hi) {
+    Stage<SRC, D> cur, nxt;
+    load(cur, key_lo);
+#pragma unroll 2
+    for (int key0 = key_lo; key0 < key_hi; key0 += STEP) {
+      if (key0 + STEP < key_hi) load(nxt, key0 + STEP);
+      compute(cur, key0);
+      cur = nxt;
+    }
+  }
+
+  // ---- results: lane holds, of row l%16, dims NT (4g + r) + j ----
+#pragma unroll
+  for (int i = 0; i < RT; ++i) {
+    const float tot = sum_groups(l[i]);
+    if (sq.n_split > 1) {
+      const int64_t part = (int64_t)sq.part0 + (unit - sq.unit0);
+      const int64_t row = part * (16 * RT) + 16 * i + n;
+      float* po = p.part_o + row * D;
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int e = 0; e < NT / 4; ++e)
+          reinterpret_cast<f4*>(po + NT * (4 * g + r))[e] =
+              f4{o[i][4 * e][r], o[i][4 * e + 1][r], o[i][4 * e + 2][r], o[i][4 * e + 3][r]};
+      if (g == 0) {
+        p.part_ml[2 * row] = m[i];
+        p.part_ml[2 * row + 1] = tot;
+      }
+    } else if (row_ok[i]) {
+      const int64_t row = (int64_t)(sq.q_row0 + row_q[i]) * p.Hq + row_h[i];
+      const float inv = tot > 0.f ? 1.f / tot : 0.f;
+      if (p.lse != nullptr && g == 0)
+        p.lse[row] = tot > 0.f ? fmaf(m[i], p.scale, __builtin_amdgcn_logf(tot) * kLn2) : -INFINITY;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        if constexpr (T::F32IO) {
+          float* dst = static_cast<float*>(p.out) + row * D + NT * (4 * g + r);
+#pragma unroll
+          for (int e = 0; e < NT / 4; ++e)
+            reinterpret_cast<f4*>(dst)[e] = f4{o[i][4 * e][r] * inv, o[i][4 * e + 1][r] * inv, o[i][4 * e + 2][r] * inv,
+                                               o[i][4 * e + 3][r] * inv};
+        } else {
+          uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + row * D + NT * (4 * g + r));
+#pragma unroll
+          for (int e = 0; e < NT / 2; ++e) dst[e] = pack_bf16(o[i][2 * e][r] * inv, o[i][2 * e + 1][r] * inv);
+        }
+      }
+    }
+  }
+}
+
+// Join of the key ranges of one row, one workgroup of four wavefronts a row:
+// o = sum_s 2^((m_s - M) c) o_s / sum_s 2^((m_s - M) c) l_s with M = max m_s.
+// Ranges that saw no key (l = 0) are not read.
+template <bool F32IO, int D>
+__global__ __launch_bounds__(256) void attn_join_kernel(const AttnArgs p, int sel) {
+  constexpr int PER = D / 64;
+  __shared__ float so[4][D];
+  __shared__ float sm[4][2];
+  const int lane = lane64(), wave = threadIdx.x >> 6;
+  const int rows_u = 16 * p.rt;
+  const AttnSeq& sq = p.s[find_seq(p.s, p.n_seq, (int)blockIdx.x, [](const AttnSeq& s) { return s.join0; })];
+  int t = (int)blockIdx.x - sq.join0;
+  const int r_in = t % rows_u;
+  t /= rows_u;
+  const int head = t % p.Hkv, rtu = t / p.Hkv, rt0 = sq.n_rt - 1 - rtu;
+  const int tiles_q = sel ? (p.group + rows_u - 1) / rows_u : 1;
+  const int r = (sel ? rt0 % tiles_q : rt0) * rows_u + r_in;
+  if (r >= (sel ? p.group : sq.q_len * p.group)) return;
+  const int query = (sel ? rt0 / tiles_q : 0) + r / p.group;
+  const float c = p.scale * kLog2e;
+  const int64_t first = (int64_t)sq.part0 + (int64_t)rtu * sq.n_split * p.Hkv + head;
+  float M = -INFINITY, L = 0.f, o[PER] = {};
+  // wavefront w takes ranges w, w + 4, ...: 64 maxima and sums at a time, then their outputs
+  for (int s0 = wave; s0 < sq.n_split; s0 += 256) {
+    const int s = s0 + 4 * lane;
+    float ms = -INFINITY, ls = 0.f;
+    if (s < sq.n_split) {
+      const int64_t row = (first + (int64_t)s * p.Hkv) * rows_u + r_in;
+      ms = p.part_ml[2 * row];
+      ls = p.part_ml[2 * row + 1];
+      if (!(ls > 0.f)) ms = -INFINITY;
+    }
+    float top = ms;
+#pragma unroll
+    for (int x = 32; x >= 1; x >>= 1) top = fmaxf(top, __shfl_xor(top, x));
+    const float Mn = fmaxf(M, top);
+    if (Mn == -INFINITY) continue;
+    const float f = __builtin_amdgcn_exp2f((M - Mn) * c);
+    const float w = ms == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((ms - Mn) * c);
+    L = L * f + w * ls;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) o[e] *= f;
+    M = Mn;
+    const int cnt = min(64, (sq.n_split - s0 + 3) / 4);
+#pragma unroll 8
+    for (int i = 0; i < cnt; ++i) {
+      const float wi = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(w), i));
+      const int64_t row = (first + (int64_t)(s0 + 4 * i) * p.Hkv) * rows_u + r_in;
+      const float* src = p.part_o + row * D + PER * lane;
+#pragma unroll
+      for (int e = 0; e < PER; ++e) o[e] += wi > 0.f ? wi * src[e] : 0.f;
+    }
+  }
+#pragma unroll
+  for (int x = 32; x >= 1; x >>= 1) L += __shfl_xor(L, x);
+  if (lane == 0) {
+    sm[wave][0] = M;
+    sm[wave][1] = L;
+  }
+#pragma unroll
+  for (int e = 0; e < PER; ++e) so[wave][PER * lane + e] = o[e];
+  __syncthreads();
+  if (wave != 0) return;
+  const float top = fmaxf(fmaxf(sm[0][0], sm[1][0]), fmaxf(sm[2][0], sm[3][0]));
+  float tot = 0.f, x[PER] = {};
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const float f = sm[w][0] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((sm[w][0] - top) * c);
+    tot += f * sm[w][1];
+#pragma unroll
+    for (int e = 0; e < PER; ++e) x[e] += f * so[w][PER * lane + e];
+  }
+  const float inv = tot > 0.f ? 1.f / tot : 0.f;
+  const int64_t row = (int64_t)(sq.q_row0 + query) * p.Hq + head * p.group + r % p.group;
+  if (p.lse != nullptr && lane == 0)
+    p.lse[row] = tot > 0.f ? fmaf(top, p.scale, __builtin_amdgcn_logf(tot) * kLn2) : -INFINITY;
+  if constexpr (F32IO) {
+    float* dst = static_cast<float*>(p.out) + row * D + PER * lane;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) dst[e] = x[e] * inv;
+  } else if constexpr (PER == 2) {
+    reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + row * D)[lane] = pack_bf16(x[0] * inv, x[1] * inv);
+  } else {
+    static_cast<__bf16*>(p.out)[row * D + lane] = (__bf16)(x[0] * inv);
+  }
+}
+
+template <int SRC, int D, int RT>
+hipError_t go(const AttnArgs& p, hipStream_t s) {
+  // few units: smaller workgroups, so that they spread over more CUs
+  const int waves = p.n_units >= 2048 ? kWaves : (p.n_units >= 512 ? 4 : 2);
+  const dim3 grid((unsigned)((p.n_units + waves - 1) / waves)), block(64 * waves);
+  if (p.idx != nullptr) {
+    if constexpr (SrcTraits<SRC>::MX) attn_kernel<SRC, D, RT, true><<<grid, block, 0, s>>>(p);
+  } else {
+    attn_kernel<SRC, D, RT, false><<<grid, block, 0, s>>>(p);
+  }
+  return hipGetLastError();
+}
+
+template <int SRC, int D>
+hipError_t go_rt(const AttnArgs& p, hipStream_t s) {
+  if constexpr (SRC != A_MX32)
+    if (p.rt == 2) return go<SRC, D, 2>(p, s);
+  return go<SRC, D, 1>(p, s);
+}
+
+template <int D>
+hipError_t go_src(int src, const AttnArgs& p, hipStream_t s) {
+  switch (src) {
+    case A_F32: return go_rt<A_F32, D>(p, s);
+    case A_BF16: return go_rt<A_BF16, D>(p, s);
+    case A_MX: return go_rt<A_MX, D>(p, s);
+    default: return go_rt<A_MX32, D>(p, s);
+  }
+}
+
+}  // namespace
+
+hipError_t launch_attn(int src, int d, const AttnArgs& p, hipStream_t s) {
+  if (p.n_units == 0) return hipSuccess;
+  return d == 128 ? go_src<128>(src, p, s) : go_src<64>(src, p, s);
+}
+
+hipError_t launch_attn_join(int src, int d, const AttnArgs& p, hipStream_t s) {
+  if (p.n_join == 0) return hipSuccess;
+  const dim3 grid((unsigned)p.n_join), block(256);
+  const int sel = p.idx != nullptr;
+  const bool f32 = src == A_F32 || src == A_MX32;
+  if (d == 128) {
+    if (f32) attn_join_kernel<true, 128><<<grid, block, 0, s>>>(p, sel);
+    else attn_join_kernel<false, 128><<<grid, block, 0, s>>>(p, sel);
+  } else {
+    if (f32) attn_join_kernel<true, 64><<<grid, block, 0, s>>>(p, sel);
+    else attn_join_kernel<false, 64><<<grid, block, 0, s>>>(p, sel);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace dosa

@@ -258,6 +258,153 @@ int dosa_indexer_topk_noalloc(const void* q, int32_t q_dtype, const float* q_sca
                               int32_t* out_idx, float* out_score,
                               const dosa_config* cfg, dosa_stats* stats, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Attention next to the indexer: a prompt's causal attention, a paged cache of
+ * keys and values in 4 bits with the attention that reads it (every visible
+ * key, or the keys the indexer selected), the attention weight each cached key
+ * received, and the eviction of the keys that received least.
+ *
+ * Common to all of them.  Hq query heads share Hkv key/value heads, query head
+ * h reads kv head h / (Hq / Hkv).  Queries of a batch are packed as above;
+ * query i of sequence b sits at position kv_lens[b] - q_lens[b] + i and sees
+ * the keys at positions 0..position.  Packed operands are [tokens, heads, d]
+ * with the elements of a token together and a stride in ELEMENTS from one
+ * token to the next (a slice of a fused projection needs no copy); their
+ * first row and their stride must be 16-byte aligned.  Pointers are DEVICE
+ * pointers on the device current on the calling thread; lengths are HOST
+ * int32 [batch] and travel as kernel arguments, so a captured graph keeps the
+ * lengths it was captured with.  Sequences with q_len = 0 are skipped.
+ * Inputs must be finite.  Scores, maxima, sums and outputs accumulate in
+ * fp32.  The calls allocate nothing, copy nothing to the device and wait for
+ * nothing; they may be captured.  Calls that share a workspace must be
+ * ordered (one stream, or graphs replayed one after the other).  Results do
+ * not change from run to run.
+ *
+ * Supported: d in {64, 128}; Hkv <= 128, Hq <= 1024, Hq a multiple of Hkv;
+ * types DOSA_F32 and DOSA_BF16; fewer than 2^31 tokens in a batch and slots in
+ * a cache; token strides up to 2^23 elements.
+ */
+
+/* Causal attention of packed sequences over contiguous keys and values.
+ *   q   [total_q, Hq, d], k and v [total_k, Hkv, d] of dtype; sequence b's keys
+ *       at rows sum(kv_lens[0..b-1]) + position (as in the indexer), so whole
+ *       prompts (q_len = kv_len), later chunks of one and single tokens mix
+ *   out [total_q, Hq, d] of dtype:
+ *       out = sum_j w_j v_j,  w = softmax_j(scale * q . k_j)
+ *   lse [total_q, Hq] fp32 or NULL: ln sum_j exp(scale * q . k_j)
+ * With bf16 the softmax weights are rounded to bf16 for their product with v. */
+size_t dsa_prompt_workspace_size(int32_t batch, const int32_t* q_lens, const int32_t* kv_lens,
+                                 int32_t Hq, int32_t Hkv, int32_t d, int32_t dtype);
+int dsa_prompt_attention(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                         const void* v, int64_t v_stride, int32_t dtype,
+                         const int32_t* q_lens, const int32_t* kv_lens, int32_t batch,
+                         int32_t Hq, int32_t Hkv, int32_t d, float scale,
+                         void* out, float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/* A paged cache of keys and values in 4 bits (OCP microscaling FP4).
+ *   codes  [num_pages, page_size, Hkv, d/2] bytes: element 2i in the low,
+ *          2i+1 in the high nibble of byte i, each an E2M1 code (sign, two
+ *          exponent bits, one mantissa bit: 0, .5, 1, 1.5, 2, 3, 4, 6)
+ *   scales [num_pages, page_size, Hkv, d/32] bytes: byte e scales 32
+ *          consecutive elements by 2^(e-127), e in 0..254
+ * Codes must be 16-byte, scales 4-byte aligned.  Position j of sequence b is
+ * in page page_table[b*max_pages + j/page_size], slot j%page_size, as in the
+ * indexer; page_size is a multiple of 16 (multiples of 64 are read faster) and
+ * max_pages * page_size covers every kv_len.  A table entry outside
+ * 0..num_pages-1 names no page: its keys are not written and not seen (they
+ * read back as zeros).  Slots past a sequence's kv_len may hold anything. */
+typedef struct {
+  void* k_codes;
+  void* k_scales;
+  void* v_codes;
+  void* v_scales;
+  const int32_t* page_table;   /* DEVICE [batch, max_pages] */
+  int32_t num_pages, page_size, max_pages;
+  int32_t Hkv, d;
+  int32_t reserved;            /* set to 0 */
+} dsa_cache;
+
+/* Quantise the q_lens[b] newest tokens of each sequence into the cache: token i
+ * of sequence b goes to position kv_lens[b] - q_lens[b] + i.  k, v
+ * [total_q, Hkv, d] of dtype.  A block of 32 elements takes the smallest scale
+ * 2^(e-127), e in 1..254, for which every element is below 7 scales in
+ * magnitude, and each element the nearest code, ties to the even one: no
+ * element is off by more than half a step.  Magnitudes must stay below 2^127.
+ * pos (DEVICE [num_pages, page_size] int32, or NULL): the token's place in the
+ * text, seen_lens[b] - q_lens[b] + i, is written to its slot; seen_lens (HOST
+ * [batch], >= kv_lens, NULL = kv_lens) counts the tokens of the text so far,
+ * evicted ones included. */
+int dsa_cache_append(const dsa_cache* cache, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                     int32_t dtype, const int32_t* q_lens, const int32_t* kv_lens, int32_t batch,
+                     int32_t* pos, const int32_t* seen_lens, void* stream);
+
+/* Read the q_lens[b] newest tokens of each sequence back: k, v
+ * [total_q, Hkv, d] of dtype (exact in both types). */
+int dsa_cache_read(const dsa_cache* cache, void* k, int64_t k_stride, void* v, int64_t v_stride,
+                   int32_t dtype, const int32_t* q_lens, const int32_t* kv_lens, int32_t batch,
+                   void* stream);
+
+/* Attention over the cache, the call's own tokens included (append first).
+ *   idx  NULL: every visible key.  Else DEVICE [total_q, topk] int32, the keys
+ *        query row t reads (dsa_indexer_topk's out_idx): logical positions in
+ *        any order; entries that are negative or past the query are skipped, a
+ *        position listed twice counts twice.  topk = 0 without idx, else
+ *        1..2^20
+ *   out, lse as dsa_prompt_attention, of q_dtype; a row that sees no key gets
+ *        zeros and -inf
+ * bf16 queries: softmax weights are rounded to bf16 for their product with v.
+ * fp32 queries: fp32 products throughout. */
+size_t dsa_cache_workspace_size(int32_t batch, const int32_t* q_lens, const int32_t* kv_lens,
+                                int32_t Hq, int32_t Hkv, int32_t d, int32_t topk);
+int dsa_cache_attention(const dsa_cache* cache, const void* q, int64_t q_stride, int32_t q_dtype,
+                        const int32_t* q_lens, const int32_t* kv_lens, int32_t batch, int32_t Hq,
+                        const int32_t* idx, int32_t topk, float scale,
+                        void* out, float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Add up the attention weight each cached key received from the call's
+ * queries, over all query heads:
+ *   acc_out[slot] = old + sum exp(scale * q . k - lse)
+ * with the lse a dsa_cache_attention call without idx returned for these
+ * queries.  old is acc[slot] for keys before the call's own tokens, 0 for the
+ * call's own tokens and everywhere if acc is NULL.  acc, acc_out: DEVICE
+ * [num_pages, page_size] fp32, may be the same.  Every visible slot of a
+ * sequence with queries is written, no other.  A query whose lse is -inf adds
+ * nothing. */
+size_t dsa_weights_workspace_size(int32_t batch, const int32_t* q_lens, const int32_t* kv_lens,
+                                  int32_t Hq, int32_t Hkv, int32_t d);
+int dsa_cache_weights(const dsa_cache* cache, const void* q, int64_t q_stride, int32_t q_dtype, const float* lse,
+                      const int32_t* q_lens, const int32_t* kv_lens, int32_t batch, int32_t Hq, float scale,
+                      const float* acc, float* acc_out, void* workspace, size_t workspace_bytes, void* stream);
+
+/* A per-slot array of a paged cache, [num_pages, page_size] rows of row_bytes
+ * (the 4-bit codes and scales, the indexer's keys, acc, pos, ...). */
+typedef struct {
+  const void* src;
+  void* dst;            /* == src: the rows that change place are copied within it;
+                           else every kept row is copied to it */
+  int64_t row_bytes;
+} dsa_evict_array;
+
+/* Keep new_lens[b] of the kv_lens[b] keys of each sequence: those of largest
+ * acc, ties to the lower index, with the first `prefix` and the latest
+ * `window` tokens of the text always among them (min(prefix + window, kv_len)
+ * <= new_len).  pos [num_pages, page_size] gives each key's place in the text
+ * and seen_lens (HOST, >= kv_lens, NULL = kv_lens) the tokens of the text so
+ * far; without pos a key's place is its index.  Kept keys at indices below
+ * new_len stay; the n-th kept key behind them moves to the n-th freed index in
+ * front.  Keys are addressed by index through page_table; attention does not
+ * depend on their order.  out_src [batch, out_stride] int32: the index each
+ * key 0..new_len-1 came from, -1 behind.  arrays (HOST, up to 16) are moved
+ * accordingly; an array's dst may be its own src and otherwise overlaps
+ * nothing the call reads or writes.  Slots from new_len on keep what they
+ * held. */
+size_t dsa_evict_workspace_size(int32_t batch, const int32_t* kv_lens, const int32_t* new_lens);
+int dsa_cache_evict(const float* acc, const int32_t* pos, const int32_t* page_table,
+                    int32_t page_size, int32_t max_pages, int32_t num_pages,
+                    const int32_t* kv_lens, const int32_t* new_lens, const int32_t* seen_lens, int32_t batch,
+                    int32_t prefix, int32_t window, const dsa_evict_array* arrays, int32_t n_arrays,
+                    int32_t* out_src, int32_t out_stride, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Per-pass timing (tracing for benchmarks).  Between dosa_profile_begin()
  * and dosa_profile_end(), every kernel the calling thread enqueues through
  * this library is bracketed by two HIP events recorded on the kernel's own
@@ -266,7 +413,9 @@ int dosa_indexer_topk_noalloc(const void* q, int32_t q_dtype, const float* q_sca
  * entries written, or a negative status.  Off by default; profiling creates
  * HIP event objects (no device memory) and reuses them across sessions.
  * Pass names: prep, key_norms, score_seed, select_seed, plan, bound, compact,
- * score_survivor_tiles, score_survivor_lists, score_dense, select_final. */
+ * score_survivor_tiles, score_survivor_lists, score_dense, select_final,
+ * prompt_attention, cache_attention, attention_join, cache_append,
+ * cache_read, cache_weights, weights_join, evict_select, evict_move. */
 typedef struct {
   const char* name;   /* static string */
   int32_t launches;

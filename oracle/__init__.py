@@ -22,4 +22,5 @@ Modules:
     formats      -- fp8 E4M3FN / bf16 / fp32 decoders written from the format definitions
     indexer      -- dense scores and exact Top-K (the plain definition)
     certificate  -- the pruning certificate in float64
+    attention    -- causal attention, the 4-bit cache format, accumulated weights, eviction
 """

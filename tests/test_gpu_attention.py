@@ -1,0 +1,675 @@
+"""The attention entry points on the GPU against their float64 definitions."""
+import numpy as np
+import pytest
+import torch
+
+import exact_top_token_amd as E
+from attention_helpers import U, check_attention, filled_cache, rows, table, weight_err
+from oracle import attention as A
+
+pytestmark = pytest.mark.gpu
+
+
+def say(*a):
+    print("[gpu]", *a, flush=True)
+
+
+def host(t):
+    return t.float().cpu().numpy()
+
+
+def space(n):
+    """A workspace of exactly n bytes, full of NaN bytes."""
+    return torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda")
+
+
+# ----------------------------------------------------------------------------
+# prompt attention
+# ----------------------------------------------------------------------------
+def run_prompt(q, k, v, ql, kl, scale=None, want_lse=True):
+    out = torch.full((q.shape[0], q.shape[1], q.shape[2]), float("nan"), dtype=q.dtype, device="cuda")
+    lse = torch.full(q.shape[:2], float("nan"), device="cuda") if want_lse else None
+    ws = space(E.prompt_workspace_size(ql, kl, q.shape[1], k.shape[1], q.shape[2], q.dtype))
+    E.dsa_prompt_attention(q, k, v, ql, kl, out, lse, scale=scale, workspace=ws)
+    torch.cuda.synchronize()
+    return out, lse
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hq,hk,ql,kl", [
+    (1, 1, [1], [1]),
+    (4, 2, [0, 3, 0], [0, 3, 5]),
+    (8, 8, [15, 16, 17], [15, 16, 17]),
+    (6, 2, [33, 1, 64, 65], [33, 40, 64, 130]),
+    (16, 1, [2, 1, 5], [129, 63, 300]),
+    (5, 5, [128, 127], [128, 255]),
+    (12, 3, [1, 1, 1, 1], [1, 64, 65, 500]),
+])
+def test_prompt(dtype, d, hq, hk, ql, kl):
+    say("prompt", dtype, d, hq, hk, ql, kl)
+    rng = np.random.default_rng(hq * 100 + d)
+    q, k, v = (rows(rng, n, h, d, dtype) for n, h in ((sum(ql), hq), (sum(kl), hk), (sum(kl), hk)))
+    out, lse = run_prompt(q.cuda(), k.cuda(), v.cuda(), ql, kl)
+    ref = A.prompt(host(q), host(k), host(v), ql, kl, d ** -0.5)
+    check_attention(out, lse, ref, d, max(kl), dtype == "bf16")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_prompt_long_chunks(dtype):
+    """Few rows over many keys (ranges joined) next to many rows over few."""
+    rng = np.random.default_rng(5)
+    ql, kl = [2, 130, 1], [9000, 200, 4097]
+    q, k, v = (rows(rng, n, h, 128, dtype) for n, h in ((sum(ql), 4), (sum(kl), 2), (sum(kl), 2)))
+    say("prompt chunks", dtype)
+    out, lse = run_prompt(q.cuda(), k.cuda(), v.cuda(), ql, kl, scale=0.3)
+    check_attention(out, lse, A.prompt(host(q), host(k), host(v), ql, kl, 0.3), 128, max(kl), dtype == "bf16")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_prompt_strided_operands(dtype, d):
+    """q, k, v as slices of one fused projection; outputs next to guards."""
+    rng = np.random.default_rng(6)
+    hq, hk, ql = 6, 2, [70, 9, 150]
+    n = sum(ql)
+    fused = rows(rng, n, hq + 2 * hk + 1, d, dtype).cuda()
+    q, k, v = fused[:, :hq], fused[:, hq:hq + hk], fused[:, hq + hk:hq + 2 * hk]
+    say("prompt strided", dtype, d)
+    guard = torch.full((n + 2, hq, d), 7.0, dtype=q.dtype, device="cuda")
+    ws = space(E.prompt_workspace_size(ql, ql, hq, hk, d, q.dtype))
+    E.dsa_prompt_attention(q, k, v, ql, ql, guard[1:-1], None, workspace=ws)
+    torch.cuda.synchronize()
+    assert torch.all(guard[0] == 7) and torch.all(guard[-1] == 7)
+    check_attention(guard[1:-1], None, A.prompt(host(q), host(k), host(v), ql, ql, d ** -0.5), d, max(ql), dtype == "bf16")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_prompt_large_scores(dtype):
+    """Scores in the hundreds and equal maxima: the running maximum moves, weights underflow."""
+    rng = np.random.default_rng(7)
+    ql = [200, 96]
+    q, k, v = (rows(rng, sum(ql), h, 64, dtype) * f for h, f in ((4, 8), (2, 8), (2, 1)))
+    k[100:] = k[100]
+    k[:50] *= -1
+    say("prompt large scores", dtype)
+    out, lse = run_prompt(q.cuda(), k.cuda(), v.cuda(), ql, ql, scale=1.0)
+    check_attention(out, lse, A.prompt(host(q), host(k), host(v), ql, ql, 1.0), 64, 200, dtype == "bf16")
+
+
+def test_prompt_many_sequences():
+    """More sequences than one launch takes, some of them empty."""
+    rng = np.random.default_rng(8)
+    kl = [int(x) for x in rng.integers(0, 40, 150)]
+    ql = [int(rng.integers(0, k + 1)) for k in kl]
+    for dtype in ("f32", "bf16"):
+        q, k, v = (rows(rng, n, h, 64, dtype) for n, h in ((sum(ql), 4), (sum(kl), 2), (sum(kl), 2)))
+        say("prompt many", dtype)
+        out, lse = run_prompt(q.cuda(), k.cuda(), v.cuda(), ql, kl)
+        check_attention(out, lse, A.prompt(host(q), host(k), host(v), ql, kl, 0.125), 64, 40, dtype == "bf16")
+
+
+# ----------------------------------------------------------------------------
+# cache write and read-back
+# ----------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hk,page,ql,kl", [
+    (1, 16, [1], [1]),
+    (2, 64, [2, 0, 33], [2, 9, 100]),
+    (3, 48, [17, 50], [40, 50]),
+    (8, 128, [129, 1], [300, 7]),
+    (40, 16, [5], [20]),
+])
+def test_append_and_read(dtype, d, hk, page, ql, kl):
+    rng = np.random.default_rng(hk)
+    t, pages = table(rng, kl, page)
+    n = sum(ql)
+    x = {w: rows(rng, n, hk + 1, d, dtype, loud=True) * torch.exp(4 * torch.from_numpy(rng.normal(size=(n, 1, 1)))).to(torch.float32)
+         for w in "kv"}
+    x = {w: y.to(torch.bfloat16 if dtype == "bf16" else torch.float32) for w, y in x.items()}
+    x["k"][0, 0] = 0
+    c = E.Cache.empty(pages, page, hk, d, torch.from_numpy(t).cuda())
+    for b in (c.k_codes, c.k_scales, c.v_codes, c.v_scales):
+        b.fill_(0xA5)
+    pos = torch.full((pages, page), -9, dtype=torch.int32, device="cuda")
+    seen = [k + 1000 * (i + 1) for i, k in enumerate(kl)]
+    say("append", dtype, d, hk, page, ql, kl)
+    g = {w: y.cuda()[:, :hk] for w, y in x.items()}      # strided rows
+    E.dsa_cache_append(c, g["k"], g["v"], ql, kl, pos=pos, seen_lens=seen)
+    back = {w: torch.empty(n, hk, d, dtype=x[w].dtype, device="cuda") for w in "kv"}
+    E.dsa_cache_read(c, back["k"], back["v"], ql, kl)
+    wide = {w: torch.full((n, hk + 2, d), 5.0, device="cuda") for w in "kv"}
+    E.dsa_cache_read(c, wide["k"][:, 1:-1], wide["v"][:, 1:-1], ql, kl)
+    torch.cuda.synchronize()
+    at = np.concatenate([A.slots(t, b, kl[b], page, pages)[kl[b] - ql[b]:] for b in range(len(kl))])
+    for w in "kv":
+        codes, scales = A.mx_encode(host(x[w])[:, :hk])
+        want_c = np.full((pages * page, hk, d // 2), 0xA5, np.uint8)
+        want_s = np.full((pages * page, hk, d // 32), 0xA5, np.uint8)
+        want_c[at], want_s[at] = codes, scales
+        assert np.array_equal(getattr(c, w + "_codes").cpu().numpy().reshape(want_c.shape), want_c)
+        assert np.array_equal(getattr(c, w + "_scales").cpu().numpy().reshape(want_s.shape), want_s)
+        val = A.mx_decode(codes, scales)
+        assert np.array_equal(host(back[w]), val)
+        assert np.array_equal(host(wide[w])[:, 1:-1], val)
+        assert torch.all(wide[w][:, 0] == 5) and torch.all(wide[w][:, -1] == 5)
+    p = np.full(pages * page, -9)
+    p[at] = np.concatenate([np.arange(s - q, s) for s, q in zip(seen, ql)])
+    assert np.array_equal(pos.cpu().numpy().reshape(-1), p)
+
+
+def test_append_borders():
+    """Every border between two codes and its neighbours, at scales over the whole range."""
+    edges = np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 0.0], np.float32)
+    v = np.concatenate([edges, np.nextafter(edges, np.float32(9)), np.nextafter(edges, np.float32(-9))])
+    v = np.concatenate([v, -v])
+    blocks = []
+    for e in (-126, -120, -60, -1, 0, 5, 60, 120):
+        for i in range(0, len(v), 31):
+            blk = np.zeros(32, np.float32)
+            part = v[i:i + 31]
+            blk[:len(part)] = part
+            blk[31] = 4.0            # fixes the scale at 2^e
+            blocks.append(np.ldexp(blk, e).astype(np.float32))
+    for top in (7.0, np.nextafter(np.float32(7), np.float32(0)), 3.5, np.nextafter(np.float32(3.5), np.float32(0)), 1e-44, 1e-40):
+        blocks.append(np.array([top] + [0.0] * 31, np.float32))
+    while len(blocks) % 2:
+        blocks.append(np.zeros(32, np.float32))
+    x = np.stack(blocks).reshape(-1, 1, 64)
+    n = len(x)
+    t = torch.zeros(1, 1, dtype=torch.int32, device="cuda")
+    c = E.Cache.empty(1, -(-n // 16) * 16, 1, 64, t)
+    g = torch.from_numpy(x).cuda()
+    say("append borders")
+    E.dsa_cache_append(c, g, -g, [n], [n])
+    torch.cuda.synchronize()
+    for w, y in (("k", x), ("v", -x)):
+        codes, scales = A.mx_encode(y)
+        assert np.array_equal(getattr(c, w + "_scales").cpu().numpy().reshape(-1, 1, 2)[:n], scales)
+        got = getattr(c, w + "_codes").cpu().numpy().reshape(-1, 1, 32)[:n]
+        assert np.array_equal(A.mx_decode(got, scales), A.mx_decode(codes, scales))
+
+
+def test_append_pages_that_do_not_exist():
+    kl, ql, page = [70, 40], [70, 40], 16
+    rng = np.random.default_rng(3)
+    t, pages = table(rng, kl, page)
+    t[0, 2], t[1, 0] = -1, pages
+    c = E.Cache.empty(pages, page, 2, 64, torch.from_numpy(t).cuda())
+    for b in (c.k_codes, c.k_scales, c.v_codes, c.v_scales):
+        b.fill_(0x11)
+    x = rows(rng, 110, 2, 64, "bf16").cuda()
+    pos = torch.full((pages, page), -9, dtype=torch.int32, device="cuda")
+    say("append bad pages")
+    E.dsa_cache_append(c, x, x, ql, kl, pos=pos)
+    k, v = torch.full_like(x, 9.0), torch.full_like(x, 9.0)
+    E.dsa_cache_read(c, k, v, ql, kl)
+    torch.cuda.synchronize()
+    gone = np.concatenate([A.slots(t, b, kl[b], page, pages) < 0 for b in range(2)])
+    want = A.mx_decode(*A.mx_encode(host(x)))
+    want[gone] = 0
+    assert np.array_equal(host(k), want) and np.array_equal(host(v), want)
+    assert int((pos == -9).sum()) == pages * page - int((~gone).sum())
+
+
+# ----------------------------------------------------------------------------
+# attention over the cache
+# ----------------------------------------------------------------------------
+def run_cache(c, q, ql, kl, idx=None, scale=None):
+    out = torch.full(tuple(q.shape), float("nan"), dtype=q.dtype, device="cuda")
+    lse = torch.full(q.shape[:2], float("nan"), device="cuda")
+    ws = space(E.cache_workspace_size(ql, kl, q.shape[1], c.Hkv, c.d, 0 if idx is None else idx.shape[1]))
+    E.dsa_cache_attention(c, q, ql, kl, out, lse, idx=idx, scale=scale, workspace=ws)
+    torch.cuda.synchronize()
+    return out, lse
+
+
+CACHE_SHAPES = [
+    (1, 1, 16, [1], [1]),
+    (4, 2, 64, [1, 0, 2], [63, 5, 65]),
+    (16, 2, 64, [2, 2, 1], [130, 64, 700]),
+    (6, 3, 48, [3, 1], [200, 47]),
+    (40, 8, 128, [1, 4], [129, 256]),
+    (64, 1, 256, [1, 2], [300, 10]),
+    (8, 4, 16, [17, 40], [50, 40]),
+    (15, 5, 64, [9], [500]),
+]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hq,hk,page,ql,kl", CACHE_SHAPES)
+def test_cache_attention(dtype, d, hq, hk, page, ql, kl):
+    rng = np.random.default_rng(hq + page)
+    c, h = filled_cache(rng, kl, page, hk, d)
+    q = rows(rng, sum(ql), hq, d, dtype)
+    say("cache attention", dtype, d, hq, hk, page, ql, kl)
+    out, lse = run_cache(c, q.cuda(), ql, kl)
+    check_attention(out, lse, A.cache_attention(host(q), h, ql, kl, d ** -0.5), d, max(kl), dtype == "bf16")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("page", [64, 80])
+def test_cache_attention_long(dtype, page):
+    """Long caches: many joined key ranges."""
+    rng = np.random.default_rng(2)
+    ql, kl = [1, 2], [20011, 4097]
+    c, h = filled_cache(rng, kl, page, 2, 128)
+    q = rows(rng, 3, 6, 128, dtype)
+    say("cache attention long", dtype, page)
+    out, lse = run_cache(c, q.cuda(), ql, kl)
+    check_attention(out, lse, A.cache_attention(host(q), h, ql, kl, 128 ** -0.5), 128, max(kl), dtype == "bf16")
+
+
+@pytest.mark.parametrize("page", [16, 64])
+def test_cache_attention_pages_that_do_not_exist(page):
+    """Keys of a bad table entry are not seen; a row all of whose keys are gone is empty."""
+    rng = np.random.default_rng(4)
+    ql, kl = [2, 1, 3], [300, 60, 129]
+    c, h = filled_cache(rng, kl, page, 2, 64)
+    t = h["table"].copy()
+    t[0, 1], t[0, -1], t[1, :], t[2, 0] = -1, -5, 1 << 20, c.num_pages
+    h["table"] = t
+    c = E.Cache(c.k_codes, c.k_scales, c.v_codes, c.v_scales, torch.from_numpy(t).cuda())
+    for dtype in ("f32", "bf16"):
+        q = rows(rng, 6, 4, 64, dtype)
+        say("cache attention bad pages", page, dtype)
+        out, lse = run_cache(c, q.cuda(), ql, kl)
+        ref = A.cache_attention(host(q), h, ql, kl, 0.125)
+        assert np.all(~np.isfinite(ref[1][2])) and np.all(np.isfinite(ref[1][0]))
+        check_attention(out, lse, ref, 64, 300, dtype == "bf16")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hq,hk,page,topk,ql,kl", [
+    (4, 2, 64, 1, [1, 2], [30, 5]),
+    (16, 2, 64, 37, [2, 0, 3], [100, 9, 30]),
+    (8, 8, 16, 64, [1, 1], [65, 64]),
+    (40, 1, 48, 130, [2], [400]),
+    (6, 2, 64, 900, [3, 1], [1200, 40]),
+])
+def test_cache_attention_selected(dtype, d, hq, hk, page, topk, ql, kl):
+    rng = np.random.default_rng(topk)
+    c, h = filled_cache(rng, kl, page, hk, d)
+    q = rows(rng, sum(ql), hq, d, dtype)
+    idx = np.full((sum(ql), topk), -1, np.int32)
+    r = 0
+    for b in range(len(ql)):
+        for i in range(ql[b]):
+            see = kl[b] - ql[b] + i + 1
+            n = min(see, topk)
+            idx[r, :n] = rng.permutation(see)[:n]
+            idx[r] = idx[r][rng.permutation(topk)]        # -1 anywhere
+            r += 1
+    say("cache attention selected", dtype, d, hq, hk, page, topk, ql, kl)
+    out, lse = run_cache(c, q.cuda(), ql, kl, torch.from_numpy(idx).cuda())
+    check_attention(out, lse, A.cache_attention(host(q), h, ql, kl, d ** -0.5, idx), d, topk, dtype == "bf16")
+
+
+def test_cache_attention_selected_oddities():
+    """Entries past the query, far outside, repeated, and rows of nothing."""
+    rng = np.random.default_rng(9)
+    ql, kl = [3, 2], [90, 20]
+    c, h = filled_cache(rng, kl, 16, 2, 64)
+    h["table"][1, 1] = -3
+    c = E.Cache(c.k_codes, c.k_scales, c.v_codes, c.v_scales, torch.from_numpy(h["table"]).cuda())
+    idx = rng.integers(-5, 200, (5, 100)).astype(np.int32)
+    idx[0] = -1
+    idx[1, ::2], idx[1, 1::2] = 2 ** 31 - 1, -2 ** 31
+    idx[2] = 7
+    idx[3] = 17        # in the page that does not exist
+    for dtype in ("f32", "bf16"):
+        q = rows(rng, 5, 4, 64, dtype)
+        say("cache attention selected oddities", dtype)
+        out, lse = run_cache(c, q.cuda(), ql, kl, torch.from_numpy(idx).cuda())
+        ref = A.cache_attention(host(q), h, ql, kl, 0.125, idx)
+        assert np.all(~np.isfinite(ref[1][[0, 1, 3]]))
+        check_attention(out, lse, ref, 64, 100, dtype == "bf16")
+
+
+def test_cache_attention_many_sequences():
+    rng = np.random.default_rng(10)
+    kl = [int(x) for x in rng.integers(1, 90, 140)]
+    ql = [int(rng.integers(0, min(k, 3) + 1)) for k in kl]
+    c, h = filled_cache(rng, kl, 16, 2, 64)
+    q = rows(rng, sum(ql), 4, 64, "bf16")
+    say("cache attention many")
+    out, lse = run_cache(c, q.cuda(), ql, kl)
+    check_attention(out, lse, A.cache_attention(host(q), h, ql, kl, 0.125), 64, 90, True)
+
+
+# ----------------------------------------------------------------------------
+# accumulated weights
+# ----------------------------------------------------------------------------
+def check_weights(c, h, q, ql, kl, dtype, acc_mode):
+    rng = np.random.default_rng(1)
+    d, H = q.shape[2], q.shape[1]
+    ref = A.cache_attention(host(q), h, ql, kl, d ** -0.5)
+    lse = torch.from_numpy(ref[1].astype(np.float32)).cuda()
+    shape = (c.num_pages, c.page_size)
+    acc = None if acc_mode == "none" else torch.from_numpy(rng.random(shape).astype(np.float32)).cuda()
+    out = acc if acc_mode == "in place" else torch.full(shape, 3.0, device="cuda")
+    first = out.cpu().numpy().copy()
+    old = None if acc is None else acc.cpu().numpy().copy()
+    ws = space(E.weights_workspace_size(ql, kl, H, c.Hkv, d))
+    E.dsa_cache_weights(c, q.cuda(), lse, ql, kl, acc, out, workspace=ws)
+    torch.cuda.synchronize()
+    want = A.accumulate(h, ref[4], ql, kl, old, first)
+    # each weight off by its own error and lse's rounding; up to q_len * H of them summed
+    e = float((weight_err(ref[3], ref[1], d, 0) + 2 * U * np.abs(np.where(np.isfinite(ref[1]), ref[1], 0))).max())
+    n = max(ql) * H
+    got = out.cpu().numpy().astype(np.float64)
+    tol = (np.abs(want) + 1e-30) * (e + (n + 4) * U)
+    assert np.all(np.abs(got - want) <= tol), float((np.abs(got - want) - tol).max())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hq,hk,page,ql,kl", CACHE_SHAPES)
+def test_weights(dtype, d, hq, hk, page, ql, kl):
+    rng = np.random.default_rng(hq + page)
+    c, h = filled_cache(rng, kl, page, hk, d)
+    q = rows(rng, sum(ql), hq, d, dtype)
+    say("weights", dtype, d, hq, hk, page, ql, kl)
+    check_weights(c, h, q, ql, kl, dtype, {0: "none", 1: "in place", 2: "other"}[(hq + d // 64) % 3])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_weights_prompt(dtype):
+    """Whole prompts: many row tiles shared by several workgroups."""
+    rng = np.random.default_rng(11)
+    ql, kl = [300, 77], [300, 200]
+    c, h = filled_cache(rng, kl, 64, 2, 64)
+    q = rows(rng, sum(ql), 8, 64, dtype)
+    say("weights prompt", dtype)
+    check_weights(c, h, q, ql, kl, dtype, "other")
+
+
+def test_weights_bad_pages_and_empty_rows():
+    rng = np.random.default_rng(12)
+    ql, kl = [2, 1], [150, 30]
+    c, h = filled_cache(rng, kl, 64, 2, 64)
+    h["table"][0, 0], h["table"][1, 0] = -1, c.num_pages + 3
+    c = E.Cache(c.k_codes, c.k_scales, c.v_codes, c.v_scales, torch.from_numpy(h["table"]).cuda())
+    say("weights bad pages")
+    check_weights(c, h, rows(rng, 3, 4, 64, "bf16"), ql, kl, "bf16", "other")
+
+
+def test_weights_many_sequences():
+    rng = np.random.default_rng(13)
+    kl = [int(x) for x in rng.integers(1, 90, 140)]
+    ql = [int(rng.integers(0, min(k, 3) + 1)) for k in kl]
+    c, h = filled_cache(rng, kl, 16, 2, 64)
+    say("weights many")
+    check_weights(c, h, rows(rng, sum(ql), 4, 64, "bf16"), ql, kl, "bf16", "in place")
+
+
+# ----------------------------------------------------------------------------
+# eviction
+# ----------------------------------------------------------------------------
+def check_evict(kl, nl, page, prefix=0, window=0, moved=False, values="distinct", seed=0, stride=None):
+    rng = np.random.default_rng(seed)
+    t, pages = table(rng, kl, page)
+    acc = np.full((pages, page), 1e9, np.float32)
+    pos = np.zeros((pages, page), np.int32)
+    seen = [k + (50 * k if moved else 0) for k in kl]
+    at = [A.slots(t, b, n, page, pages) for b, n in enumerate(kl)]
+    for b, n in enumerate(kl):
+        a = {"distinct": rng.random(n), "ties": rng.integers(0, 3, n) / 4, "same": np.zeros(n),
+             "signs": rng.choice([0.0, -0.0, -1.5, 2.0, np.inf, -np.inf, 1e-42], n)}[values]
+        acc.reshape(-1)[at[b]] = a
+        pos.reshape(-1)[at[b]] = rng.permutation(seen[b])[:n] if moved else np.arange(n)
+    codes = rng.integers(0, 256, (pages, page, 3, 32)).astype(np.uint8)          # 96-byte rows
+    odd = rng.integers(0, 256, (pages, page, 7)).astype(np.uint8)
+    g = [torch.from_numpy(x.copy()).cuda() for x in (acc, pos, codes, odd)]
+    acc_o, odd_o = torch.full_like(g[0], -2.0), torch.full_like(g[3], 9)
+    width = max(nl, default=0) + (3 if stride is None else stride)
+    out = torch.full((len(kl), width), 77, dtype=torch.int32, device="cuda")
+    ws = space(E.evict_workspace_size(kl, nl))
+    say("evict", kl[:4], nl[:4], page, prefix, window, moved, values)
+    E.dsa_cache_evict(g[0], torch.from_numpy(t).cuda(), kl, nl,
+                      [(g[0], acc_o), (g[1], g[1]), (g[2], g[2]), (g[3], odd_o)], out,
+                      pos=g[1] if moved else None, seen_lens=seen if moved else None, prefix=prefix, window=window,
+                      workspace=ws)
+    torch.cuda.synchronize()
+    want_out = np.full((len(kl), width), -1)
+    acc_w, odd_w, pos_w, codes_w = np.full_like(acc, -2).reshape(-1), np.full_like(odd, 9).reshape(-1, 7), pos.copy().reshape(-1), codes.copy().reshape(-1, 3, 32)
+    for b, (n, k) in enumerate(zip(kl, nl)):
+        src = A.evict(acc.reshape(-1)[at[b]], n, k, prefix, window, pos.reshape(-1)[at[b]] if moved else None, seen[b])
+        want_out[b, :k] = src
+        to, frm = at[b][:k], at[b][src]
+        acc_w[to], odd_w[to] = acc.reshape(-1)[frm], odd.reshape(-1, 7)[frm]
+        pos_w[to], codes_w[to] = pos.reshape(-1)[frm], codes.reshape(-1, 3, 32)[frm]
+    assert np.array_equal(out.cpu().numpy(), want_out)
+    assert np.array_equal(acc_o.cpu().numpy().reshape(-1), acc_w)
+    assert np.array_equal(odd_o.cpu().numpy().reshape(-1, 7), odd_w)
+    assert np.array_equal(g[1].cpu().numpy().reshape(-1), pos_w)
+    assert np.array_equal(g[2].cpu().numpy().reshape(-1, 3, 32), codes_w)
+    assert np.array_equal(g[0].cpu().numpy(), acc)
+
+
+@pytest.mark.parametrize("kl,nl,page,kw", [
+    ([1], [0], 16, {}),
+    ([1], [1], 16, {}),
+    ([0, 5, 5], [0, 5, 0], 16, {}),
+    ([100], [60], 16, dict(prefix=4, window=16)),
+    ([1000, 1025, 64], [999, 513, 1], 64, {}),
+    ([3000, 70], [300, 69], 48, dict(prefix=4, window=20, moved=True)),
+    ([2048], [1024], 64, dict(values="ties")),
+    ([1500], [700], 64, dict(values="same")),
+    ([900], [450], 64, dict(values="signs")),
+    ([900], [450], 64, dict(values="signs", prefix=3, window=9, moved=True)),
+    ([9000], [4500], 64, dict(values="ties", prefix=1, window=100, moved=True)),
+    ([70000], [4096], 128, dict(prefix=4, window=64)),
+    ([66000], [65990], 128, dict(values="ties")),
+    ([40], [30], 16, dict(prefix=30, window=0)),
+    ([20, 40], [20, 30], 16, dict(prefix=15, window=15)),
+])
+def test_evict(kl, nl, page, kw):
+    check_evict(kl, nl, page, **kw)
+
+
+def test_evict_many_sequences():
+    rng = np.random.default_rng(14)
+    kl = [int(x) for x in rng.integers(0, 300, 150)]
+    nl = [int(rng.integers(0, k + 1)) for k in kl]
+    check_evict(kl, nl, 16)
+
+
+def test_evict_very_long():
+    check_evict([300000, 5], [123457, 5], 64, prefix=4, window=1000)
+
+
+# ----------------------------------------------------------------------------
+# together, as a server uses them
+# ----------------------------------------------------------------------------
+def test_serving_run():
+    """Prompt attention and the prompt's weights, decode steps over the growing cache, the indexer's
+    selection read by the attention, eviction, and decoding on over the smaller cache."""
+    from exact_top_token_amd.runner import Runner, to_device
+    import synth
+
+    rng = np.random.default_rng(20)
+    hq, hk, d, page, kl = 8, 2, 64, 16, [150, 83]
+    per = [-(-(k + 40) // page) for k in kl]
+    t = np.full((2, max(per)), -1, np.int32)
+    perm = rng.permutation(sum(per))
+    t[0, :per[0]], t[1, :per[1]] = perm[:per[0]], perm[per[0]:]
+    c = E.Cache.empty(sum(per), page, hk, d, torch.from_numpy(t).cuda())
+    shape = (c.num_pages, page)
+    acc, pos = torch.zeros(shape, device="cuda"), torch.zeros(shape, dtype=torch.int32, device="cuda")
+    copy = lambda: dict(k_codes=c.k_codes.cpu().numpy(), k_scales=c.k_scales.cpu().numpy(),
+                        v_codes=c.v_codes.cpu().numpy(), v_scales=c.v_scales.cpu().numpy(), table=t)
+
+    def step(ql, kl, seen, idx=None):
+        nq = sum(ql)
+        q, k, v = rows(rng, nq, hq, d, "bf16").cuda(), rows(rng, nq, hk, d, "bf16", True).cuda(), rows(rng, nq, hk, d, "bf16").cuda()
+        E.dsa_cache_append(c, k, v, ql, kl, pos=pos, seen_lens=seen)
+        out, lse = run_cache(c, q, ql, kl)
+        ref = A.cache_attention(host(q), copy(), ql, kl, d ** -0.5)
+        check_attention(out, lse, ref, d, max(kl), True)
+        before = acc.cpu().numpy()
+        ws = space(E.weights_workspace_size(ql, kl, hq, hk, d))
+        E.dsa_cache_weights(c, q, lse, ql, kl, acc, acc, workspace=ws)
+        want = A.accumulate(copy(), ref[4], ql, kl, before, before)
+        e = float(weight_err(ref[3], ref[1], d, max(kl)).max()) * 3
+        assert np.all(np.abs(acc.cpu().numpy() - want) <= (np.abs(want) + 1e-30) * (e + max(ql) * hq * U * 2))
+        return q, k, v
+
+    say("serving: prompt")
+    q, k, v = step(kl, kl, kl)
+    out, lse = run_prompt(q, k, v, kl, kl)
+    check_attention(out, lse, A.prompt(host(q), host(k), host(v), kl, kl, d ** -0.5), d, max(kl), True)
+    seen = list(kl)
+    for i in range(3):
+        say("serving: decode", i)
+        kl, seen = [k + 2 for k in kl], [s + 2 for s in seen]
+        step([2, 2], kl, seen)
+    # the indexer's choice, read by the attention
+    wl = synth.custom(0, [(2, kl[0]), (2, kl[1])], H=8, d=64, topk=32, q_dtype="bf16", k_dtype="bf16")
+    idx, _ = Runner(to_device(wl), "dosa")()
+    q = rows(rng, 4, hq, d, "bf16").cuda()
+    say("serving: selected")
+    out, lse = run_cache(c, q, [2, 2], kl, idx)
+    check_attention(out, lse, A.cache_attention(host(q), copy(), [2, 2], kl, d ** -0.5, idx.cpu().numpy()), d, 32, True)
+    for new in ([96, 64], [80, 50]):
+        say("serving: evict", new)
+        src = torch.empty(2, 96, dtype=torch.int32, device="cuda")
+        old, oldp, was = acc.cpu().numpy().reshape(-1), pos.cpu().numpy().reshape(-1), copy()
+        E.dsa_cache_evict(acc, c.page_table, kl, new, c.arrays() + [(acc, acc), (pos, pos)], src, pos=pos, seen_lens=seen,
+                          prefix=4, window=16, workspace=space(E.evict_workspace_size(kl, new)))
+        torch.cuda.synchronize()
+        for b in range(2):
+            at = A.slots(t, b, kl[b], page, c.num_pages)
+            want = A.evict(old[at], kl[b], new[b], 4, 16, oldp[at], seen[b])
+            assert np.array_equal(src.cpu().numpy()[b, :new[b]], want)
+            for name in ("k_codes", "k_scales", "v_codes", "v_scales"):
+                now = getattr(c, name).cpu().numpy()
+                assert np.array_equal(now.reshape(-1, *now.shape[2:])[at[:new[b]]],
+                                      was[name].reshape(-1, *now.shape[2:])[at[want]])
+            assert np.array_equal(acc.cpu().numpy().reshape(-1)[at[:new[b]]], old[at[want]])
+            assert np.array_equal(pos.cpu().numpy().reshape(-1)[at[:new[b]]], oldp[at[want]])
+        kl = list(new)
+        kl, seen = [k + 1 for k in kl], [s + 1 for s in seen]
+        step([1, 1], kl, seen)
+
+
+def test_captured_and_replayed():
+    """A decode step captured into a graph and replayed, with eager work on other workspaces between the
+    replays; a second graph shares the workspace."""
+    rng = np.random.default_rng(21)
+    ql, kl, hq, hk, d = [1, 2], [5000, 300], 8, 2, 128
+    c, h = filled_cache(rng, kl, 64, hk, d)
+    shape = (c.num_pages, c.page_size)
+    need = max(E.cache_workspace_size(ql, kl, hq, hk, d), E.weights_workspace_size(ql, kl, hq, hk, d),
+               E.evict_workspace_size(kl, [4000, 200]))
+    ws = space(need)
+    graphs = []
+    say("capture")
+    for _ in range(2):
+        b = dict(q=torch.zeros(3, hq, d, dtype=torch.bfloat16, device="cuda"), k=torch.zeros(3, hk, d, dtype=torch.bfloat16, device="cuda"),
+                 out=torch.zeros(3, hq, d, dtype=torch.bfloat16, device="cuda"), lse=torch.zeros(3, hq, device="cuda"),
+                 acc=torch.zeros(shape, device="cuda"), acc2=torch.zeros(shape, device="cuda"),
+                 src=torch.zeros(2, 4000, dtype=torch.int32, device="cuda"))
+        g = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(g):
+            E.dsa_cache_append(c, b["k"], b["k"], ql, kl)
+            E.dsa_cache_attention(c, b["q"], ql, kl, b["out"], b["lse"], workspace=ws)
+            E.dsa_cache_weights(c, b["q"], b["lse"], ql, kl, b["acc"], b["acc"], workspace=ws)
+            E.dsa_cache_evict(b["acc"], c.page_table, kl, [4000, 200], [(b["acc"], b["acc2"])], b["src"], prefix=4, window=8, workspace=ws)
+        graphs.append((g, b))
+    ws2 = space(need)
+    for rep in range(3):
+        for g, b in graphs:
+            say("replay", rep)
+            b["q"].copy_(rows(rng, 3, hq, d, "bf16"))
+            b["k"].copy_(rows(rng, 3, hk, d, "bf16"))
+            acc0 = b["acc"].clone()
+            g.replay()
+            torch.cuda.synchronize()
+            got = {n: b[n].clone() for n in ("out", "lse", "acc", "acc2", "src")}
+            e = {n: torch.zeros_like(x) for n, x in got.items()}
+            E.dsa_cache_append(c, b["k"], b["k"], ql, kl)
+            E.dsa_cache_attention(c, b["q"], ql, kl, e["out"], e["lse"], workspace=ws2)
+            e["acc"].copy_(acc0)
+            E.dsa_cache_weights(c, b["q"], e["lse"], ql, kl, e["acc"], e["acc"], workspace=ws2)
+            E.dsa_cache_evict(e["acc"], c.page_table, kl, [4000, 200], [(e["acc"], e["acc2"])], e["src"], prefix=4, window=8, workspace=ws2)
+            torch.cuda.synchronize()
+            for n in ("out", "lse", "acc", "src"):
+                assert torch.equal(got[n], e[n]), n
+            at = torch.from_numpy(np.concatenate([A.slots(h["table"], i, n, 64, c.num_pages) for i, n in enumerate([4000, 200])])).cuda()
+            assert torch.equal(got["acc2"].view(-1)[at], e["acc2"].view(-1)[at])
+
+
+def test_captured_prompt():
+    rng = np.random.default_rng(22)
+    ql, kl = [200, 3], [200, 2000]
+    for dtype in ("bf16", "f32"):
+        q, k, v = (rows(rng, n, h, 64, dtype).cuda() for n, h in ((203, 4), (2200, 2), (2200, 2)))
+        out, lse = torch.zeros_like(q), torch.zeros(203, 4, device="cuda")
+        ws = space(E.prompt_workspace_size(ql, kl, 4, 2, 64, q.dtype))
+        say("capture prompt", dtype)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            E.dsa_prompt_attention(q, k, v, ql, kl, out, lse, workspace=ws)
+        for _ in range(3):
+            q.copy_(rows(rng, 203, 4, 64, dtype))
+            g.replay()
+            torch.cuda.synchronize()
+            o2, l2 = run_prompt(q, k, v, ql, kl)
+            assert torch.equal(out, o2) and torch.equal(lse, l2)
+
+
+def test_two_streams_at_once():
+    """Two calls in flight on two streams with a workspace each."""
+    rng = np.random.default_rng(23)
+    ql, kl = [1, 1], [9000, 7000]
+    c, h = filled_cache(rng, kl, 64, 2, 128)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    qs = [rows(rng, 2, 8, 128, "bf16").cuda() for _ in range(2)]
+    want = [run_cache(c, q, ql, kl) for q in qs]
+    got = [(torch.zeros_like(q), torch.zeros(2, 8, device="cuda")) for q in qs]
+    wss = [space(E.cache_workspace_size(ql, kl, 8, 2, 128)) for _ in qs]
+    torch.cuda.synchronize()
+    say("two streams")
+    for _ in range(20):
+        for s, q, (o, l), ws in zip(streams, qs, got, wss):
+            E.dsa_cache_attention(c, q, ql, kl, o, l, workspace=ws, stream=s)
+    torch.cuda.synchronize()
+    for (o, l), (o2, l2) in zip(got, want):
+        assert torch.equal(o, o2) and torch.equal(l, l2)
+
+
+def test_repeated_calls_agree():
+    rng = np.random.default_rng(24)
+    ql, kl = [1, 3], [3000, 900]
+    c, h = filled_cache(rng, kl, 64, 4, 64)
+    q = rows(rng, 4, 8, 64, "bf16").cuda()
+    first = run_cache(c, q, ql, kl)
+    acc = torch.zeros(c.num_pages, c.page_size, device="cuda")
+    ws = space(E.weights_workspace_size(ql, kl, 8, 4, 64))
+    E.dsa_cache_weights(c, q, first[1], ql, kl, None, acc, workspace=ws)
+    say("repeat")
+    for _ in range(5):
+        again = run_cache(c, q, ql, kl)
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+        acc2 = torch.zeros_like(acc)
+        E.dsa_cache_weights(c, q, first[1], ql, kl, None, acc2, workspace=ws)
+        assert torch.equal(acc, acc2)
+
+
+def test_pass_times_are_reported():
+    """The per-pass profile names the new passes."""
+    rng = np.random.default_rng(25)
+    ql, kl = [1], [3000]
+    c, h = filled_cache(rng, kl, 64, 2, 64)
+    q = rows(rng, 1, 4, 64, "bf16").cuda()
+    run_cache(c, q, ql, kl)
+    E.profile_begin()
+    run_cache(c, q, ql, kl)
+    t = E.profile_end()
+    assert t["cache_attention"][0] == 1 and t["attention_join"][0] == 1
