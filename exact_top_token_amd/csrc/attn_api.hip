@@ -110,9 +110,19 @@ struct AttnChunk {
   int64_t parts = 0;
 };
 
-// Sequences b0.. of the batch, at most kAttnSeqs with queries; returns the
-// sequence after the last one taken, or -1 if the launch would be too large.
-int plan_attn(AttnChunk& ch, int src, int b0, int32_t batch, const int32_t* q_lens, const int32_t* kv_lens,
+// Which kernel takes a sequence: bf16 prompts whose rows (queries times group
+// heads) fill more than two wavefronts of the tiled kernel go to it, its tiles
+// being shared by 256 rows; all else to the wavefront kernel.
+constexpr int64_t kTiledRows = 64;
+constexpr int64_t kTiledUnits = 512;     // workgroups of a launch of the tiled kernel: two a CU
+constexpr int64_t kTiledMinKeys = 512;
+
+bool takes_tiled(int src, int64_t rows) { return src == A_BF16 && rows > kTiledRows; }
+
+// Sequences b0.. of the batch that the kernel takes, at most kAttnSeqs with
+// queries; returns the sequence after the last one seen, or -1 if the launch
+// would be too large.
+int plan_attn(AttnChunk& ch, int src, bool tiled, int b0, int32_t batch, const int32_t* q_lens, const int32_t* kv_lens,
               int32_t Hq, int32_t Hkv, int32_t topk, int64_t* q_row, int64_t* k_row) {
   AttnArgs& a = ch.a;
   const bool sel = topk > 0;
@@ -124,7 +134,7 @@ int plan_attn(AttnChunk& ch, int src, int b0, int32_t batch, const int32_t* q_le
   int b = b0;
   int64_t most = 0;
   for (; b < batch && a.n_seq < kAttnSeqs; ++b) {
-    if (q_lens[b] > 0) {
+    if (q_lens[b] > 0 && takes_tiled(src, (int64_t)q_lens[b] * a.group) == tiled) {
       AttnSeq& s = a.s[a.n_seq++];
       s = AttnSeq{};
       s.q_row0 = (int32_t)*q_row;
@@ -137,7 +147,7 @@ int plan_attn(AttnChunk& ch, int src, int b0, int32_t batch, const int32_t* q_le
     *q_row += q_lens[b];
     *k_row += kv_lens[b];
   }
-  a.rt = most > 16 ? attn_max_rt(src) : 1;
+  a.rt = tiled ? 2 * kPromptWaves : (most > 16 ? attn_max_rt(src) : 1);
   const int64_t tile = 16 * a.rt;
   auto tiles = [&](const AttnSeq& s) -> int64_t {
     return sel ? (int64_t)s.q_len * ((a.group + tile - 1) / tile) : ((int64_t)s.q_len * a.group + tile - 1) / tile;
@@ -146,7 +156,8 @@ int plan_attn(AttnChunk& ch, int src, int b0, int32_t batch, const int32_t* q_le
   std::stable_sort(a.s, a.s + a.n_seq, [&](const AttnSeq& x, const AttnSeq& y) { return keys(x) > keys(y); });
   int64_t work = 0;
   for (int i = 0; i < a.n_seq; ++i) work += tiles(a.s[i]) * Hkv * keys(a.s[i]);
-  const int64_t len = std::max(kMinKeys, (work + kTargetUnits - 1) / kTargetUnits);
+  const int64_t target = tiled ? kTiledUnits : kTargetUnits;
+  const int64_t len = std::max(tiled ? kTiledMinKeys : kMinKeys, (work + target - 1) / target);
   int64_t units = 0, join = 0, parts = 0;
   for (int i = 0; i < a.n_seq; ++i) {
     AttnSeq& s = a.s[i];
@@ -184,12 +195,14 @@ size_t part_bytes(const AttnChunk& ch, int d) {
 size_t attn_workspace(int src, int32_t batch, const int32_t* q_lens, const int32_t* kv_lens, int32_t Hq, int32_t Hkv,
                       int32_t d, int32_t topk) {
   size_t most = 256;
-  int64_t qr = 0, kr = 0;
-  for (int b = 0; b < batch;) {
-    AttnChunk ch;
-    b = plan_attn(ch, src, b, batch, q_lens, kv_lens, Hq, Hkv, topk, &qr, &kr);
-    if (b < 0) return 0;
-    most = std::max(most, part_bytes(ch, d));
+  for (int tiled = 0; tiled < (src == A_BF16 ? 2 : 1); ++tiled) {
+    int64_t qr = 0, kr = 0;
+    for (int b = 0; b < batch;) {
+      AttnChunk ch;
+      b = plan_attn(ch, src, tiled != 0, b, batch, q_lens, kv_lens, Hq, Hkv, topk, &qr, &kr);
+      if (b < 0) return 0;
+      most = std::max(most, part_bytes(ch, d));
+    }
   }
   return most;
 }
@@ -200,26 +213,28 @@ int run_attn(int src, AttnArgs base, int32_t batch, const int32_t* q_lens, const
   if (need == 0) return fail(DOSA_ERR_UNSUPPORTED, "too many row tiles and key ranges for one launch");
   if (workspace == nullptr || workspace_bytes < need || !aligned(workspace, 16))
     return fail(DOSA_ERR_WORKSPACE, "workspace needs " + std::to_string(need) + " bytes, 16-byte aligned");
-  int64_t qr = 0, kr = 0;
-  for (int b = 0; b < batch;) {
-    AttnChunk ch;
-    ch.a = base;
-    b = plan_attn(ch, src, b, batch, q_lens, kv_lens, base.Hq, base.Hkv, base.topk, &qr, &kr);
-    AttnArgs& a = ch.a;
-    const size_t rows = (size_t)ch.parts * 16 * a.rt;
-    a.part_o = static_cast<float*>(workspace);
-    a.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + up256(rows * d * sizeof(float)));
-    hipError_t e;
-    {
-      PassScope ps(src == A_F32 || src == A_BF16 ? P_PROMPT : P_ATTEND, stream);
-      e = launch_attn(src, d, a, stream);
+  for (int tiled = src == A_BF16 ? 1 : 0; tiled >= 0; --tiled) {
+    int64_t qr = 0, kr = 0;
+    for (int b = 0; b < batch;) {
+      AttnChunk ch;
+      ch.a = base;
+      b = plan_attn(ch, src, tiled != 0, b, batch, q_lens, kv_lens, base.Hq, base.Hkv, base.topk, &qr, &kr);
+      AttnArgs& a = ch.a;
+      const size_t rows = (size_t)ch.parts * 16 * a.rt;
+      a.part_o = static_cast<float*>(workspace);
+      a.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + up256(rows * d * sizeof(float)));
+      hipError_t e;
+      if (a.n_units > 0) {
+        PassScope ps(src == A_F32 || src == A_BF16 ? P_PROMPT : P_ATTEND, stream);
+        e = tiled ? launch_prompt(d, a, stream) : launch_attn(src, d, a, stream);
+        if (e != hipSuccess) return fail_hip(e, "attention kernel launch");
+      }
+      if (a.n_join > 0) {
+        PassScope ps(P_ATTEND_JOIN, stream);
+        e = launch_attn_join(src, d, a, stream);
+        if (e != hipSuccess) return fail_hip(e, "attention join launch");
+      }
     }
-    if (e != hipSuccess) return fail_hip(e, "attention kernel launch");
-    {
-      PassScope ps(P_ATTEND_JOIN, stream);
-      e = launch_attn_join(src, d, a, stream);
-    }
-    if (e != hipSuccess) return fail_hip(e, "attention join launch");
   }
   return DOSA_OK;
 }

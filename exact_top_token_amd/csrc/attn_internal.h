@@ -56,6 +56,11 @@ struct AttnArgs {
 // 16-row tiles one wavefront may hold (chosen by the host from the row count).
 inline int attn_max_rt(int src) { return src == A_MX32 ? 1 : 2; }
 
+// Bf16 prompts over LDS tiles: units are row tiles of kPromptWaves * 32 rows of
+// one kv head, over all their keys.
+constexpr int kPromptWaves = 8;
+hipError_t launch_prompt(int d, const AttnArgs& p, hipStream_t s);
+
 hipError_t launch_attn(int src, int d, const AttnArgs& p, hipStream_t s);
 hipError_t launch_attn_join(int src, int d, const AttnArgs& p, hipStream_t s);
 

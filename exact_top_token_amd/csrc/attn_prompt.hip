@@ -1,0 +1,246 @@
+// Causal attention of bf16 prompts: workgroups of kWaves wavefronts, 32 query
+// rows each, over tiles of 64 keys in LDS.
+//
+//   s_j = q . k_j,  m = max_j s_j,  p_j = 2^((s_j - m) c),  c = scale log2(e),
+//   o = sum_j p_j v_j / sum_j p_j,  lse = scale m + ln sum_j p_j.
+//
+// Rows are the (query, group head) pairs of a kv head, so the heads of a group
+// share the tiles.  Scores are computed transposed, S^T = K Q^T, with the
+// 32x32x16 product: lane l then holds row l%32 and keys 8i + 4(l/32)..+3, and
+// numbering the reduction slots of O^T = V^T P^T the same way makes its right
+// operand without moving a value between lanes.  A row's statistics are one
+// number a lane (its other half in lane l^32).  V^T comes out of row-major
+// LDS tiles through the transposing LDS read.
+//
+// Tiles go from global memory to LDS without passing registers, one tile
+// ahead.  A lane writes LDS at its own place in the wavefront's kilobyte, so
+// the swizzle that spreads rows over the banks is applied to the address it
+// reads from.
+//
+// The running maximum is only moved when a score exceeds it by more than 8 in
+// the exponent: weights then reach 2^8 and sums 2^8 n, both far inside fp32,
+// and most tiles skip the rescaling of the outputs.  Weights are rounded to
+// bf16 for the second product; their sum is taken before the rounding.
+#include "attn_device.h"
+
+namespace dosa {
+
+namespace {
+
+typedef float f16v __attribute__((ext_vector_type(16)));
+typedef short s4v __attribute__((ext_vector_type(4)));
+
+constexpr int kKeys = 64;      // keys of a tile
+constexpr float kSlack = 8.f;  // exponent by which a score may exceed the running maximum
+
+__device__ __forceinline__ f16v mfma32(b8 a, b8 b, f16v c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+
+// 16-byte chunk of row `r` that holds logical chunk c.  Key tiles: 16 lanes
+// read one chunk of 16 rows; value tiles: 16 lanes read 32 bytes of 4 rows.
+template <int D>
+__device__ __forceinline__ int k_chunk(int r, int c) {
+  return D == 128 ? c ^ (r & 15) : c ^ ((r >> 1) & 7);
+}
+template <int D>
+__device__ __forceinline__ int v_chunk(int r, int c) {
+  return D == 128 ? c ^ ((r & 3) << 2) : c ^ (((r >> 1) & 1) << 2);
+}
+
+template <int D, int NW>
+__global__ __launch_bounds__(64 * NW, 2) void prompt_kernel(const AttnArgs p) {
+  constexpr int CH = D / 8;              // 16-byte chunks of a row
+  constexpr int TILE = kKeys * D * 2;    // bytes of a tile
+  constexpr int NS = D / 16, NT = D / 32;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[2][2][TILE];   // [buffer][k, v]
+
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = lane64(), n = lane & 31, h = lane >> 5;
+  const int unit = blockIdx.x;
+  const AttnSeq& sq = p.s[find_seq(p.s, p.n_seq, unit, [](const AttnSeq& s) { return s.unit0; })];
+  int u = unit - sq.unit0;
+  const int head = u % p.Hkv;
+  u /= p.Hkv;
+  const int split = u % sq.n_split, rt = sq.n_rt - 1 - u / sq.n_split;   // last row tile first: it sees the most keys
+  const int n_rows = sq.q_len * p.group;
+  const int wg_row = rt * (32 * NW), row0 = wg_row + 32 * wave;
+  const int before = sq.kv_len - sq.q_len;
+  int r = row0 + n;
+  const bool ok = r < n_rows;
+  r = ok ? r : n_rows - 1;
+  const int query = r / p.group, qh = head * p.group + (r - query * p.group);
+  const int vis = before + query + 1;
+  auto seen = [&](int row) { return before + (row < n_rows ? row : n_rows - 1) / p.group + 1; };
+  const int key_lo = split * sq.split_len;
+  int wg_end = seen(wg_row + 32 * NW - 1);
+  wg_end = (int64_t)key_lo + sq.split_len < wg_end ? key_lo + sq.split_len : wg_end;
+  const int first = __builtin_amdgcn_readfirstlane(seen(row0)), last = __builtin_amdgcn_readfirstlane(seen(row0 + 31));
+  const bool active = row0 < n_rows;
+
+  b8 qf[NS];
+  {
+    const i4* src = reinterpret_cast<const i4*>(static_cast<const uint16_t*>(p.q) + (int64_t)(sq.q_row0 + query) * p.q_stride +
+                                                (int64_t)qh * D + 8 * h);
+#pragma unroll
+    for (int s = 0; s < NS; ++s) qf[s] = __builtin_bit_cast(b8, src[2 * s]);
+  }
+  f16v o[NT];
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) o[j][e] = 0.f;
+  float m = -INFINITY, l = 0.f;
+  const float c = p.scale * kLog2e;
+
+  const uint16_t* kg = static_cast<const uint16_t*>(p.k) + sq.key_base * p.k_stride + head * D;
+  const uint16_t* vg = static_cast<const uint16_t*>(p.v) + sq.key_base * p.v_stride + head * D;
+  // a wavefront instruction fills 1 KB: 64 / CH rows
+  constexpr int RPI = 64 / CH, PER = kKeys / RPI / NW;
+  const int lr = lane / CH, lc = lane % CH;
+  auto fetch = [&](int buf, int key0) {
+    // rows past the last visible one repeat it; their scores are masked
+    const int lim = wg_end - 1 - key0;
+    const uint16_t* k0 = kg + (int64_t)key0 * p.k_stride;
+    const uint16_t* v0 = vg + (int64_t)key0 * p.v_stride;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int at = (wave * PER + i) * RPI;
+      const int row = at + lr, src = row < lim ? row : lim;
+      __builtin_amdgcn_global_load_lds(
+          (const __attribute__((address_space(1))) void*)(k0 + src * (int)p.k_stride + 8 * k_chunk<D>(row, lc)),
+          (__attribute__((address_space(3))) void*)(&lds[buf][0][at * D * 2]), 16, 0, 0);
+      __builtin_amdgcn_global_load_lds(
+          (const __attribute__((address_space(1))) void*)(v0 + src * (int)p.v_stride + 8 * v_chunk<D>(row, lc)),
+          (__attribute__((address_space(3))) void*)(&lds[buf][1][at * D * 2]), 16, 0, 0);
+    }
+  };
+
+  auto compute = [&](int buf, int key0) {
+    const uint8_t* kt = lds[buf][0];
+    const uint8_t* vt = lds[buf][1];
+    f16v sc[2];
+#pragma unroll
+    for (int a = 0; a < 2; ++a) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) sc[a][e] = 0.f;
+      const int row = 32 * a + n;
+#pragma unroll
+      for (int s = 0; s < NS; ++s) {
+        const b8 kf = *reinterpret_cast<const b8*>(kt + row * (D * 2) + 16 * k_chunk<D>(row, 2 * s + h));
+        sc[a] = mfma32(kf, qf[s], sc[a]);
+      }
+    }
+    if (key0 + kKeys > first || key0 + kKeys > wg_end) {
+      const int end = vis < wg_end ? vis : wg_end;
+#pragma unroll
+      for (int a = 0; a < 2; ++a)
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          sc[a][e] = key0 + 32 * a + 8 * (e >> 2) + 4 * h + (e & 3) >= end ? -INFINITY : sc[a][e];
+    }
+    float top = sc[0][0];
+#pragma unroll
+    for (int a = 0; a < 2; ++a)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) top = fmaxf(top, sc[a][e]);
+    {
+      const uint32_t w = __float_as_uint(top);
+      auto x = __builtin_amdgcn_permlane32_swap(w, w, false, false);
+      top = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
+    }
+    if (__any((top - m) * c > kSlack)) {     // (-inf) - (-inf) compares false
+      const float mn = fmaxf(m, top);
+      const float f = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((m - mn) * c);
+      m = mn;
+      l *= f;
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[j][e] *= f;
+    }
+    const float mc = m == -INFINITY ? 0.f : m * c;
+    b8 pf[4];
+#pragma unroll
+    for (int a = 0; a < 2; ++a)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const float x = __builtin_amdgcn_exp2f(fmaf(sc[a][e], c, -mc));
+        l += x;
+        pf[2 * a + (e >> 3)][e & 7] = (__bf16)x;
+      }
+    // value operand: lane supplies 8 bytes of one of 4 rows, gets one column of them
+    const int i16 = lane & 15, vr = 4 * h + (i16 >> 2), vc = 16 * ((lane >> 4) & 1) + 4 * (i16 & 3);
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        s4v x[2];
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const int row = 16 * s + 8 * y + vr, col = 32 * j + vc;
+          x[y] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+              (__attribute__((address_space(3))) s4v*)(vt + row * (D * 2) + 16 * v_chunk<D>(row, col >> 3) + (col & 7) * 2));
+        }
+        const b8 vf = __builtin_bit_cast(b8, __builtin_shufflevector(x[0], x[1], 0, 1, 2, 3, 4, 5, 6, 7));
+        o[j] = mfma32(vf, pf[s], o[j]);
+      }
+  };
+
+  if (key_lo < wg_end) fetch(0, key_lo);
+  int buf = 0;
+  for (int key0 = key_lo; key0 < wg_end; key0 += kKeys) {
+    __builtin_amdgcn_s_waitcnt(0x0f70);      // this wavefront's part of the tile is in LDS
+    __syncthreads();
+    if (key0 + kKeys < wg_end) fetch(buf ^ 1, key0 + kKeys);
+    if (active && key0 < last) compute(buf, key0);
+    buf ^= 1;
+  }
+
+  {
+    const uint32_t w = __float_as_uint(l);
+    auto x = __builtin_amdgcn_permlane32_swap(w, w, false, false);
+    l = __uint_as_float(x[0]) + __uint_as_float(x[1]);
+  }
+  if (sq.n_split > 1) {
+    const int64_t prow = ((int64_t)sq.part0 + (unit - sq.unit0)) * (32 * NW) + 32 * wave + n;
+    float* po = p.part_o + prow * D;
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        *reinterpret_cast<f4*>(po + 32 * j + 8 * e + 4 * h) =
+            f4{o[j][4 * e], o[j][4 * e + 1], o[j][4 * e + 2], o[j][4 * e + 3]};
+    if (h == 0) {
+      p.part_ml[2 * prow] = m;
+      p.part_ml[2 * prow + 1] = l;
+    }
+    return;
+  }
+  if (!ok) return;
+  const int64_t row = (int64_t)(sq.q_row0 + query) * p.Hq + qh;
+  if (p.lse != nullptr && h == 0) p.lse[row] = fmaf(m, p.scale, __builtin_amdgcn_logf(l) * kLn2);
+  const float inv = 1.f / l;
+  uint16_t* dst = static_cast<uint16_t*>(p.out) + row * D;
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      i2 x;
+      x[0] = (int)pack_bf16(o[j][4 * e] * inv, o[j][4 * e + 1] * inv);
+      x[1] = (int)pack_bf16(o[j][4 * e + 2] * inv, o[j][4 * e + 3] * inv);
+      *reinterpret_cast<i2*>(dst + 32 * j + 8 * e + 4 * h) = x;
+    }
+}
+
+}  // namespace
+
+hipError_t launch_prompt(int d, const AttnArgs& p, hipStream_t s) {
+  if (p.n_units == 0) return hipSuccess;
+  const dim3 grid((unsigned)p.n_units), block(64 * kPromptWaves);
+  if (d == 128) prompt_kernel<128, kPromptWaves><<<grid, block, 0, s>>>(p);
+  else prompt_kernel<64, kPromptWaves><<<grid, block, 0, s>>>(p);
+  return hipGetLastError();
+}
+
+}  // namespace dosa
