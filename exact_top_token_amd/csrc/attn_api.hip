@@ -339,12 +339,17 @@ int cache_io(bool write, const dsa_cache* cache, void* k, int64_t k_stride, void
   return DOSA_OK;
 }
 
-size_t evict_workspace(int32_t batch, const int32_t* new_lens, int32_t* stride) {
-  int64_t most = 1;
-  for (int b = 0; b < batch; ++b) most = std::max<int64_t>(most, new_lens[b]);
-  most = (most + 63) / 64 * 64;
-  *stride = (int32_t)std::min<int64_t>(most, kMaxInt);
-  return up256((size_t)std::max(batch, 1) * most * sizeof(int32_t));
+// Ints of a sequence's eviction workspace.
+int64_t evict_ints(int32_t kv_len, int32_t new_len) {
+  const int64_t cap = std::min(new_len, kv_len - new_len);
+  const int64_t rounds = ((int64_t)kv_len + 1023) / 1024, near = kEvictNear;
+  return (kEvictHead + 2 * cap + std::max<int64_t>(0, rounds - near) * 1024 + 15) / 16 * 16;
+}
+
+size_t evict_workspace(int32_t batch, const int32_t* kv_lens, const int32_t* new_lens) {
+  int64_t n = 0;
+  for (int b = 0; b < batch; ++b) n += evict_ints(kv_lens[b], new_lens[b]);
+  return up256((size_t)std::max<int64_t>(n, 1) * sizeof(int32_t));
 }
 
 template <class F>
@@ -538,8 +543,7 @@ size_t dsa_evict_workspace_size(int32_t batch, const int32_t* kv_lens, const int
   return guarded_size([&]() -> size_t {
     int64_t tn, tk;
     if (check_lens(batch, new_lens, kv_lens, "new_len", "kv_len", &tn, &tk) != DOSA_OK) return 0;
-    int32_t stride;
-    return evict_workspace(batch, new_lens, &stride);
+    return evict_workspace(batch, kv_lens, new_lens);
   });
 }
 
@@ -586,7 +590,7 @@ int dsa_cache_evict(const float* acc, const int32_t* pos, const int32_t* page_ta
       mv.a[i] = EvictArray{static_cast<const uint8_t*>(x.src), static_cast<uint8_t*>(x.dst), (int32_t)x.row_bytes, gran};
     }
     EvictArgs a{};
-    const size_t need = evict_workspace(batch, new_lens, &a.move_stride);
+    const size_t need = evict_workspace(batch, kv_lens, new_lens);
     if (workspace == nullptr || workspace_bytes < need || !aligned(workspace, 16))
       return fail(DOSA_ERR_WORKSPACE, "workspace needs " + std::to_string(need) + " bytes, 16-byte aligned");
     hipStream_t s = static_cast<hipStream_t>(stream);
@@ -600,7 +604,8 @@ int dsa_cache_evict(const float* acc, const int32_t* pos, const int32_t* page_ta
     a.window = window;
     a.out_src = out_src;
     a.out_stride = out_stride;
-    a.moves = static_cast<int32_t*>(workspace);
+    a.ws = static_cast<int32_t*>(workspace);
+    mv.ws = a.ws;
     mv.out_src = out_src;
     mv.table = page_table;
     mv.out_stride = out_stride;
@@ -608,14 +613,15 @@ int dsa_cache_evict(const float* acc, const int32_t* pos, const int32_t* page_ta
     mv.max_pages = max_pages;
     mv.num_pages = num_pages;
     mv.n_arr = n_arrays;
+    int64_t off = 0;
     for (int b0 = 0; b0 < batch; b0 += kEvictSeqs) {
       a.n_seq = mv.n_seq = std::min(kEvictSeqs, batch - b0);
-      mv.max_new = 0;
       for (int i = 0; i < a.n_seq; ++i) {
         const int b = b0 + i;
-        a.s[i] = EvictSeq{kv_lens[b], new_lens[b], seen_lens != nullptr ? seen_lens[b] : kv_lens[b], b};
+        a.s[i] = EvictSeq{off, kv_lens[b], new_lens[b], seen_lens != nullptr ? seen_lens[b] : kv_lens[b], b,
+                          std::min(new_lens[b], kv_lens[b] - new_lens[b]), 0};
         mv.s[i] = a.s[i];
-        mv.max_new = std::max(mv.max_new, new_lens[b]);
+        off += evict_ints(kv_lens[b], new_lens[b]);
       }
       hipError_t e;
       {

@@ -109,8 +109,16 @@ hipError_t launch_weights(bool f32, int d, const WeightArgs& p, hipStream_t s);
 hipError_t launch_weights_join(const WeightArgs& p, hipStream_t s);
 
 // Eviction.
+// A sequence's workspace: the number of moves (in its first kEvictHead ints),
+// the keys that move, the indices they move to (cap of each), and the ranks of
+// the keys beyond the kEvictNear * 1024 that its workgroup keeps in registers.
+constexpr int kEvictHead = 16;
+constexpr int kEvictNear = 16;
 struct EvictSeq {
+  int64_t ws_off;
   int32_t kv_len, new_len, seen, b;
+  int32_t cap;              // moves at most: min(new_len, kv_len - new_len)
+  int32_t pad;
 };
 constexpr int kEvictSeqs = 64;
 struct EvictArgs {
@@ -121,8 +129,7 @@ struct EvictArgs {
   int32_t prefix, window;
   int32_t* out_src;         // [batch, out_stride]
   int32_t out_stride;
-  int32_t* moves;           // workspace, move_stride ints a sequence: movers (ascending)
-  int32_t move_stride;
+  int32_t* ws;
   int32_t n_seq;
   EvictSeq s[kEvictSeqs];
 };
@@ -138,11 +145,12 @@ struct EvictMoveArgs {
   const int32_t* table;
   int32_t out_stride, page_size, max_pages, num_pages;
   int32_t n_seq, n_arr;
-  int32_t max_new;          // largest new_len
+  int32_t in_blocks;        // set by the launch
+  const int32_t* ws;
   EvictSeq s[kEvictSeqs];
   EvictArray a[kEvictArrays];
 };
 hipError_t launch_evict_select(const EvictArgs& p, hipStream_t s);
-hipError_t launch_evict_move(const EvictMoveArgs& p, hipStream_t s);
+hipError_t launch_evict_move(EvictMoveArgs p, hipStream_t s);
 
 }  // namespace dosa

@@ -15,127 +15,303 @@ namespace {
 
 constexpr int kThreads = 1024, kEvWaves = kThreads / 64;
 
-__device__ __forceinline__ uint32_t rank_of(const EvictArgs& p, const EvictSeq& s, int key) {
-  const int slot = cache_slot(p.table, s.b, p.max_pages, p.page_size, p.num_pages, key);
-  if (slot < 0) return 0u;
-  const int pos = p.pos != nullptr ? p.pos[slot] : key;
-  if (pos < p.prefix || (int64_t)pos >= (int64_t)s.seen - p.window) return 0xffffffffu;
-  const float a = p.acc[slot] + 0.f;        // -0 ranks as 0
-  const uint32_t u = __float_as_uint(a);
-  const uint32_t r = u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
-  return r < 1u ? 1u : (r > 0xfffffffeu ? 0xfffffffeu : r);
+__device__ __forceinline__ uint32_t rank_of(const EvictArgs& p, const EvictSeq& s, float acc, int pos) {
+  const uint32_t u = __float_as_uint(acc + 0.f);        // -0 ranks as 0
+  uint32_t r = u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+  r = r < 1u ? 1u : (r > 0xfffffffeu ? 0xfffffffeu : r);
+  return pos < p.prefix || (int64_t)pos >= (int64_t)s.seen - p.window ? 0xffffffffu : r;
 }
 
-// Exclusive sum over the workgroup of a 0/1 flag; *total gets the whole sum.
-__device__ __forceinline__ int block_rank(bool f, int* sh, int* total) {
-  const unsigned long long b = __ballot(f);
-  const int lane = lane64(), wave = threadIdx.x >> 6;
-  if (lane == 0) sh[wave] = __popcll(b);
-  __syncthreads();
-  int before = 0, all = 0;
+// Ranks of N rounds from round i0 on, as unsigned numbers: 0 without a page,
+// all ones if protected, else the order of the weight's bits.  Each kind of
+// load is issued for all rounds before any is used, without branches, since
+// the chain page, weight, position is all latency.  With pages of a multiple
+// of 64 keys a wavefront's keys of a round lie in one page.
+template <int N>
+__device__ __forceinline__ void load_ranks(const EvictArgs& p, const EvictSeq& s, int i0, int wave, uint32_t* rk) {
+  const int32_t* table = p.table + (int64_t)s.b * p.max_pages;
+  const bool whole = (p.page_size & 63) == 0;
+  int slot[N];
 #pragma unroll
-  for (int i = 0; i < kEvWaves; ++i) {
-    const int c = sh[i];
-    before += i < wave ? c : 0;
-    all += c;
+  for (int i = 0; i < N; ++i) {
+    const int key0 = (i0 + i) * 1024 + 64 * wave, lane = lane64();
+    int at = whole ? key0 : key0 + lane;
+    at = at < s.kv_len ? at : s.kv_len - 1;
+    const int pg = at / p.page_size;
+    const int page = whole ? table[__builtin_amdgcn_readfirstlane(pg)] : table[pg];
+    const int in = whole ? key0 + lane - pg * p.page_size : at - pg * p.page_size;
+    slot[i] = key0 + lane < s.kv_len && (uint32_t)page < (uint32_t)p.num_pages ? page * p.page_size + in : -1;
   }
-  __syncthreads();
-  *total = all;
-  return before + __popcll(b & ((1ull << lane) - 1ull));
+  float acc[N];
+  int pos[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    acc[i] = p.acc[slot[i] < 0 ? 0 : slot[i]];
+    pos[i] = (i0 + i) * 1024 + 64 * wave + lane64();
+  }
+  if (p.pos != nullptr) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) pos[i] = p.pos[slot[i] < 0 ? 0 : slot[i]];
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) rk[i] = slot[i] < 0 ? 0u : rank_of(p, s, acc[i], pos[i]);
 }
 
+// Exclusive sums over cnt[0..n), n <= kThreads, in place; one workgroup.
+__device__ __forceinline__ void block_scan(int* cnt, int n, int* sh) {
+  const int tid = threadIdx.x, lane = lane64(), wave = tid >> 6;
+  const int v = tid < n ? cnt[tid] : 0;
+  int x = v;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int y = __shfl_up(x, d);
+    x += lane >= d ? y : 0;
+  }
+  if (lane == 63) sh[wave] = x;
+  __syncthreads();
+  int before = 0;
+#pragma unroll
+  for (int i = 0; i < kEvWaves; ++i) before += i < wave ? sh[i] : 0;
+  if (tid < n) cnt[tid] = before + x - v;
+  __syncthreads();
+}
+
+// One workgroup chooses a sequence's keys.  A wavefront's 64 keys of round i
+// are i * 1024 + 64 * wave ..., a thread keeps the ranks of its first PER
+// rounds in registers; longer sequences keep theirs in the workspace.  The
+// threshold, the new_len-th largest rank, is found digit by digit (8 bits)
+// with a histogram of 32 copies, one per LDS bank, so that a lane meets at most
+// one other of its wavefront in a counter however the weights are distributed.
+// Then two prefix sums over the (round, wavefront) counts number the keys that
+// equal the threshold and the keys that move.
+// Bound by latency: a few dependent loads and about twenty barriers.
+template <int PER>
 __global__ __launch_bounds__(kThreads) void evict_select_kernel(const EvictArgs p) {
-  __shared__ uint32_t hist[256];
+  __shared__ uint32_t hist[256 * 32];
+  __shared__ uint32_t tot[256];
   __shared__ int sh[kEvWaves];
+  __shared__ int carry[3];
   __shared__ uint32_t sel[2];
   const EvictSeq& s = p.s[blockIdx.x];
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, lane = lane64(), wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   int32_t* out = p.out_src + (int64_t)s.b * p.out_stride;
-  int32_t* movers = p.moves + (int64_t)s.b * p.move_stride;
-  // threshold: the new_len-th largest rank, digit by digit
+  int32_t* ws = p.ws + s.ws_off;
+  int32_t* movers = ws + kEvictHead;
+  int32_t* holes = movers + s.cap;
+  uint32_t* far = reinterpret_cast<uint32_t*>(holes + s.cap);       // ranks of the rounds from PER on
+  const int rounds = (s.kv_len + kThreads - 1) / kThreads;
+  const int near = rounds < PER ? rounds : PER;
+  if (s.new_len == 0 || s.new_len == s.kv_len) {       // nothing to choose
+    for (int k = tid; k < p.out_stride; k += kThreads) out[k] = k < s.new_len ? k : -1;
+    if (tid == 0) ws[0] = 0;
+    return;
+  }
+  uint32_t rk[PER];
+#pragma unroll
+  for (int i = 0; i < PER; i += 8) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) rk[i + j] = 0u;
+    if (i < near) load_ranks<8>(p, s, i, wave, rk + i);
+  }
+  for (int i = PER; i < rounds; i += 8) {
+    uint32_t r[8];
+    load_ranks<8>(p, s, i, wave, r);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (i + j < rounds) far[(i + j - PER) * kThreads + tid] = r[j];
+  }
+
   uint32_t pre = 0, need = (uint32_t)s.new_len;
-  if (s.new_len > 0) {
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      if (tid < 256) hist[tid] = 0;
-      __syncthreads();
-      for (int k = tid; k < s.kv_len; k += kThreads) {
-        const uint32_t r = rank_of(p, s, k);
-        if (shift == 24 || (r >> (shift + 8)) == (pre >> (shift + 8))) atomicAdd(&hist[(r >> shift) & 255u], 1u);
-      }
-      __syncthreads();
-      if (tid == 0) {
-        uint32_t left = need;
-        int d = 255;
-        for (; d > 0 && hist[d] < left; --d) left -= hist[d];
-        sel[0] = pre | ((uint32_t)d << shift);
-        sel[1] = left;
-      }
-      __syncthreads();
-      pre = sel[0];
-      need = sel[1];
-      __syncthreads();
+  for (int shift = 24; shift >= 0; shift -= 8) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) hist[i * kThreads + tid] = 0;
+    __syncthreads();
+    const uint32_t above = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
+    auto count = [&](int i, uint32_t r) {
+      if (i * kThreads + tid < s.kv_len && (r & above) == pre) atomicAdd(&hist[((r >> shift) & 255u) * 32 + (lane & 31)], 1u);
+    };
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (i < near) count(i, rk[i]);
+    for (int i = PER; i < rounds; i += 8) {
+      uint32_t r[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) r[j] = far[((i + j < rounds ? i + j : rounds - 1) - PER) * kThreads + tid];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (i + j < rounds) count(i + j, r[j]);
     }
+    __syncthreads();
+    {
+      // thread t adds up copies 8 (t % 4).. of digit t / 4, starting at its own bank
+      uint32_t x = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x += hist[(tid >> 2) * 32 + 8 * (tid & 3) + ((i + (tid >> 2)) & 7)];
+      x += __shfl_xor(x, 1);
+      x += __shfl_xor(x, 2);
+      if ((tid & 3) == 0) tot[tid >> 2] = x;
+    }
+    __syncthreads();
+    if (wave == 0) {
+      // lane l: digits 255 - 4l downwards; the digit at which the count from the top reaches `need`
+      uint32_t v[4], x = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[j] = tot[255 - (4 * lane + j)];
+        x += v[j];
+      }
+      uint32_t incl = x;
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const uint32_t y = __shfl_up(incl, d);
+        incl += lane >= d ? y : 0u;
+      }
+      uint32_t before = incl - x;
+      if (before < need && incl >= need) {
+        int j = 0;
+        for (; j < 3 && before + v[j] < need; ++j) before += v[j];
+        sel[0] = pre | ((uint32_t)(255 - (4 * lane + j)) << shift);
+        sel[1] = need - before;
+      }
+    }
+    __syncthreads();
+    pre = sel[0];
+    need = sel[1];
   }
-  // ranks above `pre` stay, and the first `need` equal to it
-  int equal0 = 0, mover0 = 0, hole0 = 0;
-  for (int k0 = 0; k0 < s.kv_len; k0 += kThreads) {
-    const int k = k0 + tid;
-    const bool in = k < s.kv_len;
-    const uint32_t r = in && s.new_len > 0 ? rank_of(p, s, k) : 0u;
-    int n_eq, n_mv, n_ho;
-    const bool eq = in && s.new_len > 0 && r == pre;
-    const int er = equal0 + block_rank(eq, sh, &n_eq);
-    const bool keep = in && s.new_len > 0 && (r > pre || (eq && er < (int)need));
-    const bool mv = keep && k >= s.new_len, ho = in && !keep && k < s.new_len;
-    const int mr = mover0 + block_rank(mv, sh, &n_mv), hr = hole0 + block_rank(ho, sh, &n_ho);
-    if (mv) movers[mr] = k;
-    if (in && k < s.new_len) out[k] = keep ? k : -2 - hr;
-    equal0 += n_eq;
-    mover0 += n_mv;
-    hole0 += n_ho;
+
+  // ranks above `pre` stay, and the first `need` equal to it.  64 rounds of
+  // 16 wavefronts at a time, the histogram's memory for the counts
+  int* cnt = reinterpret_cast<int*>(hist);          // [64 rounds][16 wavefronts]
+  if (tid < 3) carry[tid] = 0;
+  for (int i0 = 0; i0 < rounds; i0 += 64) {
+    const int nr = rounds - i0 < 64 ? rounds - i0 : 64, n = nr * kEvWaves;
+    auto rank = [&](int i) -> uint32_t { return far[(i - PER) * kThreads + tid]; };
+    auto each = [&](auto f) {
+      // ranks from memory, eight rounds in flight
+      auto batch = [&](int from, int base) {
+        for (int i = from; i < nr; i += 8) {
+          uint32_t r[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) r[j] = rank(base + (i + j < nr ? i + j : nr - 1));
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (i + j < nr) f(i + j, r[j]);
+        }
+      };
+      if (i0 == 0) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+          if (i < nr) f(i, rk[i]);
+        batch(PER, 0);
+      } else {
+        batch(0, i0);
+      }
+    };
+    auto key = [&](int i) { return (i0 + i) * kThreads + tid; };
+    const unsigned long long below = (1ull << lane) - 1ull;
+    __syncthreads();
+    each([&](int i, uint32_t r) {
+      const unsigned long long b = __ballot(key(i) < s.kv_len && r == pre);
+      if (lane == 0) cnt[i * kEvWaves + wave] = __popcll(b);
+    });
+    __syncthreads();
+    int last = tid == n - 1 ? cnt[n - 1] : 0;
+    block_scan(cnt, n, sh);
+    const int eq0 = carry[0];
+    auto kept = [&](int i, uint32_t r) -> bool {
+      const unsigned long long b = __ballot(key(i) < s.kv_len && r == pre);
+      const int er = eq0 + cnt[i * kEvWaves + wave] + __popcll(b & below);
+      return key(i) < s.kv_len && (r > pre || (r == pre && er < (int)need));
+    };
+    int* mv = cnt + kThreads;
+    int* ho = mv + kThreads;
+    each([&](int i, uint32_t r) {
+      const bool k = kept(i, r);
+      const unsigned long long bm = __ballot(k && key(i) >= s.new_len), bh = __ballot(!k && key(i) < s.new_len);
+      if (lane == 0) {
+        mv[i * kEvWaves + wave] = __popcll(bm);
+        ho[i * kEvWaves + wave] = __popcll(bh);
+      }
+    });
+    __syncthreads();
+    const int last_m = tid == n - 1 ? mv[n - 1] : 0, last_h = tid == n - 1 ? ho[n - 1] : 0;
+    block_scan(mv, n, sh);
+    block_scan(ho, n, sh);
+    const int mv0 = carry[1], ho0 = carry[2];
+    each([&](int i, uint32_t r) {
+      const bool k = kept(i, r);
+      const bool im = k && key(i) >= s.new_len, ih = !k && key(i) < s.new_len;
+      const unsigned long long bm = __ballot(im), bh = __ballot(ih);
+      if (im) movers[mv0 + mv[i * kEvWaves + wave] + __popcll(bm & below)] = key(i);
+      if (ih) holes[ho0 + ho[i * kEvWaves + wave] + __popcll(bh & below)] = key(i);
+      if (k && key(i) < s.new_len) out[key(i)] = key(i);
+    });
+    __syncthreads();
+    if (tid == n - 1) {
+      carry[0] = eq0 + cnt[n - 1] + last;
+      carry[1] = mv0 + mv[n - 1] + last_m;
+      carry[2] = ho0 + ho[n - 1] + last_h;
+    }
+    __syncthreads();
   }
-  __threadfence_block();
-  __syncthreads();
-  for (int k = tid; k < p.out_stride; k += kThreads) {
-    if (k >= s.new_len) out[k] = -1;
-    else if (out[k] <= -2) out[k] = movers[-2 - out[k]];
-  }
+  const int moved = carry[1];
+  for (int i = tid; i < moved; i += kThreads) out[holes[i]] = movers[i];
+  for (int k = s.new_len + tid; k < p.out_stride; k += kThreads) out[k] = -1;
+  if (tid == 0) ws[0] = moved;
 }
 
-constexpr int kRows = 64;     // rows of a workgroup
+// Rows of arrays moved in place: workgroups of kMoveRows entries of the
+// sequence's list of moves.
+constexpr int kMoveRows = 8;
 
 template <class V>
-__device__ __forceinline__ void copy_rows(const EvictArray& a, const int* from, const int* to, int n, bool in_place) {
+__device__ __forceinline__ void copy_rows(const EvictArray& a, const int* from, const int* to, int n) {
   const int cols = a.row_bytes / (int)sizeof(V);
   const V* src = reinterpret_cast<const V*>(a.src);
   V* dst = reinterpret_cast<V*>(a.dst);
   for (int i = threadIdx.x; i < n * cols; i += (int)blockDim.x) {
     const int r = i / cols, c = i - r * cols;
-    const int f = from[r], t = to[r];
-    if (f < 0 || t < 0 || (in_place && f == t)) continue;
-    dst[(int64_t)t * cols + c] = src[(int64_t)f * cols + c];
+    if (from[r] >= 0 && to[r] >= 0) dst[(int64_t)to[r] * cols + c] = src[(int64_t)from[r] * cols + c];
   }
 }
 
+__device__ __forceinline__ void copy_any(const EvictArray& a, const int* from, const int* to, int n) {
+  if (a.gran == 16) copy_rows<i4>(a, from, to, n);
+  else if (a.gran == 4) copy_rows<uint32_t>(a, from, to, n);
+  else copy_rows<uint8_t>(a, from, to, n);
+}
+
+// Workgroups 0..in_blocks-1 of a sequence: the moves of the arrays in place;
+// the others: every kept row of the arrays that go elsewhere.
+constexpr int kCopyRows = 256;
+
 __global__ __launch_bounds__(256) void evict_move_kernel(const EvictMoveArgs p) {
-  __shared__ int from[kRows], to[kRows];
+  __shared__ int from[kCopyRows], to[kCopyRows];
   const EvictSeq& s = p.s[blockIdx.y];
-  const int j0 = blockIdx.x * kRows;
-  const int n = min(kRows, s.new_len - j0);
-  if (n <= 0) return;
-  if ((int)threadIdx.x < n) {
-    const int j = j0 + (int)threadIdx.x;
-    const int src = p.out_src[(int64_t)s.b * p.out_stride + j];
-    to[threadIdx.x] = cache_slot(p.table, s.b, p.max_pages, p.page_size, p.num_pages, j);
-    from[threadIdx.x] = src < 0 ? -1 : cache_slot(p.table, s.b, p.max_pages, p.page_size, p.num_pages, src);
-  }
-  __syncthreads();
-  for (int i = 0; i < p.n_arr; ++i) {
-    const EvictArray& a = p.a[i];
-    const bool in_place = a.src == a.dst;
-    if (a.gran == 16) copy_rows<i4>(a, from, to, n, in_place);
-    else if (a.gran == 4) copy_rows<uint32_t>(a, from, to, n, in_place);
-    else copy_rows<uint8_t>(a, from, to, n, in_place);
+  auto slot = [&](int key) { return cache_slot(p.table, s.b, p.max_pages, p.page_size, p.num_pages, key); };
+  const int tid = threadIdx.x;
+  if ((int)blockIdx.x < p.in_blocks) {
+    const int32_t* ws = p.ws + s.ws_off;
+    const int j0 = blockIdx.x * kMoveRows, n = min(kMoveRows, ws[0] - j0);
+    if (n <= 0) return;
+    if (tid < n) {
+      from[tid] = slot(ws[kEvictHead + j0 + tid]);
+      to[tid] = slot(ws[kEvictHead + s.cap + j0 + tid]);
+    }
+    __syncthreads();
+    for (int i = 0; i < p.n_arr; ++i)
+      if (p.a[i].src == p.a[i].dst) copy_any(p.a[i], from, to, n);
+  } else {
+    const int j0 = ((int)blockIdx.x - p.in_blocks) * kCopyRows, n = min(kCopyRows, s.new_len - j0);
+    if (n <= 0) return;
+    if (tid < n) {
+      const int src = p.out_src[(int64_t)s.b * p.out_stride + j0 + tid];
+      to[tid] = slot(j0 + tid);
+      from[tid] = src < 0 ? -1 : slot(src);
+    }
+    __syncthreads();
+    for (int i = 0; i < p.n_arr; ++i)
+      if (p.a[i].src != p.a[i].dst) copy_any(p.a[i], from, to, n);
   }
 }
 
@@ -143,13 +319,26 @@ __global__ __launch_bounds__(256) void evict_move_kernel(const EvictMoveArgs p) 
 
 hipError_t launch_evict_select(const EvictArgs& p, hipStream_t s) {
   if (p.n_seq == 0) return hipSuccess;
-  evict_select_kernel<<<dim3((unsigned)p.n_seq), dim3(kThreads), 0, s>>>(p);
+  int most = 0;
+  for (int i = 0; i < p.n_seq; ++i) most = most > p.s[i].kv_len ? most : p.s[i].kv_len;
+  const dim3 grid((unsigned)p.n_seq), block(kThreads);
+  if (most <= 8 * kThreads) evict_select_kernel<8><<<grid, block, 0, s>>>(p);
+  else evict_select_kernel<kEvictNear><<<grid, block, 0, s>>>(p);
   return hipGetLastError();
 }
 
-hipError_t launch_evict_move(const EvictMoveArgs& p, hipStream_t s) {
-  if (p.n_seq == 0 || p.n_arr == 0 || p.max_new == 0) return hipSuccess;
-  evict_move_kernel<<<dim3((unsigned)((p.max_new + kRows - 1) / kRows), (unsigned)p.n_seq), dim3(256), 0, s>>>(p);
+hipError_t launch_evict_move(EvictMoveArgs p, hipStream_t s) {
+  int most_new = 0, most_cap = 0;
+  bool in = false, away = false;
+  for (int i = 0; i < p.n_seq; ++i) {
+    most_new = most_new > p.s[i].new_len ? most_new : p.s[i].new_len;
+    most_cap = most_cap > p.s[i].cap ? most_cap : p.s[i].cap;
+  }
+  for (int i = 0; i < p.n_arr; ++i) (p.a[i].src == p.a[i].dst ? in : away) = true;
+  p.in_blocks = in ? (most_cap + kMoveRows - 1) / kMoveRows : 0;
+  const int blocks = p.in_blocks + (away ? (most_new + kCopyRows - 1) / kCopyRows : 0);
+  if (p.n_seq == 0 || blocks == 0) return hipSuccess;
+  evict_move_kernel<<<dim3((unsigned)blocks, (unsigned)p.n_seq), dim3(256), 0, s>>>(p);
   return hipGetLastError();
 }
 
