@@ -17,7 +17,7 @@ matching ``*_workspace_size`` bytes.
 """
 from __future__ import annotations
 
-import contextlib
+import array
 import ctypes
 from typing import Optional, Sequence
 
@@ -57,10 +57,16 @@ def declare(L) -> None:
         fn.argtypes, fn.restype = args, res
 
 
-def _lib():
-    from . import lib
+_loaded = None
 
-    return lib()
+
+def _lib():
+    global _loaded
+    if _loaded is None:
+        from . import lib
+
+        _loaded = lib()
+    return _loaded
 
 
 def _bad(msg: str):
@@ -76,15 +82,29 @@ def _check(st: int) -> None:
         raise DosaError(st, status_string(st))
 
 
-def _lens(v: Sequence[int]):
-    return (_I32 * max(len(v), 1))(*v)
+class _lens:
+    """Host lengths as an argument of the library; ctypes keeps the object, and so the array, for the call."""
+
+    __slots__ = ("data", "_as_parameter_")
+
+    def __init__(self, v: Sequence[int]):
+        try:
+            self.data = array.array("i", v) if len(v) else array.array("i", (0,))
+        except (TypeError, OverflowError):
+            _bad("lengths must be integers below 2^31")
+        self._as_parameter_ = self.data.buffer_info()[0]
+
+
+_codes = {"f32": 0, "bf16": 1}
 
 
 def _code(dtype, what: str) -> int:
-    name = str(dtype).rsplit(".", 1)[-1]
-    code = {"float32": 0, "f32": 0, "bfloat16": 1, "bf16": 1}.get(name)
+    code = _codes.get(dtype)
     if code is None:
-        _bad(f"{what}: type {name} (float32 and bfloat16 are supported)")
+        code = {"torch.float32": 0, "torch.bfloat16": 1}.get(str(dtype))
+        if code is None:
+            _bad(f"{what}: type {dtype} (float32 and bfloat16 are supported)")
+        _codes[dtype] = code
     return code
 
 
@@ -131,20 +151,31 @@ def _space(ws, device):
     return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
-@contextlib.contextmanager
-def _on(device, stream):
+class _On:
     """The stream to run on, with the tensors' device current."""
-    import torch
 
-    if device.type != "cuda":
-        _bad(f"tensors are on {device}, not on a GPU")
-    if torch.cuda.current_device() == device.index:
-        yield int(getattr(stream, "cuda_stream", stream) if stream is not None
-                  else torch.cuda.current_stream().cuda_stream)
-        return
-    with torch.cuda.device(device):
-        yield int(getattr(stream, "cuda_stream", stream) if stream is not None
-                  else torch.cuda.current_stream().cuda_stream)
+    __slots__ = ("back", "device", "stream")
+
+    def __init__(self, device, stream):
+        self.device, self.stream, self.back = device, stream, None
+
+    def __enter__(self) -> int:
+        import torch
+
+        if self.device.type != "cuda":
+            _bad(f"tensors are on {self.device}, not on a GPU")
+        if torch.cuda.current_device() != self.device.index:
+            self.back = torch.cuda.device(self.device)
+            self.back.__enter__()
+        st = torch.cuda.current_stream() if self.stream is None else self.stream
+        return int(getattr(st, "cuda_stream", st))
+
+    def __exit__(self, *exc):
+        if self.back is not None:
+            self.back.__exit__(*exc)
+
+
+_on = _On
 
 
 class Cache:

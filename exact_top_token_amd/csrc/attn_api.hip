@@ -97,24 +97,28 @@ CacheView view(const dsa_cache* c) {
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 // ---------------------------------------------------------------------------
-// Work split of the wavefront attention kernel.  A unit is one row tile of one
-// kv head over one key range.  Ranges are cut so that the launch has about
-// kTargetUnits units of equal work (two rounds of the wavefronts the GPU
-// holds at eight a CU), none shorter than kMinKeys.
+// Work split of the attention kernels.  A unit is one row tile of one kv head
+// over one key range.  The range length is the shortest (kMinKeys at least)
+// for which the launch's units fit in kRounds rounds of what the GPU holds at
+// once: a launch a little over a whole number of rounds would leave most of
+// the GPU idle in its last one.  One round against two: 0.48 and 0.50 ms for a
+// decode step of 64 sequences, 38 and 50 us for 2048 selected keys of 64
+// queries, whose partial results halve.
 // ---------------------------------------------------------------------------
-constexpr int64_t kTargetUnits = 4096;
+constexpr int64_t kResident = 2048;      // wavefronts at eight a CU
+constexpr int64_t kRounds = 1;
 constexpr int64_t kMinKeys = 128;
 
 struct AttnChunk {
   AttnArgs a;
-  int64_t parts = 0;
+  int64_t parts;
 };
 
-// Which kernel takes a sequence: bf16 prompts whose rows (queries times group
-// heads) fill more than two wavefronts of the tiled kernel go to it, its tiles
-// being shared by 256 rows; all else to the wavefront kernel.
-constexpr int64_t kTiledRows = 64;
-constexpr int64_t kTiledUnits = 512;     // workgroups of a launch of the tiled kernel: two a CU
+// Which kernel takes a sequence: bf16 prompts of more than 16 rows (queries
+// times group heads) go to the tiled kernel, whose 256 rows share what is read
+// of the keys; all else to the wavefront kernel.
+constexpr int64_t kTiledRows = 16;
+constexpr int64_t kTiledResident = 256;  // workgroups of the tiled kernel: one a CU
 constexpr int64_t kTiledMinKeys = 512;
 
 bool takes_tiled(int src, int64_t rows) { return src == A_BF16 && rows > kTiledRows; }
@@ -122,7 +126,7 @@ bool takes_tiled(int src, int64_t rows) { return src == A_BF16 && rows > kTiledR
 // Sequences b0.. of the batch that the kernel takes, at most kAttnSeqs with
 // queries; returns the sequence after the last one seen, or -1 if the launch
 // would be too large.
-int plan_attn(AttnChunk& ch, int src, bool tiled, int b0, int32_t batch, const int32_t* q_lens, const int32_t* kv_lens,
+int plan_attn(AttnChunk& ch, int src, int d, bool tiled, int b0, int32_t batch, const int32_t* q_lens, const int32_t* kv_lens,
               int32_t Hq, int32_t Hkv, int32_t topk, int64_t* q_row, int64_t* k_row) {
   AttnArgs& a = ch.a;
   const bool sel = topk > 0;
@@ -147,17 +151,28 @@ int plan_attn(AttnChunk& ch, int src, bool tiled, int b0, int32_t batch, const i
     *q_row += q_lens[b];
     *k_row += kv_lens[b];
   }
-  a.rt = tiled ? 2 * kPromptWaves : (most > 16 ? attn_max_rt(src) : 1);
-  const int64_t tile = 16 * a.rt;
+  a.rt = tiled ? 2 * kPromptWaves : (most > 16 ? attn_max_rt(src, d) : 1);
+  a.hp = tiled ? 1 : attn_heads(src, a.rt, Hkv);
+  const int64_t tile = 16 * a.rt, heads = Hkv / a.hp;
   auto tiles = [&](const AttnSeq& s) -> int64_t {
     return sel ? (int64_t)s.q_len * ((a.group + tile - 1) / tile) : ((int64_t)s.q_len * a.group + tile - 1) / tile;
   };
   auto keys = [&](const AttnSeq& s) -> int64_t { return sel ? topk : s.kv_len; };
   std::stable_sort(a.s, a.s + a.n_seq, [&](const AttnSeq& x, const AttnSeq& y) { return keys(x) > keys(y); });
-  int64_t work = 0;
-  for (int i = 0; i < a.n_seq; ++i) work += tiles(a.s[i]) * Hkv * keys(a.s[i]);
-  const int64_t target = tiled ? kTiledUnits : kTargetUnits;
-  const int64_t len = std::max(tiled ? kTiledMinKeys : kMinKeys, (work + target - 1) / target);
+  const int64_t cap = kRounds * (tiled ? kTiledResident : kResident);
+  auto units_at = [&](int64_t len) {
+    int64_t n = 0;
+    for (int i = 0; i < a.n_seq; ++i) n += tiles(a.s[i]) * heads * ((keys(a.s[i]) + len - 1) / len);
+    return n;
+  };
+  // shortest range length in steps of 64 that keeps to the cap, or one range each
+  int64_t lo = (tiled ? kTiledMinKeys : kMinKeys) / 64, hi = lo;
+  for (int i = 0; i < a.n_seq; ++i) hi = std::max(hi, (keys(a.s[i]) + 63) / 64);
+  while (lo < hi) {
+    const int64_t mid = (lo + hi) / 2;
+    if (units_at(64 * mid) <= cap) hi = mid; else lo = mid + 1;
+  }
+  const int64_t len = 64 * lo;
   int64_t units = 0, join = 0, parts = 0;
   for (int i = 0; i < a.n_seq; ++i) {
     AttnSeq& s = a.s[i];
@@ -172,9 +187,9 @@ int plan_attn(AttnChunk& ch, int src, bool tiled, int b0, int32_t batch, const i
     s.unit0 = (int32_t)units;
     s.join0 = (int32_t)join;
     s.part0 = (int32_t)parts;
-    units += nrt * n * Hkv;
+    units += nrt * n * heads;
     if (n > 1) {
-      join += nrt * Hkv * tile;
+      join += (int64_t)s.q_len * Hq;
       parts += nrt * n * Hkv;
     }
     if (join > kMaxInt) return -1;
@@ -199,7 +214,7 @@ size_t attn_workspace(int src, int32_t batch, const int32_t* q_lens, const int32
     int64_t qr = 0, kr = 0;
     for (int b = 0; b < batch;) {
       AttnChunk ch;
-      b = plan_attn(ch, src, tiled != 0, b, batch, q_lens, kv_lens, Hq, Hkv, topk, &qr, &kr);
+      b = plan_attn(ch, src, d, tiled != 0, b, batch, q_lens, kv_lens, Hq, Hkv, topk, &qr, &kr);
       if (b < 0) return 0;
       most = std::max(most, part_bytes(ch, d));
     }
@@ -207,19 +222,31 @@ size_t attn_workspace(int src, int32_t batch, const int32_t* q_lens, const int32
   return most;
 }
 
-int run_attn(int src, AttnArgs base, int32_t batch, const int32_t* q_lens, const int32_t* kv_lens, int32_t d,
+int run_attn(int src, const AttnArgs& base, int32_t batch, const int32_t* q_lens, const int32_t* kv_lens, int32_t d,
              void* workspace, size_t workspace_bytes, hipStream_t stream) {
-  const size_t need = attn_workspace(src, batch, q_lens, kv_lens, base.Hq, base.Hkv, d, base.topk);
-  if (need == 0) return fail(DOSA_ERR_UNSUPPORTED, "too many row tiles and key ranges for one launch");
+  // each kernel's first launch is planned once, for the size check and the run
+  AttnChunk head[2];
+  int next[2];
+  int64_t qr[2] = {0, 0}, kr[2] = {0, 0};
+  const int classes = src == A_BF16 ? 2 : 1;
+  size_t need = 256;
+  for (int tiled = 0; tiled < classes; ++tiled) {
+    head[tiled].a = base;
+    next[tiled] = plan_attn(head[tiled], src, d, tiled != 0, 0, batch, q_lens, kv_lens, base.Hq, base.Hkv, base.topk,
+                            &qr[tiled], &kr[tiled]);
+    if (next[tiled] < 0) return fail(DOSA_ERR_UNSUPPORTED, "too many row tiles and key ranges for one launch");
+    need = std::max(need, part_bytes(head[tiled], d));
+  }
+  if (next[0] < batch || next[classes - 1] < batch) {
+    need = attn_workspace(src, batch, q_lens, kv_lens, base.Hq, base.Hkv, d, base.topk);
+    if (need == 0) return fail(DOSA_ERR_UNSUPPORTED, "too many row tiles and key ranges for one launch");
+  }
   if (workspace == nullptr || workspace_bytes < need || !aligned(workspace, 16))
     return fail(DOSA_ERR_WORKSPACE, "workspace needs " + std::to_string(need) + " bytes, 16-byte aligned");
-  for (int tiled = src == A_BF16 ? 1 : 0; tiled >= 0; --tiled) {
-    int64_t qr = 0, kr = 0;
-    for (int b = 0; b < batch;) {
-      AttnChunk ch;
-      ch.a = base;
-      b = plan_attn(ch, src, tiled != 0, b, batch, q_lens, kv_lens, base.Hq, base.Hkv, base.topk, &qr, &kr);
-      AttnArgs& a = ch.a;
+  for (int tiled = classes - 1; tiled >= 0; --tiled) {
+    AttnChunk& ch = head[tiled];
+    AttnArgs& a = ch.a;
+    for (int b = next[tiled];;) {
       const size_t rows = (size_t)ch.parts * 16 * a.rt;
       a.part_o = static_cast<float*>(workspace);
       a.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + up256(rows * d * sizeof(float)));
@@ -234,6 +261,9 @@ int run_attn(int src, AttnArgs base, int32_t batch, const int32_t* q_lens, const
         e = launch_attn_join(src, d, a, stream);
         if (e != hipSuccess) return fail_hip(e, "attention join launch");
       }
+      if (b >= batch) break;
+      b = plan_attn(ch, src, d, tiled != 0, b, batch, q_lens, kv_lens, base.Hq, base.Hkv, base.topk, &qr[tiled],
+                    &kr[tiled]);
     }
   }
   return DOSA_OK;
@@ -324,10 +354,13 @@ int cache_io(bool write, const dsa_cache* cache, void* k, int64_t k_stride, void
   int64_t row = 0;
   for (int b = 0; b < batch;) {
     a.n_seq = 0;
+    int32_t units = 0;
     for (; b < batch && a.n_seq < kAttnSeqs; ++b) {
-      if (q_lens[b] > 0)
-        a.s[a.n_seq++] = CacheSeq{(int32_t)row, q_lens[b], kv_lens[b] - q_lens[b],
+      if (q_lens[b] > 0) {
+        a.s[a.n_seq++] = CacheSeq{units, (int32_t)row, q_lens[b], kv_lens[b] - q_lens[b],
                                   (seen_lens != nullptr ? seen_lens[b] : kv_lens[b]) - q_lens[b], b};
+        units += (q_lens[b] + kCacheTokens - 1) / kCacheTokens;
+      }
       row += q_lens[b];
     }
     if (a.n_seq == 0) continue;

@@ -49,29 +49,35 @@ struct AttnArgs {
   int64_t q_stride, k_stride, v_stride;   // elements between token rows
   int32_t topk, Hq, Hkv, group;           // group = Hq / Hkv
   float scale;
-  int32_t n_seq, n_units, n_join, rt;     // rt: 16-row tiles per unit
+  int32_t n_seq, n_units, n_join, rt, hp; // rt: 16-row tiles per unit and head, hp: heads per unit
   AttnSeq s[kAttnSeqs];
 };
 
-// 16-row tiles one wavefront may hold (chosen by the host from the row count).
-inline int attn_max_rt(int src) { return src == A_MX32 ? 1 : 2; }
+// 16-row tiles one wavefront may hold: what fits its 256 registers next to the
+// keys in flight (bf16 rows beyond 16 go to the tiled kernel).
+constexpr int attn_max_rt(int src, int d) { return src == A_MX || (src == A_F32 && d == 64) ? 2 : 1; }
 
 // Bf16 prompts over LDS tiles: units are row tiles of kPromptWaves * 32 rows of
 // one kv head, over all their keys.
 constexpr int kPromptWaves = 8;
 hipError_t launch_prompt(int d, const AttnArgs& p, hipStream_t s);
 
+// Heads one wavefront takes together: pairs where the rows of the call are one
+// tile, so that the registers are there.
+constexpr int attn_heads(int src, int rt, int Hkv) { return src == A_MX && rt == 1 && Hkv % 2 == 0 ? 2 : 1; }
 hipError_t launch_attn(int src, int d, const AttnArgs& p, hipStream_t s);
 hipError_t launch_attn_join(int src, int d, const AttnArgs& p, hipStream_t s);
 
 // Cache write and read-back.
 struct CacheSeq {
+  int32_t unit0;      // first workgroup (kCacheTokens tokens each)
   int32_t row0;       // first token row of the packed tokens
   int32_t n;          // tokens
   int32_t pos0;       // logical position of the first
   int32_t seen0;      // value of pos[] of the first
   int32_t b;
 };
+constexpr int kCacheTokens = 16;
 struct CacheIoArgs {
   CacheView cache;
   void* k;            // [total, Hkv, d]
