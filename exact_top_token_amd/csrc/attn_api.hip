@@ -43,6 +43,14 @@ int check_heads(int32_t Hq, int32_t Hkv, int32_t d) {
   return DOSA_OK;
 }
 
+// Rows of a sequence (queries times group heads) are int32 in the kernels.
+int check_row_count(int32_t batch, const int32_t* q_lens, int32_t Hq, int32_t Hkv) {
+  for (int b = 0; b < batch; ++b)
+    if ((int64_t)q_lens[b] * (Hq / Hkv) > (int64_t(1) << 30))
+      return fail(DOSA_ERR_UNSUPPORTED, "sequence " + std::to_string(b) + ": more than 2^30 query rows per kv head");
+  return DOSA_OK;
+}
+
 int check_scale(float scale) {
   if (!(scale > 0.f) || !std::isfinite(scale)) return fail(DOSA_ERR_INVALID_ARG, "scale must be positive and finite");
   return DOSA_OK;
@@ -270,62 +278,123 @@ int run_attn(int src, const AttnArgs& base, int32_t batch, const int32_t* q_lens
 }
 
 // ---------------------------------------------------------------------------
-// Work split of the weights kernel: workgroups per 64-key tile, so that the
-// launch has about kWeightUnits of them and none is left without a row tile.
+// Work split of the weights kernels.
+//   few rows    ranges of keys, as long as 512 workgroups (two a CU) allow,
+//               64..kWeightRowKeys
+//   many rows   512-key chunks x heads x shares of the rows, the shares such
+//               that about kWeightUnits workgroups have work; the causal half
+//               of them has none
+//   any         64-key tiles x shares
 // ---------------------------------------------------------------------------
 constexpr int64_t kWeightUnits = 1024;
 
-int plan_weights(WeightArgs& a, int64_t* parts, int b0, int32_t batch, const int32_t* q_lens, const int32_t* kv_lens,
-                 int32_t Hq, int32_t Hkv, int64_t* q_row) {
+WeightKind weight_kind(bool f32, int64_t rows) {
+  if (rows <= kWeightRows) return WK_ROWS;
+  return f32 ? WK_ANY : WK_TILES;
+}
+
+// The next launch of a kind: sequences from b0 on, at most kAttnSeqs of the
+// kind; floats of partial sums in *floats.  Returns the sequence after the
+// last one seen, or -1 if the launch would be too large.
+int plan_weights(WeightArgs& a, WeightKind kind, bool f32, int64_t* floats, int b0, int32_t batch,
+                 const int32_t* q_lens, const int32_t* kv_lens, int32_t Hq, int32_t Hkv, int64_t* q_row) {
   a.Hq = Hq;
   a.group = Hq / Hkv;
   a.n_seq = 0;
   int b = b0;
-  int64_t work = 0;
+  int64_t work = 0, keys = 0, most = 0;
   for (; b < batch && a.n_seq < kAttnSeqs; ++b) {
-    if (q_lens[b] > 0) {
+    const int64_t rows = (int64_t)q_lens[b] * a.group;
+    if (q_lens[b] > 0 && weight_kind(f32, rows) == kind) {
       WeightSeq& s = a.s[a.n_seq++];
       s = WeightSeq{};
       s.q_row0 = (int32_t)*q_row;
       s.q_len = q_lens[b];
       s.kv_len = kv_lens[b];
       s.b = b;
-      work += ((int64_t)s.kv_len + 63) / 64 * (((int64_t)s.q_len * a.group + 15) / 16 * Hkv);
+      keys += s.kv_len;
+      most = std::max(most, rows);
+      work += ((int64_t)s.kv_len + 63) / 64 * ((rows + 15) / 16 * Hkv);
     }
     *q_row += q_lens[b];
   }
-  std::stable_sort(a.s, a.s + a.n_seq, [](const WeightSeq& x, const WeightSeq& y) { return x.q_len > y.q_len; });
-  int64_t units = 0, tiles = 0;
-  *parts = 0;
-  const int64_t share = std::max<int64_t>(8, (work + kWeightUnits - 1) / kWeightUnits);   // row tiles x heads a workgroup
-  for (int i = 0; i < a.n_seq; ++i) {
-    WeightSeq& s = a.s[i];
-    const int64_t nt = ((int64_t)s.kv_len + 63) / 64;
-    const int64_t w = ((int64_t)s.q_len * a.group + 15) / 16 * Hkv;
-    const int64_t np = std::min<int64_t>(64, std::max<int64_t>(1, w / share));
-    s.n_part = (int32_t)np;
-    s.unit0 = (int32_t)units;
-    s.tile0 = (int32_t)tiles;
-    s.part0 = (int32_t)*parts;
-    units += nt * np;
-    tiles += nt;
-    if (np > 1) *parts += nt * np;
-    if (units > kMaxInt) return -1;
+  *floats = 0;
+  a.n_units = a.n_tiles = 0;
+  if (a.n_seq == 0) return b;
+  std::stable_sort(a.s, a.s + a.n_seq, [](const WeightSeq& x, const WeightSeq& y) {
+    return x.q_len != y.q_len ? x.q_len > y.q_len : x.kv_len > y.kv_len;
+  });
+  int64_t units = 0, tiles = 0, parts = 0;
+  if (kind == WK_ROWS) {
+    a.rt = most > 16 ? 2 : 1;
+    int64_t range = 64;
+    auto count = [&](int64_t r) {
+      int64_t n = 0;
+      for (int i = 0; i < a.n_seq; ++i) n += (a.s[i].kv_len + r - 1) / r;
+      return n;
+    };
+    while (range < kWeightRowKeys && count(range) > 512) range += 64;
+    a.range = (int32_t)range;
+    for (int i = 0; i < a.n_seq; ++i) {
+      a.s[i].unit0 = (int32_t)units;
+      units += (a.s[i].kv_len + range - 1) / range;
+    }
+  } else if (kind == WK_TILES) {
+    for (int i = 0; i < a.n_seq; ++i) {
+      WeightSeq& s = a.s[i];
+      const int64_t rows = (int64_t)s.q_len * a.group, nc = ((int64_t)s.kv_len + kWeightChunk - 1) / kWeightChunk;
+      // shares in proportion to the sequence's part of the work
+      const int64_t w = ((int64_t)s.kv_len + 63) / 64 * ((rows + 15) / 16 * Hkv);
+      const int64_t want = 2 * kWeightUnits * w / std::max<int64_t>(work, 1) / (nc * Hkv);
+      const int64_t np = std::min<int64_t>(std::max<int64_t>(want, 1), (rows + 127) / 128);
+      s.part_rows = (int32_t)(((rows + np - 1) / np + 63) / 64 * 64);
+      s.n_part = (int32_t)((rows + s.part_rows - 1) / s.part_rows);
+      s.unit0 = (int32_t)units;
+      s.tile0 = (int32_t)tiles;
+      s.part0 = (int32_t)parts;
+      units += nc * s.n_part * Hkv;
+      parts += nc * s.n_part * Hkv;
+      tiles += nc * (kWeightChunk / 256);
+      if (units > kMaxInt) return -1;
+    }
+    *floats = parts * kWeightChunk;
+    a.n_tiles = (int32_t)tiles;
+  } else {
+    const int64_t share = std::max<int64_t>(8, (work + kWeightUnits - 1) / kWeightUnits);   // row tiles x heads a workgroup
+    for (int i = 0; i < a.n_seq; ++i) {
+      WeightSeq& s = a.s[i];
+      const int64_t nt = ((int64_t)s.kv_len + 63) / 64;
+      const int64_t w = ((int64_t)s.q_len * a.group + 15) / 16 * Hkv;
+      const int64_t np = std::min<int64_t>(64, std::max<int64_t>(1, w / share));
+      s.n_part = (int32_t)np;
+      s.unit0 = (int32_t)units;
+      s.tile0 = (int32_t)tiles;
+      s.part0 = (int32_t)parts;
+      units += nt * np;
+      tiles += nt;
+      if (np > 1) parts += nt * np;
+      if (units > kMaxInt) return -1;
+    }
+    *floats = parts * 64;
+    a.n_tiles = parts > 0 ? (int32_t)tiles : 0;
   }
+  if (units > kMaxInt) return -1;
   a.n_units = (int32_t)units;
-  a.n_tiles = *parts > 0 ? (int32_t)tiles : 0;
   return b;
 }
 
-size_t weights_workspace(int32_t batch, const int32_t* q_lens, const int32_t* kv_lens, int32_t Hq, int32_t Hkv) {
+size_t weights_workspace(bool f32, int32_t batch, const int32_t* q_lens, const int32_t* kv_lens, int32_t Hq,
+                         int32_t Hkv) {
   size_t most = 256;
-  int64_t qr = 0;
-  for (int b = 0; b < batch;) {
-    WeightArgs a;
-    int64_t parts;
-    b = plan_weights(a, &parts, b, batch, q_lens, kv_lens, Hq, Hkv, &qr);
-    if (b < 0) return 0;
-    most = std::max(most, up256((size_t)parts * 64 * sizeof(float)));
+  for (int kind = 0; kind < WK_KINDS; ++kind) {
+    int64_t qr = 0;
+    for (int b = 0; b < batch;) {
+      WeightArgs a;
+      int64_t floats;
+      b = plan_weights(a, (WeightKind)kind, f32, &floats, b, batch, q_lens, kv_lens, Hq, Hkv, &qr);
+      if (b < 0) return 0;
+      most = std::max(most, up256((size_t)floats * sizeof(float)));
+    }
   }
   return most;
 }
@@ -414,7 +483,8 @@ size_t dsa_prompt_workspace_size(int32_t batch, const int32_t* q_lens, const int
   return guarded_size([&]() -> size_t {
     int64_t tq, tk;
     if (check_lens(batch, q_lens, kv_lens, "q_len", "kv_len", &tq, &tk) != DOSA_OK ||
-        check_heads(Hq, Hkv, d) != DOSA_OK || check_float(dtype) != DOSA_OK)
+        check_heads(Hq, Hkv, d) != DOSA_OK || check_row_count(batch, q_lens, Hq, Hkv) != DOSA_OK ||
+        check_float(dtype) != DOSA_OK)
       return 0;
     return attn_workspace(dtype == DOSA_F32 ? A_F32 : A_BF16, batch, q_lens, kv_lens, Hq, Hkv, d, 0);
   });
@@ -428,6 +498,7 @@ int dsa_prompt_attention(const void* q, int64_t q_stride, const void* k, int64_t
     int64_t tq, tk;
     int st = check_lens(batch, q_lens, kv_lens, "q_len", "kv_len", &tq, &tk);
     if (st == DOSA_OK) st = check_heads(Hq, Hkv, d);
+    if (st == DOSA_OK) st = check_row_count(batch, q_lens, Hq, Hkv);
     if (st == DOSA_OK) st = check_float(dtype);
     if (st == DOSA_OK) st = check_scale(scale);
     if (st == DOSA_OK) st = check_rows("q", q, q_stride, Hq, d, dtype, tq);
@@ -474,7 +545,7 @@ size_t dsa_cache_workspace_size(int32_t batch, const int32_t* q_lens, const int3
   return guarded_size([&]() -> size_t {
     int64_t tq, tk;
     if (check_lens(batch, q_lens, kv_lens, "q_len", "kv_len", &tq, &tk) != DOSA_OK ||
-        check_heads(Hq, Hkv, d) != DOSA_OK)
+        check_heads(Hq, Hkv, d) != DOSA_OK || check_row_count(batch, q_lens, Hq, Hkv) != DOSA_OK)
       return 0;
     if (topk < 0 || topk > (1 << 20)) return 0;
     return std::max(attn_workspace(A_MX, batch, q_lens, kv_lens, Hq, Hkv, d, topk),
@@ -491,6 +562,7 @@ int dsa_cache_attention(const dsa_cache* cache, const void* q, int64_t q_stride,
     int st = check_lens(batch, q_lens, kv_lens, "q_len", "kv_len", &tq, &tk);
     if (st == DOSA_OK) st = check_cache(cache, batch, kv_lens);
     if (st == DOSA_OK) st = check_heads(Hq, cache->Hkv, cache->d);
+    if (st == DOSA_OK) st = check_row_count(batch, q_lens, Hq, cache->Hkv);
     if (st == DOSA_OK) st = check_float(q_dtype);
     if (st == DOSA_OK) st = check_scale(scale);
     if (st == DOSA_OK) st = check_rows("q", q, q_stride, Hq, cache->d, q_dtype, tq);
@@ -520,9 +592,11 @@ size_t dsa_weights_workspace_size(int32_t batch, const int32_t* q_lens, const in
   return guarded_size([&]() -> size_t {
     int64_t tq, tk;
     if (check_lens(batch, q_lens, kv_lens, "q_len", "kv_len", &tq, &tk) != DOSA_OK ||
-        check_heads(Hq, Hkv, d) != DOSA_OK)
+        check_heads(Hq, Hkv, d) != DOSA_OK || check_row_count(batch, q_lens, Hq, Hkv) != DOSA_OK)
       return 0;
-    return weights_workspace(batch, q_lens, kv_lens, Hq, Hkv);
+    const size_t a = weights_workspace(false, batch, q_lens, kv_lens, Hq, Hkv);
+    const size_t b = weights_workspace(true, batch, q_lens, kv_lens, Hq, Hkv);
+    return a == 0 || b == 0 ? 0 : std::max(a, b);
   });
 }
 
@@ -534,39 +608,48 @@ int dsa_cache_weights(const dsa_cache* cache, const void* q, int64_t q_stride, i
     int st = check_lens(batch, q_lens, kv_lens, "q_len", "kv_len", &tq, &tk);
     if (st == DOSA_OK) st = check_cache(cache, batch, kv_lens);
     if (st == DOSA_OK) st = check_heads(Hq, cache->Hkv, cache->d);
+    if (st == DOSA_OK) st = check_row_count(batch, q_lens, Hq, cache->Hkv);
     if (st == DOSA_OK) st = check_float(q_dtype);
     if (st == DOSA_OK) st = check_scale(scale);
     if (st == DOSA_OK) st = check_rows("q", q, q_stride, Hq, cache->d, q_dtype, tq);
     if (st != DOSA_OK) return st;
     if (tq > 0 && (lse == nullptr || acc_out == nullptr)) return fail(DOSA_ERR_INVALID_ARG, "lse or acc_out is NULL");
-    const size_t need = weights_workspace(batch, q_lens, kv_lens, Hq, cache->Hkv);
+    const bool f32 = q_dtype == DOSA_F32;
+    const size_t need = weights_workspace(f32, batch, q_lens, kv_lens, Hq, cache->Hkv);
     if (need == 0) return fail(DOSA_ERR_UNSUPPORTED, "too many key tiles for one launch");
     if (workspace == nullptr || workspace_bytes < need || !aligned(workspace, 16))
       return fail(DOSA_ERR_WORKSPACE, "workspace needs " + std::to_string(need) + " bytes, 16-byte aligned");
-    int64_t qr = 0;
-    for (int b = 0; b < batch;) {
-      WeightArgs a{};
-      int64_t parts;
-      b = plan_weights(a, &parts, b, batch, q_lens, kv_lens, Hq, cache->Hkv, &qr);
-      a.cache = view(cache);
-      a.q = q;
-      a.q_stride = q_stride;
-      a.lse = lse;
-      a.acc = acc;
-      a.acc_out = acc_out;
-      a.part = static_cast<float*>(workspace);
-      a.scale = scale;
-      hipError_t e;
-      {
-        PassScope ps(P_WEIGHTS, static_cast<hipStream_t>(stream));
-        e = launch_weights(q_dtype == DOSA_F32, cache->d, a, static_cast<hipStream_t>(stream));
+    WeightArgs a{};
+    a.cache = view(cache);
+    a.q = q;
+    a.q_stride = q_stride;
+    a.lse = lse;
+    a.acc = acc;
+    a.acc_out = acc_out;
+    a.part = static_cast<float*>(workspace);
+    a.scale = scale;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    for (int k = 0; k < WK_KINDS; ++k) {
+      const WeightKind kind = (WeightKind)k;
+      int64_t qr = 0;
+      for (int b = 0; b < batch;) {
+        int64_t floats;
+        b = plan_weights(a, kind, f32, &floats, b, batch, q_lens, kv_lens, Hq, cache->Hkv, &qr);
+        if (a.n_units == 0) continue;
+        hipError_t e;
+        {
+          PassScope ps(P_WEIGHTS, s);
+          e = kind == WK_ROWS ? launch_weights_rows(f32, cache->d, a, s)
+                              : (kind == WK_TILES ? launch_weights_tiles(cache->d, a, s) : launch_weights(f32, cache->d, a, s));
+        }
+        if (e != hipSuccess) return fail_hip(e, "weights kernel launch");
+        if (a.n_tiles == 0) continue;
+        {
+          PassScope ps(P_WEIGHTS_JOIN, s);
+          e = kind == WK_TILES ? launch_weights_tiles_join(a, s) : launch_weights_join(a, s);
+        }
+        if (e != hipSuccess) return fail_hip(e, "weights join launch");
       }
-      if (e != hipSuccess) return fail_hip(e, "weights kernel launch");
-      {
-        PassScope ps(P_WEIGHTS_JOIN, static_cast<hipStream_t>(stream));
-        e = launch_weights_join(a, static_cast<hipStream_t>(stream));
-      }
-      if (e != hipSuccess) return fail_hip(e, "weights join launch");
     }
     return DOSA_OK;
   });

@@ -90,13 +90,19 @@ struct CacheIoArgs {
 hipError_t launch_cache_append(bool f32, int d, const CacheIoArgs& p, hipStream_t s);
 hipError_t launch_cache_read(bool f32, int d, const CacheIoArgs& p, hipStream_t s);
 
-// Accumulated attention weights.
+// Accumulated attention weights.  Three kernels: few rows (queries times group
+// heads), many bf16 rows, and the rest.
+constexpr int kWeightRows = 32;        // rows of the first
+constexpr int kWeightRowKeys = 1024;   // keys of its workgroup at most
+constexpr int kWeightChunk = 512;      // keys of a workgroup of the second
+enum WeightKind : int { WK_ROWS = 0, WK_TILES = 1, WK_ANY = 2, WK_KINDS = 3 };
 struct WeightSeq {
   int32_t unit0;      // first workgroup
-  int32_t tile0;      // first 64-key tile (of all tiles of the launch)
-  int32_t part0;      // first 64-float partial of the sequence
+  int32_t tile0;      // first workgroup of the join
+  int32_t part0;      // first partial (64 floats; kWeightChunk for WK_TILES)
   int32_t q_row0, q_len, kv_len, b;
-  int32_t n_part;     // workgroups per 64-key tile
+  int32_t n_part;     // shares of a key tile's work
+  int32_t part_rows;  // WK_TILES: rows of a share
 };
 struct WeightArgs {
   CacheView cache;
@@ -104,15 +110,19 @@ struct WeightArgs {
   const float* lse;
   const float* acc;   // or NULL
   float* acc_out;
-  float* part;        // [parts, 64]
+  float* part;
   int64_t q_stride;
   int32_t Hq, group;
   float scale;
   int32_t n_seq, n_units, n_tiles;
+  int32_t range, rt;  // WK_ROWS: keys of a workgroup, 16-row tiles
   WeightSeq s[kAttnSeqs];
 };
 hipError_t launch_weights(bool f32, int d, const WeightArgs& p, hipStream_t s);
 hipError_t launch_weights_join(const WeightArgs& p, hipStream_t s);
+hipError_t launch_weights_rows(bool f32, int d, const WeightArgs& p, hipStream_t s);
+hipError_t launch_weights_tiles(int d, const WeightArgs& p, hipStream_t s);
+hipError_t launch_weights_tiles_join(const WeightArgs& p, hipStream_t s);
 
 // Eviction.
 // A sequence's workspace: the number of moves (in its first kEvictHead ints),
