@@ -126,8 +126,8 @@ hipError_t launch_weights_tiles_join(const WeightArgs& p, hipStream_t s);
 
 // Eviction.
 // A sequence's workspace: the number of moves (in its first kEvictHead ints),
-// the keys that move, the indices they move to (cap of each), and the ranks of
-// the keys beyond the kEvictNear * 1024 that its workgroup keeps in registers.
+// the indices keys move to and then, directly behind, the keys that move (at
+// most cap of each), and the ranks of the keys beyond the kEvictNear * 1024 that its workgroup keeps in registers.
 constexpr int kEvictHead = 16;
 constexpr int kEvictNear = 16;
 struct EvictSeq {

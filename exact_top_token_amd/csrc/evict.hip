@@ -82,23 +82,25 @@ __device__ __forceinline__ void block_scan(int* cnt, int n, int* sh) {
 // threshold, the new_len-th largest rank, is found digit by digit (8 bits)
 // with a histogram of 32 copies, one per LDS bank, so that a lane meets at most
 // one other of its wavefront in a counter however the weights are distributed.
-// Then two prefix sums over the (round, wavefront) counts number the keys that
-// equal the threshold and the keys that move.
+// Then a prefix sum over (round, wavefront) counts numbers, in order of the
+// index, the holes in front of the new end and the keys that move from behind
+// it: as many of one as of the other, holes first, so one list holds both.
+// Only if not all keys that equal the threshold stay does another prefix sum
+// number those.
 // Bound by latency: a few dependent loads and about twenty barriers.
 template <int PER>
 __global__ __launch_bounds__(kThreads) void evict_select_kernel(const EvictArgs p) {
   __shared__ uint32_t hist[256 * 32];
   __shared__ uint32_t tot[256];
   __shared__ int sh[kEvWaves];
-  __shared__ int carry[3];
-  __shared__ uint32_t sel[2];
+  __shared__ int carry[2];
+  __shared__ uint32_t sel[3];
   const EvictSeq& s = p.s[blockIdx.x];
   const int tid = threadIdx.x, lane = lane64(), wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   int32_t* out = p.out_src + (int64_t)s.b * p.out_stride;
   int32_t* ws = p.ws + s.ws_off;
-  int32_t* movers = ws + kEvictHead;
-  int32_t* holes = movers + s.cap;
-  uint32_t* far = reinterpret_cast<uint32_t*>(holes + s.cap);       // ranks of the rounds from PER on
+  int32_t* list = ws + kEvictHead;         // holes, then keys that move
+  uint32_t* far = reinterpret_cast<uint32_t*>(list + 2 * s.cap);    // ranks of the rounds from PER on
   const int rounds = (s.kv_len + kThreads - 1) / kThreads;
   const int near = rounds < PER ? rounds : PER;
   if (s.new_len == 0 || s.new_len == s.kv_len) {       // nothing to choose
@@ -172,6 +174,7 @@ __global__ __launch_bounds__(kThreads) void evict_select_kernel(const EvictArgs 
         for (; j < 3 && before + v[j] < need; ++j) before += v[j];
         sel[0] = pre | ((uint32_t)(255 - (4 * lane + j)) << shift);
         sel[1] = need - before;
+        sel[2] = v[j];                      // keys with this digit
       }
     }
     __syncthreads();
@@ -181,8 +184,10 @@ __global__ __launch_bounds__(kThreads) void evict_select_kernel(const EvictArgs 
 
   // ranks above `pre` stay, and the first `need` equal to it.  64 rounds of
   // 16 wavefronts at a time, the histogram's memory for the counts
-  int* cnt = reinterpret_cast<int*>(hist);          // [64 rounds][16 wavefronts]
-  if (tid < 3) carry[tid] = 0;
+  const bool ties = need < sel[2];
+  int* eqs = reinterpret_cast<int*>(hist);          // [64 rounds][16 wavefronts]
+  int* cnt = eqs + kThreads;
+  if (tid < 2) carry[tid] = 0;
   for (int i0 = 0; i0 < rounds; i0 += 64) {
     const int nr = rounds - i0 < 64 ? rounds - i0 : 64, n = nr * kEvWaves;
     auto rank = [&](int i) -> uint32_t { return far[(i - PER) * kThreads + tid]; };
@@ -210,52 +215,50 @@ __global__ __launch_bounds__(kThreads) void evict_select_kernel(const EvictArgs 
     auto key = [&](int i) { return (i0 + i) * kThreads + tid; };
     const unsigned long long below = (1ull << lane) - 1ull;
     __syncthreads();
+    int eq0 = 0, eq_last = 0;
+    if (ties) {
+      each([&](int i, uint32_t r) {
+        const unsigned long long b = __ballot(key(i) < s.kv_len && r == pre);
+        if (lane == 0) eqs[i * kEvWaves + wave] = __popcll(b);
+      });
+      __syncthreads();
+      eq_last = tid == n - 1 ? eqs[n - 1] : 0;
+      block_scan(eqs, n, sh);
+      eq0 = carry[0];
+    }
+    // a hole in front of the new end, or a key behind it that stays
+    auto listed = [&](int i, uint32_t r) -> bool {
+      const int k = key(i);
+      bool keep = r >= pre;
+      if (ties) {
+        const unsigned long long b = __ballot(k < s.kv_len && r == pre);
+        if (r == pre) keep = eq0 + eqs[i * kEvWaves + wave] + __popcll(b & below) < (int)need;
+      }
+      return k < s.kv_len && keep == (k >= s.new_len);
+    };
     each([&](int i, uint32_t r) {
-      const unsigned long long b = __ballot(key(i) < s.kv_len && r == pre);
+      const unsigned long long b = __ballot(listed(i, r));
       if (lane == 0) cnt[i * kEvWaves + wave] = __popcll(b);
     });
     __syncthreads();
-    int last = tid == n - 1 ? cnt[n - 1] : 0;
+    const int last = tid == n - 1 ? cnt[n - 1] : 0;
     block_scan(cnt, n, sh);
-    const int eq0 = carry[0];
-    auto kept = [&](int i, uint32_t r) -> bool {
-      const unsigned long long b = __ballot(key(i) < s.kv_len && r == pre);
-      const int er = eq0 + cnt[i * kEvWaves + wave] + __popcll(b & below);
-      return key(i) < s.kv_len && (r > pre || (r == pre && er < (int)need));
-    };
-    int* mv = cnt + kThreads;
-    int* ho = mv + kThreads;
+    const int at0 = carry[1];
     each([&](int i, uint32_t r) {
-      const bool k = kept(i, r);
-      const unsigned long long bm = __ballot(k && key(i) >= s.new_len), bh = __ballot(!k && key(i) < s.new_len);
-      if (lane == 0) {
-        mv[i * kEvWaves + wave] = __popcll(bm);
-        ho[i * kEvWaves + wave] = __popcll(bh);
-      }
-    });
-    __syncthreads();
-    const int last_m = tid == n - 1 ? mv[n - 1] : 0, last_h = tid == n - 1 ? ho[n - 1] : 0;
-    block_scan(mv, n, sh);
-    block_scan(ho, n, sh);
-    const int mv0 = carry[1], ho0 = carry[2];
-    each([&](int i, uint32_t r) {
-      const bool k = kept(i, r);
-      const bool im = k && key(i) >= s.new_len, ih = !k && key(i) < s.new_len;
-      const unsigned long long bm = __ballot(im), bh = __ballot(ih);
-      if (im) movers[mv0 + mv[i * kEvWaves + wave] + __popcll(bm & below)] = key(i);
-      if (ih) holes[ho0 + ho[i * kEvWaves + wave] + __popcll(bh & below)] = key(i);
-      if (k && key(i) < s.new_len) out[key(i)] = key(i);
+      const bool f = listed(i, r);
+      const unsigned long long b = __ballot(f);
+      if (f) list[at0 + cnt[i * kEvWaves + wave] + __popcll(b & below)] = key(i);
+      else if (key(i) < s.new_len) out[key(i)] = key(i);
     });
     __syncthreads();
     if (tid == n - 1) {
-      carry[0] = eq0 + cnt[n - 1] + last;
-      carry[1] = mv0 + mv[n - 1] + last_m;
-      carry[2] = ho0 + ho[n - 1] + last_h;
+      if (ties) carry[0] = eq0 + eqs[n - 1] + eq_last;
+      carry[1] = at0 + cnt[n - 1] + last;
     }
     __syncthreads();
   }
-  const int moved = carry[1];
-  for (int i = tid; i < moved; i += kThreads) out[holes[i]] = movers[i];
+  const int moved = carry[1] / 2;
+  for (int i = tid; i < moved; i += kThreads) out[list[i]] = list[moved + i];
   for (int k = s.new_len + tid; k < p.out_stride; k += kThreads) out[k] = -1;
   if (tid == 0) ws[0] = moved;
 }
@@ -295,8 +298,8 @@ __global__ __launch_bounds__(256) void evict_move_kernel(const EvictMoveArgs p) 
     const int j0 = blockIdx.x * kMoveRows, n = min(kMoveRows, ws[0] - j0);
     if (n <= 0) return;
     if (tid < n) {
-      from[tid] = slot(ws[kEvictHead + j0 + tid]);
-      to[tid] = slot(ws[kEvictHead + s.cap + j0 + tid]);
+      to[tid] = slot(ws[kEvictHead + j0 + tid]);
+      from[tid] = slot(ws[kEvictHead + ws[0] + j0 + tid]);
     }
     __syncthreads();
     for (int i = 0; i < p.n_arr; ++i)
