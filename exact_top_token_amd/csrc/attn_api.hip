@@ -16,6 +16,7 @@ using namespace dosa;
 namespace {
 
 constexpr int64_t kMaxInt = (int64_t(1) << 31) - 1;
+constexpr int64_t kMaxTokens = (int64_t(1) << 31) - (1 << 16);   // positions a tile or two ahead stay int32
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
@@ -31,7 +32,7 @@ int check_lens(int32_t batch, const int32_t* a, const int32_t* b, const char* an
     *ta += a[i];
     *tb += b[i];
   }
-  if (*ta > kMaxInt || *tb > kMaxInt) return fail(DOSA_ERR_UNSUPPORTED, "more than 2^31 - 1 tokens in a batch");
+  if (*ta > kMaxTokens || *tb > kMaxTokens) return fail(DOSA_ERR_UNSUPPORTED, "more than 2^31 - 2^16 tokens in a batch");
   return DOSA_OK;
 }
 
@@ -52,7 +53,9 @@ int check_row_count(int32_t batch, const int32_t* q_lens, int32_t Hq, int32_t Hk
 }
 
 int check_scale(float scale) {
-  if (!(scale > 0.f) || !std::isfinite(scale)) return fail(DOSA_ERR_INVALID_ARG, "scale must be positive and finite");
+  // a subnormal scale would be flushed, and 0 times a masked score's -inf is not 0
+  if (!(scale > 0.f) || !std::isnormal(scale))
+    return fail(DOSA_ERR_INVALID_ARG, "scale must be positive, finite and not subnormal");
   return DOSA_OK;
 }
 
@@ -77,7 +80,7 @@ int check_pages(const int32_t* table, int32_t num_pages, int32_t page_size, int3
                 const int32_t* kv_lens) {
   if (page_size <= 0 || page_size % 16 != 0 || num_pages <= 0 || max_pages < 0)
     return fail(DOSA_ERR_INVALID_ARG, "page_size must be a positive multiple of 16, num_pages positive");
-  if ((int64_t)num_pages * page_size > kMaxInt) return fail(DOSA_ERR_UNSUPPORTED, "more than 2^31 - 1 cache slots");
+  if ((int64_t)num_pages * page_size > kMaxTokens) return fail(DOSA_ERR_UNSUPPORTED, "more than 2^31 - 2^16 cache slots");
   for (int b = 0; b < batch; ++b) {
     if (kv_lens[b] > 0 && table == nullptr) return fail(DOSA_ERR_INVALID_ARG, "page_table is NULL");
     if ((int64_t)max_pages * page_size < kv_lens[b])
@@ -115,7 +118,7 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 // ---------------------------------------------------------------------------
 constexpr int64_t kResident = 2048;      // wavefronts at eight a CU
 constexpr int64_t kRounds = 1;
-constexpr int64_t kMinKeys = 128;
+constexpr int64_t kMinKeys = 64;
 
 struct AttnChunk {
   AttnArgs a;
@@ -692,7 +695,7 @@ int dsa_cache_evict(const float* acc, const int32_t* pos, const int32_t* page_ta
       const dsa_evict_array& x = arrays[i];
       if (x.src == nullptr || x.dst == nullptr || x.row_bytes <= 0)
         return fail(DOSA_ERR_INVALID_ARG, "array " + std::to_string(i) + ": NULL pointer or no row bytes");
-      if (x.row_bytes > (1 << 24)) return fail(DOSA_ERR_UNSUPPORTED, "array " + std::to_string(i) + ": rows above 2^24 bytes");
+      if (x.row_bytes > (1 << 20)) return fail(DOSA_ERR_UNSUPPORTED, "array " + std::to_string(i) + ": rows above 2^20 bytes");
       for (int j = 0; j < n_arrays; ++j)
         if (j != i && (arrays[j].dst == x.dst || arrays[j].src == static_cast<const void*>(x.dst)))
           return fail(DOSA_ERR_INVALID_ARG, "array " + std::to_string(i) + " writes where another one reads or writes");

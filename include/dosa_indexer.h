@@ -281,8 +281,9 @@ int dosa_indexer_topk_noalloc(const void* q, int32_t q_dtype, const float* q_sca
  * not change from run to run.
  *
  * Supported: d in {64, 128}; Hkv <= 128, Hq <= 1024, Hq a multiple of Hkv;
- * types DOSA_F32 and DOSA_BF16; fewer than 2^31 tokens in a batch and slots in
- * a cache; token strides up to 2^23 elements.
+ * types DOSA_F32 and DOSA_BF16; at most 2^31 - 2^16 tokens in a batch and slots
+ * in a cache, 2^30 queries times group heads in a sequence; token strides up
+ * to 2^23 elements.  scale is positive, finite and not subnormal.
  */
 
 /* Causal attention of packed sequences over contiguous keys and values.
@@ -312,7 +313,10 @@ int dsa_prompt_attention(const void* q, int64_t q_stride, const void* k, int64_t
  * indexer; page_size is a multiple of 16 (multiples of 64 are read faster) and
  * max_pages * page_size covers every kv_len.  A table entry outside
  * 0..num_pages-1 names no page: its keys are not written and not seen (they
- * read back as zeros).  Slots past a sequence's kv_len may hold anything. */
+ * read back as zeros).  Slots past a sequence's kv_len may hold anything.
+ * Sequences may share pages they only read (dsa_cache_read,
+ * dsa_cache_attention); a call that writes to a page (append, weights,
+ * eviction) must find it in one sequence only. */
 typedef struct {
   void* k_codes;
   void* k_scales;
@@ -382,7 +386,7 @@ typedef struct {
   const void* src;
   void* dst;            /* == src: the rows that change place are copied within it;
                            else every kept row is copied to it */
-  int64_t row_bytes;
+  int64_t row_bytes;    /* 1..2^20 */
 } dsa_evict_array;
 
 /* Keep new_lens[b] of the kv_lens[b] keys of each sequence: those of largest

@@ -62,6 +62,7 @@ def _prompt(**over):
     (dict(scale=-1.0), -1),
     (dict(scale=float("nan")), -1),
     (dict(scale=float("inf")), -1),
+    (dict(scale=1e-40), -1),
     (dict(ws=_space(16)), -3),
 ])
 def test_prompt_refusals(over, status):
@@ -230,6 +231,28 @@ def test_null_pointers_and_reserved_at_the_c_interface():
                                   1 << 12, 1 << 20, None) == -1
     assert L.dsa_prompt_attention(1 << 12, 64, 1 << 12, 64, 1 << 12, 64, 1, one, two, -1, 1, 1, 64, 0.1, 1 << 12, None,
                                   1 << 12, 1 << 20, None) == -1
+
+
+def test_limits_of_32_bit_counts():
+    L = E.lib()
+    big = (1 << 31) - (1 << 16)
+    one = AT._lens([1])
+    # tokens of a batch, slots of a cache, rows of a sequence
+    assert L.dsa_cache_workspace_size(1, one, AT._lens([big]), 8, 8, 64, 0) > 0
+    assert L.dsa_cache_workspace_size(1, one, AT._lens([big + 1]), 8, 8, 64, 0) == 0
+    assert L.dsa_cache_workspace_size(2, AT._lens([1, 1]), AT._lens([big - 5, 6]), 8, 8, 64, 0) == 0
+    n = 1 << 25
+    assert L.dsa_weights_workspace_size(1, AT._lens([n]), AT._lens([n]), 32, 1, 64) > 0
+    assert L.dsa_weights_workspace_size(1, AT._lens([n + 1]), AT._lens([n + 1]), 32, 1, 64) == 0
+    assert L.dsa_prompt_workspace_size(1, AT._lens([n + 1]), AT._lens([n + 1]), 32, 1, 64, 1) == 0
+    s = AT.DsaCache(1 << 12, 1 << 12, 1 << 12, 1 << 12, 1 << 12, (1 << 27) - (1 << 12) + 1, 16, 2, 2, 64, 0)
+    assert L.dsa_cache_append(ctypes.byref(s), 1 << 12, 128, 1 << 12, 128, 0, one, AT._lens([20]), 1, None, None, None) == -2
+    acc = torch.zeros(4, 16)
+    wide = torch.zeros(4, 16, (1 << 20) + 1, dtype=torch.uint8)
+    with pytest.raises(E.DosaError) as ei:
+        E.dsa_cache_evict(acc, torch.zeros(1, 2, dtype=torch.int32), [20], [10], [(wide, wide)],
+                          torch.zeros(1, 10, dtype=torch.int32), workspace=_space(4096), stream=STREAM)
+    assert ei.value.status == -2
 
 
 def test_workspace_sizes():

@@ -483,6 +483,78 @@ def test_evict_very_long():
 
 
 # ----------------------------------------------------------------------------
+# offsets beyond 32 bits
+# ----------------------------------------------------------------------------
+@pytest.mark.parametrize("page", [64, 48])
+def test_cache_slots_beyond_4_gib(page):
+    """A pool of more than 4 GiB a buffer, the sequences' pages at its far end (and one at its start)."""
+    rng = np.random.default_rng(30)
+    hq, hk, d, kl, ql = 8, 8, 128, [200, 90], [3, 1]
+    pages = (9 << 20) // page                       # 9M slots of 512 bytes
+    t = np.full((2, 8), -1, np.int32)
+    per = [-(-k // page) for k in kl]
+    t[0, :per[0]] = pages - 1 - np.arange(per[0])
+    t[1, :per[1]] = pages - 20 - np.arange(per[1])
+    t[1, 0] = 0
+    c = E.Cache.empty(pages, page, hk, d, torch.from_numpy(t).cuda())
+    assert c.k_codes.numel() > 1 << 32
+    k, v = rows(rng, sum(kl), hk, d, "bf16", True), rows(rng, sum(kl), hk, d, "bf16")
+    say("4 GiB cache", page)
+    E.dsa_cache_append(c, k.cuda(), v.cuda(), kl, kl)
+    kb, vb = torch.empty_like(k, device="cuda"), torch.empty_like(v, device="cuda")
+    E.dsa_cache_read(c, kb, vb, kl, kl)
+    torch.cuda.synchronize()
+    val = {n: A.mx_decode(*A.mx_encode(host(x))) for n, x in (("k", k), ("v", v))}
+    assert np.array_equal(host(kb), val["k"]) and np.array_equal(host(vb), val["v"])
+    # the oracle on a small pool with the same rows
+    h = {}
+    for n, x in (("k", k), ("v", v)):
+        h[n + "_codes"], h[n + "_scales"] = (y[None] for y in A.mx_encode(host(x)))
+    h["table"] = np.zeros((2, 1), np.int32)
+    small = {n: np.concatenate([h[n][0][:200], np.zeros((100,) + h[n].shape[2:], np.uint8), h[n][0][200:],
+                                np.zeros((210,) + h[n].shape[2:], np.uint8)]).reshape(2, 300, *h[n].shape[2:])
+             for n in h if n != "table"}
+    small["table"] = np.array([[0], [1]], np.int32)
+    q = rows(rng, sum(ql), hq, d, "bf16")
+    out, lse = run_cache(c, q.cuda(), ql, kl)
+    ref = A.cache_attention(host(q), small, ql, kl, d ** -0.5)
+    check_attention(out, lse, ref, d, 200, True)
+    idx = torch.from_numpy(rng.integers(0, 80, (4, 64)).astype(np.int32))
+    out, lse = run_cache(c, q.cuda(), ql, kl, idx.cuda())
+    check_attention(out, lse, A.cache_attention(host(q), small, ql, kl, d ** -0.5, idx.numpy()), d, 64, True)
+    acc = torch.zeros(pages, page, device="cuda")
+    _, lse = run_cache(c, q.cuda(), ql, kl)
+    E.dsa_cache_weights(c, q.cuda(), lse, ql, kl, None, acc, workspace=space(E.weights_workspace_size(ql, kl, hq, hk, d)))
+    qp = rows(rng, 200, hq, d, "bf16").cuda()       # the prompts' kernel
+    _, lp = run_cache(c, qp, [200, 0], kl)
+    accp = torch.zeros(pages, page, device="cuda")
+    E.dsa_cache_weights(c, qp, lp, [200, 0], kl, None, accp, workspace=space(E.weights_workspace_size([200, 0], kl, hq, hk, d)))
+    torch.cuda.synchronize()
+    for got, r, b in ((acc, ref, 0), (acc, ref, 1), (accp, A.cache_attention(host(qp), small, [200, 0], kl, d ** -0.5), 0)):
+        at = A.slots(t, b, kl[b], page, pages)
+        x = got.view(-1)[torch.from_numpy(at).cuda()].cpu().numpy()
+        want = r[4][b].sum((1, 2))
+        e = float(weight_err(r[3], r[1], d, 200).max()) + 4 * U * float(np.abs(r[1]).max())
+        assert np.all(np.abs(x - want) <= want * (e + 200 * hq * U) + 1e-30)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_prompt_rows_beyond_2_31_elements(dtype):
+    """Token strides of 2^23 elements: the last rows lie past 2^31 elements."""
+    rng = np.random.default_rng(31)
+    stride, n, hq, hk, d = 1 << 23, 290, 4, 2, 64
+    x = torch.empty(stride * (n - 1) + (hq + 2 * hk) * d, dtype=torch.float32 if dtype == "f32" else torch.bfloat16, device="cuda")
+    cut = lambda at, h: x[at:].as_strided((n, h, d), (stride, d, 1))
+    q, k, v = cut(0, hq), cut(hq * d, hk), cut((hq + hk) * d, hk)
+    a, b, c = rows(rng, n, hq, d, dtype), rows(rng, n, hk, d, dtype), rows(rng, n, hk, d, dtype)
+    q.copy_(a), k.copy_(b), v.copy_(c)
+    ql = [30, 260]
+    say("far rows", dtype)
+    out, lse = run_prompt(q, k, v, ql, ql)
+    check_attention(out, lse, A.prompt(host(a), host(b), host(c), ql, ql, d ** -0.5), d, 260, dtype == "bf16")
+
+
+# ----------------------------------------------------------------------------
 # together, as a server uses them
 # ----------------------------------------------------------------------------
 def test_serving_run():
