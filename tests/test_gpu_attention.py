@@ -66,6 +66,18 @@ def test_prompt_long_chunks(dtype):
     check_attention(out, lse, A.prompt(host(q), host(k), host(v), ql, kl, 0.3), 128, max(kl), dtype == "bf16")
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_prompt_chunks_with_joined_ranges(d):
+    """Chunks of more than 16 rows over long keys: the tiled kernel's key ranges joined, row tiles that end
+    inside it, key counts off its tiles, next to sequences of the other kernel."""
+    rng = np.random.default_rng(50 + d)
+    ql, kl = [20, 100, 3, 9], [3001, 4999, 700, 520]
+    q, k, v = (rows(rng, n, h, d, "bf16") for n, h in ((sum(ql), 6), (sum(kl), 2), (sum(kl), 2)))
+    say("prompt joined ranges", d)
+    out, lse = run_prompt(q.cuda(), k.cuda(), v.cuda(), ql, kl)
+    check_attention(out, lse, A.prompt(host(q), host(k), host(v), ql, kl, d ** -0.5), d, max(kl), True)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("d", [64, 128])
 def test_prompt_strided_operands(dtype, d):
@@ -385,6 +397,17 @@ def test_weights_prompt(dtype):
     q = rows(rng, sum(ql), 8, 64, dtype)
     say("weights prompt", dtype)
     check_weights(c, h, q, ql, kl, dtype, "other")
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("bf16", 128), ("f32", 64)])
+def test_weights_prompt_chunks(dtype, d):
+    """Several 512-key chunks, row shares that a chunk's first rows leave empty, odd groups."""
+    rng = np.random.default_rng(60 + d)
+    ql, kl = [600, 40], [1300, 520]
+    c, h = filled_cache(rng, kl, 48 if d == 64 else 64, 2, d)
+    q = rows(rng, sum(ql), 6, d, dtype)
+    say("weights prompt chunks", dtype, d)
+    check_weights(c, h, q, ql, kl, dtype, "in place")
 
 
 def test_weights_bad_pages_and_empty_rows():
