@@ -287,7 +287,7 @@ int run_attn(int src, const AttnArgs& base, int32_t batch, const int32_t* q_lens
 //   many rows   512-key chunks x heads x shares of the rows, the shares such
 //               that about kWeightUnits workgroups have work; the causal half
 //               of them has none
-//   any         64-key tiles x shares
+//   fp32        64-key tiles x shares
 // ---------------------------------------------------------------------------
 constexpr int64_t kWeightUnits = 512;
 
@@ -643,7 +643,7 @@ int dsa_cache_weights(const dsa_cache* cache, const void* q, int64_t q_stride, i
         {
           PassScope ps(P_WEIGHTS, s);
           e = kind == WK_ROWS ? launch_weights_rows(f32, cache->d, a, s)
-                              : (kind == WK_TILES ? launch_weights_tiles(cache->d, a, s) : launch_weights(f32, cache->d, a, s));
+                              : (kind == WK_TILES ? launch_weights_tiles(cache->d, a, s) : launch_weights(cache->d, a, s));
         }
         if (e != hipSuccess) return fail_hip(e, "weights kernel launch");
         if (a.n_tiles == 0) continue;

@@ -91,7 +91,7 @@ hipError_t launch_cache_append(bool f32, int d, const CacheIoArgs& p, hipStream_
 hipError_t launch_cache_read(bool f32, int d, const CacheIoArgs& p, hipStream_t s);
 
 // Accumulated attention weights.  Three kernels: few rows (queries times group
-// heads), many bf16 rows, and the rest.
+// heads), many bf16 rows, many fp32 rows.
 constexpr int kWeightRows = 32;        // rows of the first
 constexpr int kWeightRowKeys = 1024;   // keys of its workgroup at most
 constexpr int kWeightChunk = 512;      // keys of a workgroup of the second
@@ -118,7 +118,7 @@ struct WeightArgs {
   int32_t range, rt;  // WK_ROWS: keys of a workgroup, 16-row tiles
   WeightSeq s[kAttnSeqs];
 };
-hipError_t launch_weights(bool f32, int d, const WeightArgs& p, hipStream_t s);
+hipError_t launch_weights(int d, const WeightArgs& p, hipStream_t s);
 hipError_t launch_weights_join(const WeightArgs& p, hipStream_t s);
 hipError_t launch_weights_rows(bool f32, int d, const WeightArgs& p, hipStream_t s);
 hipError_t launch_weights_tiles(int d, const WeightArgs& p, hipStream_t s);

@@ -8,7 +8,10 @@
 // and 1.75 * 4 = 7.  The codes are the converter's, to nearest with ties to
 // the even code.
 //
-// Bound by memory: 2 (4) bytes in and 17/32 byte out per element.  Four lanes
+// Bound by memory: 2 (4) bytes in and 17/32 byte out per element (42395 tokens
+// of 8 heads, d = 128, bf16: 220 MB in 37-69 us, the longer when the cache in
+// front of the memory is full of someone's writes; read back in fp32, 393 MB in
+// 73 us).  A decode step's 128 tokens take 5 us, latency.  Four lanes
 // share a block, eight elements each: 16-byte loads and 4-byte stores without
 // gaps (fp32: eight lanes of four elements), the block maximum from two lane swaps.
 #include "attn_device.h"

@@ -2,14 +2,17 @@
 //   w_s = sum over queries i that see s and query heads h of exp(scale q_ih . k_s - lse_ih),
 //   acc_out[s] = (acc[s], or 0 for the call's own tokens) + w_s.
 // The normalisers come from an attention call, so one pass suffices and every
-// key is summed by itself: a workgroup owns 64 keys, its wavefronts share the
-// (kv head, query row) work between them, and the sums meet in LDS and, where
-// several workgroups share 64 keys, in a buffer that a second launch adds up
-// in a fixed order.  No atomics: the result does not change from run to run.
+// key is summed by itself: no atomics, and the result does not change from run
+// to run.
 //
-// A wavefront holds the 64 keys of a head as bf16 matrix operands (decoded
-// once), and streams the query rows past them: S^T = K Q^T leaves a lane with
-// one query row and 16 keys, whose weights it adds to 16 running sums.
+// This is the kernel for fp32 queries of more than 32 rows; the others are in
+// weights_tiles.hip.  A workgroup owns 64 keys, its wavefronts share the (kv
+// head, query row) work between them, and the sums meet in LDS and, where
+// several workgroups share 64 keys, in a buffer that a second launch adds up
+// in a fixed order.  A wavefront holds the 64 keys of a head as bf16 matrix
+// operands (decoded once) and streams the query rows past them as three bf16
+// terms each: S^T = K Q^T leaves a lane with one query row and 16 keys, whose
+// weights it adds to 16 running sums.  Bound by the products (three for one).
 #include "attn_device.h"
 
 namespace dosa {
@@ -18,9 +21,9 @@ namespace {
 
 constexpr int kWaves = 8;
 
-template <bool F32, int D>
+template <int D>
 __global__ __launch_bounds__(64 * kWaves) void weights_kernel(const WeightArgs p) {
-  constexpr int NS = D / 32, TERMS = F32 ? 3 : 1;
+  constexpr int NS = D / 32, TERMS = 3;
   __shared__ __attribute__((aligned(16))) uint32_t sc[kWaves][64];
   __shared__ float sums[kWaves][64];
   __shared__ int slots[64];
@@ -87,23 +90,17 @@ __global__ __launch_bounds__(64 * kWaves) void weights_kernel(const WeightArgs p
         const float lc = ok && lse > -INFINITY ? lse * kLog2e : INFINITY;
         b8 qf[TERMS][NS];
         const int64_t at = tok * p.q_stride + (int64_t)qh * D + g * (D / 4);
-        if constexpr (F32) {
-          const f4* src = reinterpret_cast<const f4*>(static_cast<const float*>(p.q) + at);
+        const f4* src = reinterpret_cast<const f4*>(static_cast<const float*>(p.q) + at);
 #pragma unroll
-          for (int s = 0; s < NS; ++s) {
-            const f4 x0 = src[2 * s], x1 = src[2 * s + 1];
+        for (int s = 0; s < NS; ++s) {
+          const f4 x0 = src[2 * s], x1 = src[2 * s + 1];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              float tt[3];
-              split3(e < 4 ? x0[e & 3] : x1[e & 3], tt);
+          for (int e = 0; e < 8; ++e) {
+            float tt[3];
+            split3(e < 4 ? x0[e & 3] : x1[e & 3], tt);
 #pragma unroll
-              for (int k = 0; k < TERMS; ++k) qf[k][s][e] = (__bf16)tt[k];
-            }
+            for (int k = 0; k < TERMS; ++k) qf[k][s][e] = (__bf16)tt[k];
           }
-        } else {
-          const i4* src = reinterpret_cast<const i4*>(static_cast<const uint16_t*>(p.q) + at);
-#pragma unroll
-          for (int s = 0; s < NS; ++s) qf[0][s] = __builtin_bit_cast(b8, src[s]);
         }
         f4 s4[4];
 #pragma unroll
@@ -167,18 +164,14 @@ __global__ __launch_bounds__(64) void weights_join_kernel(const WeightArgs p) {
 
 }  // namespace
 
-hipError_t launch_weights(bool f32, int d, const WeightArgs& p, hipStream_t s) {
-  if (p.n_units == 0) return hipSuccess;
+hipError_t launch_weights(int d, const WeightArgs& p, hipStream_t s) {
   const dim3 grid((unsigned)p.n_units), block(64 * kWaves);
-  if (f32 && d == 128) weights_kernel<true, 128><<<grid, block, 0, s>>>(p);
-  else if (f32) weights_kernel<true, 64><<<grid, block, 0, s>>>(p);
-  else if (d == 128) weights_kernel<false, 128><<<grid, block, 0, s>>>(p);
-  else weights_kernel<false, 64><<<grid, block, 0, s>>>(p);
+  if (d == 128) weights_kernel<128><<<grid, block, 0, s>>>(p);
+  else weights_kernel<64><<<grid, block, 0, s>>>(p);
   return hipGetLastError();
 }
 
 hipError_t launch_weights_join(const WeightArgs& p, hipStream_t s) {
-  if (p.n_tiles == 0) return hipSuccess;
   weights_join_kernel<<<dim3((unsigned)p.n_tiles), dim3(64), 0, s>>>(p);
   return hipGetLastError();
 }

@@ -87,7 +87,9 @@ __device__ __forceinline__ void block_scan(int* cnt, int n, int* sh) {
 // it: as many of one as of the other, holes first, so one list holds both.
 // Only if not all keys that equal the threshold stay does another prefix sum
 // number those.
-// Bound by latency: a few dependent loads and about twenty barriers.
+// Bound by latency for short sequences (16 of 4160 keys: 15 us, a few dependent
+// loads and about twenty barriers), by the one CU's instructions for long ones
+// (4 of up to 65536 keys: 85 us).
 template <int PER>
 __global__ __launch_bounds__(kThreads) void evict_select_kernel(const EvictArgs p) {
   __shared__ uint32_t hist[256 * 32];
@@ -285,7 +287,9 @@ __device__ __forceinline__ void copy_any(const EvictArray& a, const int* from, c
 }
 
 // Workgroups 0..in_blocks-1 of a sequence: the moves of the arrays in place;
-// the others: every kept row of the arrays that go elsewhere.
+// the others: every kept row of the arrays that go elsewhere.  4 KB a key in
+// two arrays: 64 moves in each of 16 sequences 6 us, 16 thousand moves 24 us
+// (5.3 TB/s).
 constexpr int kCopyRows = 256;
 
 __global__ __launch_bounds__(256) void evict_move_kernel(const EvictMoveArgs p) {

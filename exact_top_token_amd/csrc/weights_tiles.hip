@@ -5,14 +5,18 @@
 // Its wavefronts hold the query rows of a kv head (or of a pair, whose 64-byte
 // key rows share a line) and stream the keys, S = Q K^T: a lane then has four
 // rows of one key, adds their weights, and the four lane groups meet in two
-// swaps.  Bound by the key rows' bytes.
+// swaps.  Bound by the key rows' bytes: 16 sequences, 288K cached keys of 8
+// heads, 159 MB in 37 us.
 //
 // Many bf16 rows (a prompt): a wavefront holds 64 keys of a head as matrix
 // operands, eight of them make 512 keys, and the query rows go past them in
 // LDS tiles of 64 rows loaded one ahead, S^T = K Q^T on the 32x32x16 product:
 // a lane has one row and adds the weights of 32 keys, one normaliser a lane.
 // Bound by the exponentials (quarter rate) next to the product: 64 keys x 32
-// rows are 16 products of 32 cycles and 32 x 24 vector cycles.
+// rows are 16 products of 32 cycles and 32 x 24 vector cycles.  Prompts of 8192
+// and 1031 queries, 32 heads on 8: 0.45 ms, 650 TFLOP/s.  Computing a block's
+// weights under the next block's scores, or four row tiles in flight, did not
+// change that (0.48 and 0.50 ms).
 #include "attn_device.h"
 
 namespace dosa {
