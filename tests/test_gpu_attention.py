@@ -506,6 +506,68 @@ def test_evict_very_long():
 
 
 # ----------------------------------------------------------------------------
+# shapes the kernels divide differently
+# ----------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("hq,hk,page,ql,kl", [
+    (48, 24, 64, [1, 2], [200, 70]),       # more head pairs than wavefronts
+    (22, 11, 16, [2], [150]),              # an odd number of kv heads, more than wavefronts
+    (8, 2, 64, [150, 1], [400, 65]),       # a chunk of a prompt over the cache
+    (24, 1, 48, [3], [210]),               # all heads on one, rows beyond one tile
+])
+def test_cache_attention_and_weights_of_other_shapes(dtype, hq, hk, page, ql, kl):
+    rng = np.random.default_rng(hq * hk)
+    for d in (64, 128):
+        c, h = filled_cache(rng, kl, page, hk, d)
+        q = rows(rng, sum(ql), hq, d, dtype)
+        say("other shapes", dtype, d, hq, hk, page, ql, kl)
+        out, lse = run_cache(c, q.cuda(), ql, kl)
+        check_attention(out, lse, A.cache_attention(host(q), h, ql, kl, d ** -0.5), d, max(kl), dtype == "bf16")
+        idx = rng.integers(-1, min(kl), (sum(ql), 70)).astype(np.int32)
+        out, lse = run_cache(c, q.cuda(), ql, kl, torch.from_numpy(idx).cuda())
+        check_attention(out, lse, A.cache_attention(host(q), h, ql, kl, d ** -0.5, idx), d, 70, dtype == "bf16")
+        check_weights(c, h, q, ql, kl, dtype, "other")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_cache_calls_with_strided_queries_on_another_stream(dtype):
+    """Queries as a slice of a fused projection, calls on the stream that is current."""
+    rng = np.random.default_rng(70)
+    ql, kl, hq, hk, d = [2, 40], [300, 100], 4, 2, 64
+    c, h = filled_cache(rng, kl, 64, hk, d)
+    q = rows(rng, sum(ql), hq + 3, d, dtype).cuda()[:, 1:1 + hq]
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    say("strided queries", dtype)
+    with torch.cuda.stream(s):
+        out, lse = run_cache(c, q, ql, kl)
+        ref = A.cache_attention(host(q), h, ql, kl, d ** -0.5)
+        check_attention(out, lse, ref, d, max(kl), dtype == "bf16")
+        acc = torch.zeros(c.num_pages, c.page_size, device="cuda")
+        E.dsa_cache_weights(c, q, lse, ql, kl, None, acc, workspace=space(E.weights_workspace_size(ql, kl, hq, hk, d)))
+    s.synchronize()
+    want = A.accumulate(h, ref[4], ql, kl, None, np.zeros((c.num_pages, c.page_size)))
+    e = float(weight_err(ref[3], ref[1], d, max(kl)).max()) * 3
+    assert np.all(np.abs(acc.cpu().numpy() - want) <= (np.abs(want) + 1e-30) * (e + max(ql) * hq * U * 2))
+
+
+def test_append_many_sequences():
+    rng = np.random.default_rng(71)
+    kl = [int(x) for x in rng.integers(0, 60, 150)]
+    ql = [int(rng.integers(0, k + 1)) for k in kl]
+    t, pages = table(rng, kl, 16)
+    c = E.Cache.empty(pages, 16, 2, 64, torch.from_numpy(t).cuda())
+    x = rows(rng, sum(ql), 2, 64, "bf16", True).cuda()
+    say("append many")
+    E.dsa_cache_append(c, x, x, ql, kl)
+    k, v = torch.empty_like(x), torch.empty_like(x)
+    E.dsa_cache_read(c, k, v, ql, kl)
+    torch.cuda.synchronize()
+    want = A.mx_decode(*A.mx_encode(host(x)))
+    assert np.array_equal(host(k), want) and np.array_equal(host(v), want)
+
+
+# ----------------------------------------------------------------------------
 # offsets beyond 32 bits
 # ----------------------------------------------------------------------------
 @pytest.mark.parametrize("page", [64, 48])
