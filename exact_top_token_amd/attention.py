@@ -57,15 +57,17 @@ def declare(L) -> None:
         fn.argtypes, fn.restype = args, res
 
 
-_loaded = None
+_loaded = _torch = None
 
 
 def _lib():
-    global _loaded
+    global _loaded, _torch
     if _loaded is None:
+        import torch
+
         from . import lib
 
-        _loaded = lib()
+        _loaded, _torch = lib(), torch
     return _loaded
 
 
@@ -118,13 +120,13 @@ def _size(n: int, what: str) -> int:
 
 def _rows(t, name: str, heads: int, d: int, tokens: int, like, contiguous: bool = False) -> int:
     """Token stride of a packed operand [tokens, heads, d] of `like`'s type and device."""
-    if t.dim() != 3 or tuple(t.shape) != (tokens, heads, d):
+    if t.shape != (tokens, heads, d):
         _bad(f"{name} must be [{tokens}, {heads}, {d}], is {list(t.shape)}")
     if t.dtype != like.dtype or t.device != like.device:
         _bad(f"{name} must be {like.dtype} on {like.device}, is {t.dtype} on {t.device}")
-    s = t.stride()
     if tokens == 0:
         return heads * d
+    s = t.stride()
     if (s[2] != 1 and d > 1) or (heads > 1 and s[1] != d):
         _bad(f"{name}: the heads of a token must lie together")
     if tokens == 1:
@@ -138,7 +140,7 @@ def _tensor(t, name: str, dtype, shape, device) -> Optional[int]:
     """Address of a contiguous tensor of the given type, shape and device."""
     if t is None:
         return None
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != device:
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != device:
         _bad(f"{name} must be a contiguous {dtype} {list(shape)} on {device}, is {t.dtype} {list(t.shape)} on {t.device}")
     return t.data_ptr()
 
@@ -160,8 +162,7 @@ class _On:
         self.device, self.stream, self.back = device, stream, None
 
     def __enter__(self) -> int:
-        import torch
-
+        torch = _torch
         if self.device.type != "cuda":
             _bad(f"tensors are on {self.device}, not on a GPU")
         if torch.cuda.current_device() != self.device.index:
@@ -231,8 +232,7 @@ def dsa_prompt_attention(q, k, v, q_lens, kv_lens, out, lse=None, scale: Optiona
                          stream=None):
     """Causal attention of packed sequences: q, out [total_q, Hq, d], k, v [total_k, Hkv, d], lse
     [total_q, Hq] fp32 or None; scale defaults to d ** -0.5."""
-    import torch
-
+    L, torch = _lib(), _torch
     if q.dim() != 3 or k.dim() != 3:
         _bad("q and k must be [tokens, heads, d]")
     if len(q_lens) != len(kv_lens):
@@ -244,7 +244,7 @@ def dsa_prompt_attention(q, k, v, q_lens, kv_lens, out, lse=None, scale: Optiona
     plse = _tensor(lse, "lse", torch.float32, (nq, hq), q.device)
     ws, n = _space(workspace, q.device)
     with _on(q.device, stream) as st:
-        _check(_lib().dsa_prompt_attention(q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv, _code(q.dtype, "q"),
+        _check(L.dsa_prompt_attention(q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv, _code(q.dtype, "q"),
                                            _lens(q_lens), _lens(kv_lens), len(q_lens), hq, hk, d,
                                            d ** -0.5 if scale is None else scale, out.data_ptr(), plse, ws, n, st))
 
@@ -263,12 +263,11 @@ def _io(fn, cache, k, v, q_lens, kv_lens, extra, stream):
 def dsa_cache_append(cache: Cache, k, v, q_lens, kv_lens, pos=None, seen_lens=None, stream=None):
     """Quantise the newest q_lens[b] tokens of each sequence, k, v [total_q, Hkv, d], into the cache; pos
     int32 [num_pages, page_size] gets their places in the text."""
-    import torch
-
+    L, torch = _lib(), _torch
     p = _tensor(pos, "pos", torch.int32, (cache.num_pages, cache.page_size), cache.device)
     if seen_lens is not None and len(seen_lens) != len(kv_lens):
         _bad("seen_lens and kv_lens differ in length")
-    _io(_lib().dsa_cache_append, cache, k, v, q_lens, kv_lens, (p, None if seen_lens is None else _lens(seen_lens)), stream)
+    _io(L.dsa_cache_append, cache, k, v, q_lens, kv_lens, (p, None if seen_lens is None else _lens(seen_lens)), stream)
 
 
 def dsa_cache_read(cache: Cache, k, v, q_lens, kv_lens, stream=None):
@@ -285,8 +284,7 @@ def dsa_cache_attention(cache: Cache, q, q_lens, kv_lens, out, lse=None, idx=Non
                         workspace=None, stream=None):
     """Attention over the cache: q, out [total_q, Hq, d]; idx int32 [total_q, topk] restricts each query
     to the keys it lists (an indexer's out_idx)."""
-    import torch
-
+    L, torch = _lib(), _torch
     n = cache._batch(q_lens, kv_lens)
     nq = sum(q_lens)
     if q.dim() != 3 or q.device != cache.device:
@@ -305,7 +303,7 @@ def dsa_cache_attention(cache: Cache, q, q_lens, kv_lens, out, lse=None, idx=Non
         return
     ws, nb = _space(workspace, q.device)
     with _on(q.device, stream) as st:
-        _check(_lib().dsa_cache_attention(ctypes.byref(cache.struct), q.data_ptr(), sq, _code(q.dtype, "q"),
+        _check(L.dsa_cache_attention(ctypes.byref(cache.struct), q.data_ptr(), sq, _code(q.dtype, "q"),
                                           _lens(q_lens), _lens(kv_lens), n, hq, pidx, topk,
                                           cache.d ** -0.5 if scale is None else scale, out.data_ptr(), plse, ws, nb, st))
 
@@ -319,8 +317,7 @@ def dsa_cache_weights(cache: Cache, q, lse, q_lens, kv_lens, acc, acc_out, scale
                       workspace=None, stream=None):
     """acc_out = acc (0 for the call's own tokens; None: 0) + the weight each key received from the
     queries whose normalisers are lse; acc, acc_out fp32 [num_pages, page_size]."""
-    import torch
-
+    L, torch = _lib(), _torch
     n = cache._batch(q_lens, kv_lens)
     nq = sum(q_lens)
     if q.dim() != 3 or q.device != cache.device:
@@ -333,7 +330,7 @@ def dsa_cache_weights(cache: Cache, q, lse, q_lens, kv_lens, acc, acc_out, scale
     po = _tensor(acc_out, "acc_out", torch.float32, shape, q.device)
     ws, nb = _space(workspace, q.device)
     with _on(q.device, stream) as st:
-        _check(_lib().dsa_cache_weights(ctypes.byref(cache.struct), q.data_ptr(), sq, _code(q.dtype, "q"), plse,
+        _check(L.dsa_cache_weights(ctypes.byref(cache.struct), q.data_ptr(), sq, _code(q.dtype, "q"), plse,
                                         _lens(q_lens), _lens(kv_lens), n, hq,
                                         cache.d ** -0.5 if scale is None else scale, pa, po, ws, nb, st))
 
@@ -347,8 +344,7 @@ def dsa_cache_evict(acc, page_table, kv_lens, new_lens, arrays, out_src, pos=Non
     """Keep the new_lens[b] keys of largest acc of each sequence and move the rows of ``arrays``, (src, dst)
     pairs of contiguous tensors [num_pages, page_size, ...] (dst may be src); out_src int32 [batch, >= new_len]
     gets the index each kept key came from."""
-    import torch
-
+    L, torch = _lib(), _torch
     if acc.dim() != 2 or page_table.dim() != 2 or out_src.dim() != 2:
         _bad("acc must be [num_pages, page_size], page_table [batch, max_pages], out_src [batch, n]")
     n = len(kv_lens)
@@ -370,6 +366,6 @@ def dsa_cache_evict(acc, page_table, kv_lens, new_lens, arrays, out_src, pos=Non
         recs[i] = DsaEvictArray(a.data_ptr(), b.data_ptr(), a[0, 0].numel() * a.element_size() if a.numel() else 0)
     ws, nb = _space(workspace, dev)
     with _on(dev, stream) as st:
-        _check(_lib().dsa_cache_evict(pacc, ppos, ptab, acc.shape[1], page_table.shape[1], acc.shape[0], _lens(kv_lens),
+        _check(L.dsa_cache_evict(pacc, ppos, ptab, acc.shape[1], page_table.shape[1], acc.shape[0], _lens(kv_lens),
                                       _lens(new_lens), None if seen_lens is None else _lens(seen_lens), n, prefix, window,
                                       recs, len(arrays), psrc, out_src.shape[1], ws, nb, st))
