@@ -289,7 +289,7 @@ int run_attn(int src, const AttnArgs& base, int32_t batch, const int32_t* q_lens
 //               of them has none
 //   fp32        64-key tiles x shares
 // ---------------------------------------------------------------------------
-constexpr int64_t kWeightUnits = 512;
+constexpr int64_t kWeightUnits = 2048;
 
 WeightKind weight_kind(bool f32, int64_t rows) {
   if (rows <= kWeightRows) return WK_ROWS;

@@ -14,9 +14,10 @@
 // a lane has one row and adds the weights of 32 keys, one normaliser a lane.
 // Bound by the exponentials (quarter rate) next to the product: 64 keys x 32
 // rows are 16 products of 32 cycles and 32 x 24 vector cycles.  Prompts of 8192
-// and 1031 queries, 32 heads on 8: 0.45 ms, 650 TFLOP/s.  Computing a block's
-// weights under the next block's scores, or four row tiles in flight, did not
-// change that (0.48 and 0.50 ms).
+// and 1031 queries, 32 heads on 8: 0.39 ms, 760 TFLOP/s.  The chunks' work is
+// uneven (the causal mask), so the rows are cut into more shares than the GPU
+// holds at once: 0.46 ms with a quarter of them.  Computing a block's weights
+// under the next block's scores, or four row tiles in flight, did not help.
 #include "attn_device.h"
 
 namespace dosa {
@@ -204,6 +205,22 @@ __device__ __forceinline__ f16v mfma32(b8 a, b8 b, f16v c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
 
+// Sum over the 32 lanes of a half, in every lane: rotations within 16 lanes,
+// then a swap of the neighbouring 16.
+template <int N>
+__device__ __forceinline__ float add_rotated(float x) {
+  return x + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x120 + N, 0xf, 0xf, false));
+}
+__device__ __forceinline__ float sum_half(float x) {
+  x = add_rotated<8>(x);
+  x = add_rotated<4>(x);
+  x = add_rotated<2>(x);
+  x = add_rotated<1>(x);
+  const uint32_t u = __float_as_uint(x);
+  auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
 constexpr int kRowTile = 64;
 
 template <int D>
@@ -259,11 +276,10 @@ __global__ __launch_bounds__(64 * kWaves) void weights_tiles_kernel(const Weight
 #pragma unroll
       for (int e = 0; e < 4; ++e) w[4 * x + e] = (uint32_t)y[e];
     }
+    uint32_t by = D == 128 ? *reinterpret_cast<const uint16_t*>(sr) : (uint32_t)*sr;
+    by = sl < 0 ? 0u : by;
 #pragma unroll
-    for (int s = 0; s < NS; ++s) {
-      const uint32_t e = sl < 0 ? 0u : sr[s / 4];
-      kf[a][s] = mx8(w[s], __uint_as_float(e << 23));
-    }
+    for (int s = 0; s < NS; ++s) kf[a][s] = mx8(w[s], mx_scale(by, 8 * (s / 4)));
   }
   f16v acc[2];
 #pragma unroll
@@ -335,18 +351,20 @@ __global__ __launch_bounds__(64 * kWaves) void weights_tiles_kernel(const Weight
     }
     buf ^= 1;
   }
-  // sum over the 32 rows' lanes; lane 0 and 32 hold the keys of their half
+  // sum over the 32 rows' lanes (all of them get it); lane n then writes the
+  // n-th of the 16 keys its half holds of each 32
   if (!active) return;
   float* out = p.part + ((int64_t)sq.part0 + (((int64_t)chunk * sq.n_part + part) * cv.Hkv + head)) * kWeightChunk + 64 * wave;
 #pragma unroll
-  for (int a = 0; a < 2; ++a)
+  for (int a = 0; a < 2; ++a) {
+    float mine = 0.f;
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
-      float x = acc[a][e];
-#pragma unroll
-      for (int m = 1; m < 32; m <<= 1) x += __shfl_xor(x, m);
-      if (n == 0) out[32 * a + 8 * (e >> 2) + 4 * h + (e & 3)] = x;
+      const float x = sum_half(acc[a][e]);
+      mine = n == e ? x : mine;
     }
+    if (n < 16) out[32 * a + 8 * (n >> 2) + 4 * h + (n & 3)] = mine;
+  }
 }
 
 // Adds up the parts and heads of each key, in order.
@@ -357,14 +375,19 @@ __global__ __launch_bounds__(256) void weights_tiles_join_kernel(const WeightArg
   const int in = b % (kWeightChunk / 256) * 256 + (int)threadIdx.x, key = chunk * kWeightChunk + in;
   if (key >= sq.kv_len) return;
   const int sl = cache_slot(cv.table, sq.b, cv.max_pages, cv.page_size, cv.num_pages, key);
+  // the chunk's shares with work are the last ones, from the one that holds
+  // its first visible row on; theirs and their heads' sums lie one after another
+  const int before = sq.kv_len - sq.q_len, key0 = chunk * kWeightChunk;
+  const int64_t seen = (int64_t)(key0 > before ? key0 - before : 0) * p.group;
+  const int first = (int)(seen / sq.part_rows), n = (sq.n_part - first) * cv.Hkv;
+  const float* src = p.part + ((int64_t)sq.part0 + ((int64_t)chunk * sq.n_part + first) * cv.Hkv) * kWeightChunk + in;
   float x = 0.f;
-  for (int i = 0; i < sq.n_part; ++i) {
-    int r0, r1;
-    part_rows(p, sq, chunk, i, &r0, &r1);
-    if (r0 >= r1) continue;
-    const float* src = p.part + ((int64_t)sq.part0 + ((int64_t)chunk * sq.n_part + i) * cv.Hkv) * kWeightChunk + in;
-#pragma unroll 8
-    for (int hd = 0; hd < cv.Hkv; ++hd) x += src[(int64_t)hd * kWeightChunk];
+  for (int i = 0; i < n; i += 32) {
+    float v[32];
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = src[(int64_t)(i + j < n ? i + j : n - 1) * kWeightChunk];
+#pragma unroll
+    for (int j = 0; j < 32; ++j) x += i + j < n ? v[j] : 0.f;
   }
   if (sl >= 0) p.acc_out[sl] = (key < sq.kv_len - sq.q_len && p.acc != nullptr ? p.acc[sl] : 0.f) + x;
 }
