@@ -348,7 +348,7 @@ int plan_weights(WeightArgs& a, WeightKind kind, bool f32, int64_t* floats, int 
       const int64_t rows = (int64_t)s.q_len * a.group, nc = ((int64_t)s.kv_len + kWeightChunk - 1) / kWeightChunk;
       // shares in proportion to the sequence's part of the work
       const int64_t w = ((int64_t)s.kv_len + 63) / 64 * ((rows + 15) / 16 * Hkv);
-      const int64_t want = 2 * kWeightUnits * w / std::max<int64_t>(work, 1) / (nc * Hkv);
+      const int64_t want = w / std::max<int64_t>(work / (2 * kWeightUnits), 1) / (nc * Hkv);
       const int64_t np = std::min<int64_t>(std::max<int64_t>(want, 1), (rows + 127) / 128);
       s.part_rows = (int32_t)(((rows + np - 1) / np + 63) / 64 * 64);
       s.n_part = (int32_t)((rows + s.part_rows - 1) / s.part_rows);
