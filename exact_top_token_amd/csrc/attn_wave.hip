@@ -61,7 +61,7 @@ struct MxStage {
   uint32_t v[HP][4 * KT];   // per head and key 16t+4g+r: dims [n D/16, (n+1) D/16)
   uint32_t ks, vs;          // scale bytes of key l % (16 KT), head l / (16 KT)
   uint32_t mask;            // bit 4t+r: key 16t+4g+r is not there
-  bool gone;                // key l % (16 KT) is not there (W_PAGES, W_SEL)
+  bool gone;                // key l % (16 KT) is not there (W_RUN: the step's page names none)
 };
 template <int D, int HP>
 struct Stage<A_MX, D, HP> : MxStage<D, HP> {};
@@ -246,9 +246,11 @@ __global__ __launch_bounds__(64 * kWaves) void attn_kernel(const AttnArgs p) {
         // scalar bases, one lane offset per kind, scalar row offsets
         const Rows k1 = rows_at(kb + slot * row_b), v1 = rows_at(vb + slot * row_b);
         const Rows ks1 = rows_at(ksb + slot * row_s), vs1 = rows_at(vsb + slot * row_s);
-        // the scales of keys past the range become zero bytes, which keeps
-        // whatever their slots hold finite
+        // the scales of keys past the range and of a step without a page (which
+        // reads page 0) become zero bytes, which keeps whatever their slots hold
+        // finite: a masked key's weight of 0 is still multiplied by its values
         st.mask = bad ? 0xffffu : 0u;
+        st.gone = bad;
         if constexpr (D == 128) {
           st.ks = __builtin_amdgcn_raw_buffer_load_b32(ks1, s_off, 0, 0);
           st.vs = __builtin_amdgcn_raw_buffer_load_b32(vs1, s_off, 0, 0);
@@ -377,7 +379,7 @@ __global__ __launch_bounds__(64 * kWaves) void attn_kernel(const AttnArgs p) {
     f4 vscale[HP][KT];
     if constexpr (MX) {
       wave_sync();
-      const bool in = WALK == W_RUN ? key0 + s_key < key_hi : !st.gone;
+      const bool in = !st.gone && (WALK != W_RUN || key0 + s_key < key_hi);
       lds[wave][0][lane] = in ? st.ks : 0u;
       lds[wave][1][lane] = in ? st.vs : 0u;
       wave_sync();

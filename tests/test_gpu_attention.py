@@ -830,3 +830,58 @@ def test_pass_times_are_reported():
     run_cache(c, q, ql, kl)
     t = E.profile_end()
     assert t["cache_attention"][0] == 1 and t["attention_join"][0] == 1
+
+
+# ----------------------------------------------------------------------------
+# table entries without a page, and a first page that holds nothing
+# ----------------------------------------------------------------------------
+def without_first_page(c, h):
+    """The cache with its first page in no table row and full of 0xFF: its rows move to a spare page."""
+    t = h["table"].copy()
+    used = set(t[(t >= 0) & (t < c.num_pages)].tolist())
+    spare = max(set(range(c.num_pages)) - used)
+    assert spare > 0
+    t[t == 0] = spare
+    for n in ("k_codes", "k_scales", "v_codes", "v_scales"):
+        if 0 in used:
+            h[n][spare] = h[n][0]
+        h[n][0] = 0xFF
+        getattr(c, n).copy_(torch.from_numpy(h[n]))
+    h["table"] = t
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hq,hk,page,ql,kl", [
+    (4, 2, 16, [2, 1, 3], [300, 60, 129]),
+    (4, 2, 64, [2, 1, 3], [300, 60, 129]),
+    (3, 3, 64, [2, 1, 3], [300, 60, 129]),
+    (4, 2, 128, [2, 1, 3], [300, 60, 129]),
+    (16, 8, 64, [1] * 60, [600, 60] * 30),       # ranges longer than a page: head pairs,
+    (9, 9, 64, [1] * 60, [600, 60] * 30),        # single heads,
+    (16, 8, 64, [1] * 7 + [80], [600, 60] * 3 + [130, 2400]),      # two row tiles
+    (9, 9, 128, [80, 1], [2400, 100]),
+])
+def test_cache_attention_missing_pages_next_to_an_unused_one(dtype, d, hq, hk, page, ql, kl):
+    """Nothing of a page that no table entry names reaches a result, whatever its bytes: neither the rows of
+    a query that sees other keys nor those of one that sees none."""
+    rng = np.random.default_rng(80 + hk)
+    c, h = filled_cache(rng, kl, page, hk, d)
+    without_first_page(c, h)
+    t = h["table"]
+    for b, n in enumerate(kl):
+        last = (n - 1) // page
+        if b % 3 == 1:
+            t[b] = -1 - b                                # every page gone
+        elif last > 0:
+            t[b, last // 2] = (-1, c.num_pages)[b & 1]   # one inside
+            if b % 3 == 2:
+                t[b, 0] = 1 << 20                        # and the first
+    c = E.Cache(c.k_codes, c.k_scales, c.v_codes, c.v_scales, torch.from_numpy(t).cuda())
+    q = rows(rng, sum(ql), hq, d, dtype)
+    say("missing pages", dtype, d, hq, hk, page, ql[-1], kl[-1])
+    out, lse = run_cache(c, q.cuda(), ql, kl)
+    ref = A.cache_attention(host(q), h, ql, kl, d ** -0.5)
+    assert np.any(~np.isfinite(ref[1])) and np.any(np.isfinite(ref[1]))
+    check_attention(out, lse, ref, d, max(kl), dtype == "bf16")
+    check_weights(c, h, q, ql, kl, dtype, "other")
