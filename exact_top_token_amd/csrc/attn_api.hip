@@ -53,9 +53,11 @@ int check_row_count(int32_t batch, const int32_t* q_lens, int32_t Hq, int32_t Hk
 }
 
 int check_scale(float scale) {
-  // a subnormal scale would be flushed, and 0 times a masked score's -inf is not 0
-  if (!(scale > 0.f) || !std::isnormal(scale))
-    return fail(DOSA_ERR_INVALID_ARG, "scale must be positive, finite and not subnormal");
+  // a subnormal scale would be flushed, and 0 times a masked score's -inf is not
+  // 0; the kernels multiply by scale * log2(e), and infinity times an equal
+  // maximum's difference of 0 is not 0 either
+  if (!(scale > 0.f) || !std::isnormal(scale) || !std::isfinite(scale * 1.44269504f))
+    return fail(DOSA_ERR_INVALID_ARG, "scale must be positive, not subnormal, and scale * log2(e) finite in fp32");
   return DOSA_OK;
 }
 

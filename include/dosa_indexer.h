@@ -274,16 +274,20 @@ int dosa_indexer_topk_noalloc(const void* q, int32_t q_dtype, const float* q_sca
  * pointers on the device current on the calling thread; lengths are HOST
  * int32 [batch] and travel as kernel arguments, so a captured graph keeps the
  * lengths it was captured with.  Sequences with q_len = 0 are skipped.
- * Inputs must be finite.  Scores, maxima, sums and outputs accumulate in
- * fp32.  The calls allocate nothing, copy nothing to the device and wait for
- * nothing; they may be captured.  Calls that share a workspace must be
- * ordered (one stream, or graphs replayed one after the other).  Results do
+ * Inputs must be finite, and so must what fp32 makes of them: a row's sums of
+ * |q_e k_e| stay below 2^127, as they are and times scale, and its sum of |v|
+ * over the keys below 2^119 (outputs are divided by the softmax sum last, and
+ * weights before that reach 2^8).  Scores, maxima, sums and outputs accumulate
+ * in fp32.  The calls allocate nothing, copy nothing to the device and wait for
+ * nothing; they may be captured.  Calls that share a workspace must be ordered
+ * (one stream, or graphs replayed one after the other).  Results do
  * not change from run to run.
  *
  * Supported: d in {64, 128}; Hkv <= 128, Hq <= 1024, Hq a multiple of Hkv;
  * types DOSA_F32 and DOSA_BF16; at most 2^31 - 2^16 tokens in a batch and slots
  * in a cache, 2^30 queries times group heads in a sequence; token strides up
- * to 2^23 elements.  scale is positive, finite and not subnormal.
+ * to 2^23 elements.  scale is positive, not subnormal, and scale * log2(e)
+ * finite in fp32 (scale up to 2.3e38).
  */
 
 /* Causal attention of packed sequences over contiguous keys and values.

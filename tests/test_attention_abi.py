@@ -290,3 +290,19 @@ def test_empty_calls_do_nothing():
                         stream=STREAM)
     E.dsa_cache_evict(torch.zeros(4, 16), c.page_table, [], [], [], torch.empty(0, 0, dtype=torch.int32),
                       workspace=_space(256), stream=STREAM)
+
+
+@pytest.mark.parametrize("scale", [2.4e38, 3.4e38])
+def test_scales_whose_base_2_form_overflows_are_refused(scale):
+    """scale * log2(e), which the kernels multiply by, must be finite in fp32."""
+    q, c = torch.zeros(1, 2, 64), _cache()
+    acc = torch.zeros(4, 16)
+    for call in (lambda s: E.dsa_prompt_attention(q, q, q.clone(), [1], [1], torch.empty_like(q), scale=s,
+                                                  workspace=_space(1 << 20), stream=STREAM),
+                 lambda s: E.dsa_cache_attention(c, q, [1], [1], torch.empty_like(q), scale=s, workspace=_space(1 << 20),
+                                                 stream=STREAM),
+                 lambda s: E.dsa_cache_weights(c, q, torch.zeros(1, 2), [1], [1], acc, acc, scale=s,
+                                               workspace=_space(1 << 20), stream=STREAM)):
+        with pytest.raises(E.DosaError) as ei:
+            call(scale)
+        assert ei.value.status == -1 and "scale" in str(ei.value)
