@@ -553,8 +553,10 @@ size_t dsa_cache_workspace_size(int32_t batch, const int32_t* q_lens, const int3
         check_heads(Hq, Hkv, d) != DOSA_OK || check_row_count(batch, q_lens, Hq, Hkv) != DOSA_OK)
       return 0;
     if (topk < 0 || topk > (1 << 20)) return 0;
-    return std::max(attn_workspace(A_MX, batch, q_lens, kv_lens, Hq, Hkv, d, topk),
-                    attn_workspace(A_MX32, batch, q_lens, kv_lens, Hq, Hkv, d, topk));
+    // fp32 queries take more row tiles than bf16 ones: either may be too many
+    const size_t a = attn_workspace(A_MX, batch, q_lens, kv_lens, Hq, Hkv, d, topk);
+    const size_t b = attn_workspace(A_MX32, batch, q_lens, kv_lens, Hq, Hkv, d, topk);
+    return a == 0 || b == 0 ? 0 : std::max(a, b);
   });
 }
 

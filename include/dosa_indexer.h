@@ -288,6 +288,10 @@ int dosa_indexer_topk_noalloc(const void* q, int32_t q_dtype, const float* q_sca
  * in a cache, 2^30 queries times group heads in a sequence; token strides up
  * to 2^23 elements.  scale is positive, not subnormal, and scale * log2(e)
  * finite in fp32 (scale up to 2.3e38).
+ *
+ * The *_workspace_size functions return the bytes a call with these arguments
+ * needs (over the cache: with queries of either type), and 0 for arguments that
+ * a call (of either type) would refuse.
  */
 
 /* Causal attention of packed sequences over contiguous keys and values.

@@ -306,3 +306,13 @@ def test_scales_whose_base_2_form_overflows_are_refused(scale):
         with pytest.raises(E.DosaError) as ei:
             call(scale)
         assert ei.value.status == -1 and "scale" in str(ei.value)
+
+
+def test_workspace_size_of_zero_if_either_query_type_is_refused():
+    """2^30 rows a head on 32 heads: 2^31 row tiles of 16 for fp32 queries, one more than a call may have, half
+    as many for bf16 ones."""
+    n = [1 << 30]
+    with pytest.raises(E.DosaError) as ei:
+        E.cache_workspace_size(n, n, 32, 32, 64)
+    assert ei.value.status == -2
+    assert E.cache_workspace_size(n, n, 31, 31, 64) > 0
