@@ -6,7 +6,9 @@
 // front of the new end do not move; the n-th kept key behind it (in order)
 // moves into the n-th hole in front of it.  So a periodic eviction of a few
 // keys moves a few rows, and no row is read from a place another is written
-// to: the moves are independent.
+// to: the moves are independent.  An index in front of the new end whose table
+// entry names no page holds nothing and is no hole: it ranks with the protected
+// keys, so that no key moves to where it would be lost.
 #include "attn_device.h"
 
 namespace dosa {
@@ -22,8 +24,9 @@ __device__ __forceinline__ uint32_t rank_of(const EvictArgs& p, const EvictSeq& 
   return pos < p.prefix || (int64_t)pos >= (int64_t)s.seen - p.window ? 0xffffffffu : r;
 }
 
-// Ranks of N rounds from round i0 on, as unsigned numbers: 0 without a page,
-// all ones if protected, else the order of the weight's bits.  Each kind of
+// Ranks of N rounds from round i0 on, as unsigned numbers: all ones if protected
+// or without a page in front of the new end, 0 without a page behind it, else
+// the order of the weight's bits.  Each kind of
 // load is issued for all rounds before any is used, without branches, since
 // the chain page, weight, position is all latency.  With pages of a multiple
 // of 64 keys a wavefront's keys of a round lie in one page.
@@ -54,7 +57,10 @@ __device__ __forceinline__ void load_ranks(const EvictArgs& p, const EvictSeq& s
     for (int i = 0; i < N; ++i) pos[i] = p.pos[slot[i] < 0 ? 0 : slot[i]];
   }
 #pragma unroll
-  for (int i = 0; i < N; ++i) rk[i] = slot[i] < 0 ? 0u : rank_of(p, s, acc[i], pos[i]);
+  for (int i = 0; i < N; ++i) {
+    const bool front = (i0 + i) * 1024 + 64 * wave + lane64() < s.new_len;
+    rk[i] = slot[i] < 0 ? (front ? 0xffffffffu : 0u) : rank_of(p, s, acc[i], pos[i]);
+  }
 }
 
 // Exclusive sums over cnt[0..n), n <= kThreads, in place; one workgroup.

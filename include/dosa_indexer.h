@@ -404,7 +404,10 @@ typedef struct {
  * and seen_lens (HOST, >= kv_lens, NULL = kv_lens) the tokens of the text so
  * far; without pos a key's place is its index.  Kept keys at indices below
  * new_len stay; the n-th kept key behind them moves to the n-th freed index in
- * front.  Keys are addressed by index through page_table; attention does not
+ * front.  An index in front of new_len whose table entry names no page counts
+ * as a key that stays: nothing moves to it, and one key fewer is kept; with so
+ * few places left that protected keys do not all fit, the lowest indices among
+ * them stay.  Keys are addressed by index through page_table; attention does not
  * depend on their order.  out_src [batch, out_stride] int32: the index each
  * key 0..new_len-1 came from, -1 behind.  arrays (HOST, up to 16) are moved
  * accordingly; an array's dst may be its own src and otherwise overlaps

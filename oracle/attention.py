@@ -147,12 +147,16 @@ def accumulate(cache, weights, q_lens, kv_lens, acc, acc_out):
 # ----------------------------------------------------------------------------
 # eviction
 # ----------------------------------------------------------------------------
-def evict(acc, kv_len, new_len, prefix, window, pos=None, seen=None):
-    """Source index of each kept key 0..new_len-1.  acc, pos: values by key index."""
+def evict(acc, kv_len, new_len, prefix, window, pos=None, seen=None, there=None):
+    """Source index of each kept key 0..new_len-1.  acc, pos: values by key index; there: whether the key
+    has a page (None: all have).  An index in front of the new end without a page stays as it is, so that
+    no key moves to it; such keys behind it go first."""
     place = np.arange(kv_len) if pos is None else np.asarray(pos[:kv_len])
     seen = kv_len if seen is None else seen
-    safe = (place < prefix) | (place >= seen - window)
-    order = sorted(range(kv_len), key=lambda j: (not safe[j], 0.0 if safe[j] else -float(acc[j]), j))
+    there = np.ones(kv_len, bool) if there is None else np.asarray(there)
+    safe = np.where(there, (place < prefix) | (place >= seen - window), np.arange(kv_len) < new_len)
+    order = sorted(range(kv_len), key=lambda j: (0 if safe[j] else 1 if there[j] else 2,
+                                                 -float(acc[j]) if there[j] and not safe[j] else 0.0, j))
     kept = set(order[:new_len])
     movers = [j for j in range(new_len, kv_len) if j in kept]
     src, nth = [], 0

@@ -75,3 +75,14 @@ def test_evict_keeps_the_best(seed):
             assert safe[i] or acc[i] > acc[j] or (acc[i] == acc[j] and i < j)
     for j, i in enumerate(src):
         assert i == j or (i >= keep and j in rest)
+
+
+def test_evict_moves_nothing_to_an_index_without_a_page():
+    acc = [5.0, 1.0, 2.0, 9.0, 8.0, 7.0, 3.0, 6.0]
+    there = np.array([True, False, True, True, True, False, True, True])
+    # places 0, 2, 3 are left in front of 4: of the keys with a page 9, 8 and 6 stay
+    assert A.evict(acc, 8, 4, 0, 0, there=there).tolist() == [4, 1, 7, 3]
+    # a protected key of small weight takes a place
+    assert A.evict(acc, 8, 4, 1, 1, there=there).tolist() == [0, 1, 7, 3]
+    # more protected keys than places: the lowest indices
+    assert A.evict(acc, 8, 4, 2, 2, there=np.array([False, False, False, True, True, True, True, True])).tolist() == [0, 1, 2, 6]

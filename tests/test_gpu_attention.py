@@ -885,3 +885,48 @@ def test_cache_attention_missing_pages_next_to_an_unused_one(dtype, d, hq, hk, p
     assert np.any(~np.isfinite(ref[1])) and np.any(np.isfinite(ref[1]))
     check_attention(out, lse, ref, d, max(kl), dtype == "bf16")
     check_weights(c, h, q, ql, kl, dtype, "other")
+
+
+@pytest.mark.parametrize("kl,nl,page,kw", [
+    ([100], [60], 16, {}),
+    ([200, 64, 30], [130, 40, 16], 16, dict(prefix=4, window=9)),
+    ([3000, 500], [700, 480], 64, dict(prefix=4, window=40)),
+    ([9000], [5000], 48, dict(prefix=1, window=100)),
+    ([70000], [20000], 128, dict(prefix=4, window=64)),
+])
+def test_evict_without_some_pages(kl, nl, page, kw):
+    """Keys move only to indices that have a page: those of largest acc are all still there afterwards."""
+    rng = np.random.default_rng(sum(kl))
+    t, pages = table(rng, kl, page)
+    for b, n in enumerate(kl):
+        for p in range(-(-n // page)):
+            if p % 3 == 1:
+                t[b, p] = (-1, pages)[p & 1]
+    at = [A.slots(t, b, n, page, pages) for b, n in enumerate(kl)]
+    acc = rng.random((pages, page)).astype(np.float32)
+    rows_ = rng.integers(0, 256, (pages, page, 48)).astype(np.uint8)
+    a, r = torch.from_numpy(acc.copy()).cuda(), torch.from_numpy(rows_.copy()).cuda()
+    away = torch.zeros_like(r)
+    out = torch.full((len(kl), max(nl)), 77, dtype=torch.int32, device="cuda")
+    say("evict missing pages", kl, nl, page)
+    E.dsa_cache_evict(a, torch.from_numpy(t).cuda(), kl, nl, [(r, r), (r.clone(), away), (a, a)], out,
+                      workspace=space(E.evict_workspace_size(kl, nl)), **kw)
+    torch.cuda.synchronize()
+    pre, win = kw.get("prefix", 0), kw.get("window", 0)
+    for b, (n, k) in enumerate(zip(kl, nl)):
+        there = at[b] >= 0
+        src = A.evict(acc.reshape(-1)[at[b]], n, k, pre, win, there=there)
+        got = out.cpu().numpy()[b]
+        assert np.array_equal(got[:k], src) and np.all(got[k:] == -1)
+        to, frm = at[b][:k], at[b][src]
+        assert np.array_equal(to < 0, frm < 0)                 # no row goes where none can be
+        to, frm = to[to >= 0], frm[frm >= 0]
+        assert np.array_equal(r.cpu().numpy().reshape(-1, 48)[to], rows_.reshape(-1, 48)[frm])
+        assert np.array_equal(away.cpu().numpy().reshape(-1, 48)[to], rows_.reshape(-1, 48)[frm])
+        # the weights that stay are the largest that the remaining places hold, protected keys first
+        place = np.arange(n)
+        safe = there & ((place < pre) | (place >= n - win))
+        want = np.sort(np.concatenate([acc.reshape(-1)[at[b][safe]],
+                                       -np.sort(-acc.reshape(-1)[at[b][there & ~safe]])[:max(len(to) - safe.sum(), 0)]]))
+        if safe.sum() <= len(to):
+            assert np.array_equal(np.sort(a.cpu().numpy().reshape(-1)[to]), want)
