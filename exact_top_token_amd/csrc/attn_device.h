@@ -64,14 +64,15 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 }
 
 // x = t0 + t1 + t2 in bf16 terms: 24 significant bits, so products of the
-// terms with exact bf16 operands, summed in fp32, are fp32 products.
+// terms with exact bf16 operands, summed in fp32, are fp32 products.  The terms
+// are cut off, not rounded: eight bits each suffice, and a number next to the
+// largest would round to infinity.
+__device__ __forceinline__ float top_bits(float x) { return __uint_as_float(__float_as_uint(x) & 0xffff0000u); }
 __device__ __forceinline__ void split3(float x, float* t) {
-  const float a = (float)(__bf16)x;
-  const float r = x - a;
-  const float b = (float)(__bf16)r;
-  t[0] = a;
-  t[1] = b;
-  t[2] = r - b;
+  t[0] = top_bits(x);
+  const float r = x - t[0];
+  t[1] = top_bits(r);
+  t[2] = r - t[1];
 }
 
 // Maximum / sum over the four 16-lane groups (lanes l, l^16, l^32, l^48).

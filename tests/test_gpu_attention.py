@@ -930,3 +930,59 @@ def test_evict_without_some_pages(kl, nl, page, kw):
                                        -np.sort(-acc.reshape(-1)[at[b][there & ~safe]])[:max(len(to) - safe.sum(), 0)]]))
         if safe.sum() <= len(to):
             assert np.array_equal(np.sort(a.cpu().numpy().reshape(-1)[to]), want)
+
+
+# ----------------------------------------------------------------------------
+# ends of the number ranges
+# ----------------------------------------------------------------------------
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("ql,kl", [([2, 1], [100, 20]), ([70], [150])])
+def test_cache_calls_with_the_largest_fp32_queries(d, ql, kl):
+    """Queries up to the largest fp32 number over keys so small that the scores are ordinary."""
+    rng = np.random.default_rng(90 + d)
+    c, h = filled_cache(rng, kl, 64, 2, d)
+    vis = h["k_scales"] != 0xFF
+    h["k_scales"][vis] -= 64
+    c.k_scales.copy_(torch.from_numpy(h["k_scales"]))
+    q = rows(rng, sum(ql), 4, d, "f32") * 2.0 ** 100
+    top = float(np.finfo(np.float32).max)
+    q[:, :, 3], q[:, 1::2, 5] = top, -top
+    scale = 2.0 ** -67
+    say("largest queries", d, ql, kl)
+    out, lse = run_cache(c, q.cuda(), ql, kl, scale=scale)
+    ref = A.cache_attention(host(q), h, ql, kl, scale)
+    assert ref[3].max() < 500
+    check_attention(out, lse, ref, d, max(kl), False)
+    acc = torch.zeros(c.num_pages, c.page_size, device="cuda")
+    E.dsa_cache_weights(c, q.cuda(), torch.from_numpy(ref[1].astype(np.float32)).cuda(), ql, kl, None, acc, scale=scale,
+                        workspace=space(E.weights_workspace_size(ql, kl, 4, 2, d)))
+    torch.cuda.synchronize()
+    want = A.accumulate(h, ref[4], ql, kl, None, np.zeros((c.num_pages, c.page_size)))
+    e = float((weight_err(ref[3], ref[1], d, 0) + 2 * U * np.abs(ref[1])).max())
+    assert np.all(np.abs(acc.cpu().numpy() - want) <= (np.abs(want) + 1e-30) * (e + (max(ql) * 4 + 4) * U))
+
+
+def test_read_of_every_code_and_scale():
+    """A cache that other code wrote: every scale byte in 0..254 with every code whose value is finite."""
+    n, d = 256, 64
+    codes = np.tile(np.arange(16, dtype=np.uint8), 4)
+    scales = np.zeros((n, 1, 2), np.uint8)
+    scales[:255, 0, :] = np.arange(255, dtype=np.uint8)[:, None]
+    x = np.repeat(codes[None], n, 0)
+    big = A.GRID[x & 7] * np.ldexp(1.0, scales[:, 0, :1].astype(int) - 127) >= 2.0 ** 128
+    x[big] &= 8
+    packed = (x[:, ::2] | (x[:, 1::2] << 4)).astype(np.uint8)[:, None, :]
+    t = torch.zeros(1, 1, dtype=torch.int32, device="cuda")
+    c = E.Cache.empty(1, n, 1, d, t)
+    for w in "kv":
+        getattr(c, w + "_codes").copy_(torch.from_numpy(packed[None]))
+        getattr(c, w + "_scales").copy_(torch.from_numpy(scales[None]))
+    want = A.mx_decode(packed, scales)
+    for dtype in (torch.float32, torch.bfloat16):
+        say("every code", dtype)
+        k, v = (torch.empty(n, 1, d, dtype=dtype, device="cuda") for _ in "kv")
+        E.dsa_cache_read(c, k, v, [n], [n])
+        torch.cuda.synchronize()
+        for y in (k, v):
+            bad = np.argwhere(y.double().cpu().numpy() != want)
+            assert len(bad) == 0, bad[:4].tolist()
