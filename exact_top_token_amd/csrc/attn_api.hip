@@ -52,6 +52,15 @@ int check_row_count(int32_t batch, const int32_t* q_lens, int32_t Hq, int32_t Hk
   return DOSA_OK;
 }
 
+// The GPU counts a launch's threads in 32 bits.
+constexpr int64_t kLaunchThreads = int64_t(1) << 32;
+
+int check_launch(const char* what, int64_t threads) {
+  if (threads >= kLaunchThreads)
+    return fail(DOSA_ERR_UNSUPPORTED, std::string(what) + ": a launch of 2^32 threads or more, split the call");
+  return DOSA_OK;
+}
+
 int check_scale(float scale) {
   // a subnormal scale would be flushed, and 0 times a masked score's -inf is not
   // 0; the kernels multiply by scale * log2(e), and infinity times an equal
@@ -218,10 +227,14 @@ size_t part_bytes(const AttnChunk& ch, int d) {
   return up256(rows * d * sizeof(float)) + up256(rows * 2 * sizeof(float));
 }
 
+int64_t attn_threads(const AttnChunk& ch, bool tiled) {
+  return ch.a.n_units * int64_t(tiled ? 64 * kPromptWaves : 64);
+}
+
 // Bytes of partial results the call's launches need (each launch reuses them);
-// 0 if a launch would be too large.
+// 0 if a launch would be too large.  threads: those of the largest launch.
 size_t attn_workspace(int src, int32_t batch, const int32_t* q_lens, const int32_t* kv_lens, int32_t Hq, int32_t Hkv,
-                      int32_t d, int32_t topk) {
+                      int32_t d, int32_t topk, int64_t* threads = nullptr) {
   size_t most = 256;
   for (int tiled = 0; tiled < (src == A_BF16 ? 2 : 1); ++tiled) {
     int64_t qr = 0, kr = 0;
@@ -230,6 +243,7 @@ size_t attn_workspace(int src, int32_t batch, const int32_t* q_lens, const int32
       b = plan_attn(ch, src, d, tiled != 0, b, batch, q_lens, kv_lens, Hq, Hkv, topk, &qr, &kr);
       if (b < 0) return 0;
       most = std::max(most, part_bytes(ch, d));
+      if (threads != nullptr) *threads = std::max(*threads, attn_threads(ch, tiled != 0));
     }
   }
   return most;
@@ -240,7 +254,7 @@ int run_attn(int src, const AttnArgs& base, int32_t batch, const int32_t* q_lens
   // each kernel's first launch is planned once, for the size check and the run
   AttnChunk head[2];
   int next[2];
-  int64_t qr[2] = {0, 0}, kr[2] = {0, 0};
+  int64_t qr[2] = {0, 0}, kr[2] = {0, 0}, threads = 0;
   const int classes = src == A_BF16 ? 2 : 1;
   size_t need = 256;
   for (int tiled = 0; tiled < classes; ++tiled) {
@@ -249,11 +263,14 @@ int run_attn(int src, const AttnArgs& base, int32_t batch, const int32_t* q_lens
                             &qr[tiled], &kr[tiled]);
     if (next[tiled] < 0) return fail(DOSA_ERR_UNSUPPORTED, "too many row tiles and key ranges for one launch");
     need = std::max(need, part_bytes(head[tiled], d));
+    threads = std::max(threads, attn_threads(head[tiled], tiled != 0));
   }
   if (next[0] < batch || next[classes - 1] < batch) {
-    need = attn_workspace(src, batch, q_lens, kv_lens, base.Hq, base.Hkv, d, base.topk);
+    need = attn_workspace(src, batch, q_lens, kv_lens, base.Hq, base.Hkv, d, base.topk, &threads);
     if (need == 0) return fail(DOSA_ERR_UNSUPPORTED, "too many row tiles and key ranges for one launch");
   }
+  const int st = check_launch("attention", threads + 64 * 8);   // its last workgroup may be partly empty
+  if (st != DOSA_OK) return st;
   if (workspace == nullptr || workspace_bytes < need || !aligned(workspace, 16))
     return fail(DOSA_ERR_WORKSPACE, "workspace needs " + std::to_string(need) + " bytes, 16-byte aligned");
   for (int tiled = classes - 1; tiled >= 0; --tiled) {
@@ -389,7 +406,7 @@ int plan_weights(WeightArgs& a, WeightKind kind, bool f32, int64_t* floats, int 
 }
 
 size_t weights_workspace(bool f32, int32_t batch, const int32_t* q_lens, const int32_t* kv_lens, int32_t Hq,
-                         int32_t Hkv) {
+                         int32_t Hkv, int64_t* threads = nullptr) {
   size_t most = 256;
   for (int kind = 0; kind < WK_KINDS; ++kind) {
     int64_t qr = 0;
@@ -399,6 +416,7 @@ size_t weights_workspace(bool f32, int32_t batch, const int32_t* q_lens, const i
       b = plan_weights(a, (WeightKind)kind, f32, &floats, b, batch, q_lens, kv_lens, Hq, Hkv, &qr);
       if (b < 0) return 0;
       most = std::max(most, up256((size_t)floats * sizeof(float)));
+      if (threads != nullptr) *threads = std::max({*threads, int64_t(a.n_units) * 512, int64_t(a.n_tiles) * 256});
     }
   }
   return most;
@@ -418,6 +436,11 @@ int cache_io(bool write, const dsa_cache* cache, void* k, int64_t k_stride, void
   for (int b = 0; seen_lens != nullptr && b < batch; ++b)
     if (seen_lens[b] < kv_lens[b])
       return fail(DOSA_ERR_INVALID_ARG, "sequence " + std::to_string(b) + ": need seen_len >= kv_len");
+  auto blocks = [&](int b) { return ((int64_t)q_lens[b] + kCacheTokens - 1) / kCacheTokens; };
+  for (int b = 0; b < batch; ++b) {
+    st = check_launch("cache append or read", blocks(b) * 256);
+    if (st != DOSA_OK) return st;
+  }
   CacheIoArgs a{};
   a.cache = view(cache);
   a.k = k;
@@ -429,11 +452,11 @@ int cache_io(bool write, const dsa_cache* cache, void* k, int64_t k_stride, void
   for (int b = 0; b < batch;) {
     a.n_seq = 0;
     int32_t units = 0;
-    for (; b < batch && a.n_seq < kAttnSeqs; ++b) {
+    for (; b < batch && a.n_seq < kAttnSeqs && (units + blocks(b)) * 256 < kLaunchThreads; ++b) {
       if (q_lens[b] > 0) {
         a.s[a.n_seq++] = CacheSeq{units, (int32_t)row, q_lens[b], kv_lens[b] - q_lens[b],
                                   (seen_lens != nullptr ? seen_lens[b] : kv_lens[b]) - q_lens[b], b};
-        units += (q_lens[b] + kCacheTokens - 1) / kCacheTokens;
+        units += (int32_t)blocks(b);
       }
       row += q_lens[b];
     }
@@ -622,8 +645,11 @@ int dsa_cache_weights(const dsa_cache* cache, const void* q, int64_t q_stride, i
     if (st != DOSA_OK) return st;
     if (tq > 0 && (lse == nullptr || acc_out == nullptr)) return fail(DOSA_ERR_INVALID_ARG, "lse or acc_out is NULL");
     const bool f32 = q_dtype == DOSA_F32;
-    const size_t need = weights_workspace(f32, batch, q_lens, kv_lens, Hq, cache->Hkv);
+    int64_t threads = 0;
+    const size_t need = weights_workspace(f32, batch, q_lens, kv_lens, Hq, cache->Hkv, &threads);
     if (need == 0) return fail(DOSA_ERR_UNSUPPORTED, "too many key tiles for one launch");
+    st = check_launch("weights", threads);
+    if (st != DOSA_OK) return st;
     if (workspace == nullptr || workspace_bytes < need || !aligned(workspace, 16))
       return fail(DOSA_ERR_WORKSPACE, "workspace needs " + std::to_string(need) + " bytes, 16-byte aligned");
     WeightArgs a{};
@@ -692,6 +718,13 @@ int dsa_cache_evict(const float* acc, const int32_t* pos, const int32_t* page_ta
     }
     if (n_arrays < 0 || n_arrays > kEvictArrays || (n_arrays > 0 && arrays == nullptr))
       return fail(DOSA_ERR_INVALID_ARG, "n_arrays must be in 0.." + std::to_string(kEvictArrays) + ", with arrays");
+    int64_t cap = 0, kept = 0;
+    for (int b = 0; b < batch; ++b) {
+      cap = std::max<int64_t>(cap, std::min(new_lens[b], kv_lens[b] - new_lens[b]));
+      kept = std::max<int64_t>(kept, new_lens[b]);
+    }
+    st = check_launch("eviction", evict_move_threads(cap, kept));
+    if (st != DOSA_OK) return st;
     if (batch == 0 || out_stride == 0) return DOSA_OK;
     if (acc == nullptr || out_src == nullptr) return fail(DOSA_ERR_INVALID_ARG, "acc or out_src is NULL");
     EvictMoveArgs mv{};

@@ -166,6 +166,13 @@ struct EvictMoveArgs {
   EvictSeq s[kEvictSeqs];
   EvictArray a[kEvictArrays];
 };
+// Rows of a workgroup of the move: entries of the list of moves, rows copied
+// elsewhere; and the threads that so many of each take.
+constexpr int kMoveRows = 8;
+constexpr int kCopyRows = 256;
+constexpr int64_t evict_move_threads(int64_t moves, int64_t copies) {
+  return ((moves + kMoveRows - 1) / kMoveRows + (copies + kCopyRows - 1) / kCopyRows) * 256;
+}
 hipError_t launch_evict_select(const EvictArgs& p, hipStream_t s);
 hipError_t launch_evict_move(EvictMoveArgs p, hipStream_t s);
 

@@ -271,10 +271,7 @@ __global__ __launch_bounds__(kThreads) void evict_select_kernel(const EvictArgs 
   if (tid == 0) ws[0] = moved;
 }
 
-// Rows of arrays moved in place: workgroups of kMoveRows entries of the
-// sequence's list of moves.
-constexpr int kMoveRows = 8;
-
+// Copies the rows of one array from slots to slots.
 template <class V>
 __device__ __forceinline__ void copy_rows(const EvictArray& a, const int* from, const int* to, int n) {
   const int cols = a.row_bytes / (int)sizeof(V);
@@ -292,12 +289,10 @@ __device__ __forceinline__ void copy_any(const EvictArray& a, const int* from, c
   else copy_rows<uint8_t>(a, from, to, n);
 }
 
-// Workgroups 0..in_blocks-1 of a sequence: the moves of the arrays in place;
-// the others: every kept row of the arrays that go elsewhere.  4 KB a key in
-// two arrays: 64 moves in each of 16 sequences 6 us, 16 thousand moves 24 us
-// (5.3 TB/s).
-constexpr int kCopyRows = 256;
-
+// Workgroups 0..in_blocks-1 of a sequence: kMoveRows entries each of its list
+// of moves, for the arrays in place; the others: kCopyRows kept rows each of
+// the arrays that go elsewhere.  4 KB a key in two arrays: 64 moves in each of
+// 16 sequences 6 us, 16 thousand moves 24 us (5.3 TB/s).
 __global__ __launch_bounds__(256) void evict_move_kernel(const EvictMoveArgs p) {
   __shared__ int from[kCopyRows], to[kCopyRows];
   const EvictSeq& s = p.s[blockIdx.y];

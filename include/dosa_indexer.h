@@ -287,7 +287,10 @@ int dosa_indexer_topk_noalloc(const void* q, int32_t q_dtype, const float* q_sca
  * types DOSA_F32 and DOSA_BF16; at most 2^31 - 2^16 tokens in a batch and slots
  * in a cache, 2^30 queries times group heads in a sequence; token strides up
  * to 2^23 elements.  scale is positive, not subnormal, and scale * log2(e)
- * finite in fp32 (scale up to 2.3e38).
+ * finite in fp32 (scale up to 2.3e38).  A launch has less than 2^32 threads: a
+ * call that would need more in one (such as 2^26 queries times kv heads over
+ * selected keys, 2^31 rows of a bf16 prompt times kv heads, 2^28 tokens appended
+ * to a sequence, 2^27 keys moved in one) is refused, to be split.
  *
  * The *_workspace_size functions return the bytes a call with these arguments
  * needs (over the cache: with queries of either type), and 0 for arguments that

@@ -316,3 +316,22 @@ def test_workspace_size_of_zero_if_either_query_type_is_refused():
         E.cache_workspace_size(n, n, 32, 32, 64)
     assert ei.value.status == -2
     assert E.cache_workspace_size(n, n, 31, 31, 64) > 0
+
+
+def test_launches_of_2_32_threads_are_refused():
+    """Calls whose lengths pass but whose launch would have too many threads; nothing is read of the pointers."""
+    L, p, big = E.lib(), 1 << 12, 1 << 40
+    n = lambda x: AT._lens([x])
+    cache = lambda hk: ctypes.byref(AT.DsaCache(p, p, p, p, p, 4, 1 << 14, 1 << 16, hk, 64, 0))
+    m = 1 << 20        # selected keys: a tile for each query and head
+    assert L.dsa_cache_attention(cache(64), p, 64 * 64, 0, n(m), n(m), 1, 64, p, 2048, 0.1, p, None, p, big, None) == -2
+    m = 1 << 27        # 2^30 rows a head
+    assert L.dsa_prompt_attention(p, 64 * 64, p, 8 * 64, p, 8 * 64, 1, n(m), n(m), 1, 64, 8, 64, 0.1, p, None, p, big, None) == -2
+    m = 1 << 30        # 2^24 tiles of 64 keys
+    assert L.dsa_cache_weights(cache(1), p, 64, 0, p, n(40), n(m), 1, 1, 0.1, None, p, p, big, None) == -2
+    m = 1 << 28
+    for fn, tail in ((L.dsa_cache_append, (None, None, None)), (L.dsa_cache_read, (None,))):
+        assert fn(cache(1), p, 64, p, 64, 1, n(m), n(m), 1, *tail) == -2
+    assert L.dsa_cache_evict(p, None, p, 1 << 14, 1 << 16, 4, n(1 << 29), n(1 << 28), None, 1, 0, 0, None, 0, p, 1 << 28, p, big,
+                             None) == -2
+    assert "2^32" in E.status_string(-2)
