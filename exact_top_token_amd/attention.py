@@ -11,9 +11,9 @@ The arguments and results are those of include/dosa_indexer.h:
     dsa_cache_weights      attention weight each cached key received
     dsa_cache_evict        keep the keys that received most
 
-Calls run on ``stream`` (default: the current stream of the tensors' device)
-and raise :class:`DosaError`.  ``workspace`` is a device tensor of at least the
-matching ``*_workspace_size`` bytes.
+Calls run on ``stream`` (a torch stream of the tensors' device or a handle of
+one; default: its current stream) and raise :class:`DosaError`.  ``workspace``
+is a device tensor of at least the matching ``*_workspace_size`` bytes.
 """
 from __future__ import annotations
 
@@ -165,6 +165,8 @@ class _On:
         torch = _torch
         if self.device.type != "cuda":
             _bad(f"tensors are on {self.device}, not on a GPU")
+        if getattr(self.stream, "device", self.device) != self.device:
+            _bad(f"stream is of {self.stream.device}, the tensors are on {self.device}")
         if torch.cuda.current_device() != self.device.index:
             self.back = torch.cuda.device(self.device)
             self.back.__enter__()

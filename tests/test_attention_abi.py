@@ -3,6 +3,7 @@ anything touches a GPU.  The tensors are CPU tensors; the binding's own refusal 
 that a call gets to the library's checks."""
 import contextlib
 import ctypes
+from types import SimpleNamespace
 
 import pytest
 import torch
@@ -335,3 +336,12 @@ def test_launches_of_2_32_threads_are_refused():
     assert L.dsa_cache_evict(p, None, p, 1 << 14, 1 << 16, 4, n(1 << 29), n(1 << 28), None, 1, 0, 0, None, 0, p, 1 << 28, p, big,
                              None) == -2
     assert "2^32" in E.status_string(-2)
+
+
+def test_cpu_tensors_refused_and_streams_of_another_device():
+    """A stream belongs to the tensors' device (the binding's own check, before it touches a GPU)."""
+    other = SimpleNamespace(device=torch.device("cuda", 1), cuda_stream=1 << 12)
+    with pytest.raises(E.DosaError) as ei:
+        with AT._On(torch.device("cuda", 0), other):
+            pass
+    assert ei.value.status == -1 and "stream" in str(ei.value)
