@@ -84,7 +84,7 @@ struct CacheIoArgs {
   void* v;
   int64_t k_stride, v_stride;
   int32_t* pos;       // [num_pages, page_size] or NULL (write only)
-  int32_t n_seq, total;
+  int32_t n_seq;
   CacheSeq s[kAttnSeqs];
 };
 hipError_t launch_cache_append(bool f32, int d, const CacheIoArgs& p, hipStream_t s);

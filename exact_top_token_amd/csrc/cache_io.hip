@@ -44,7 +44,6 @@ __device__ __forceinline__ Where place(const CacheIoArgs& p, int* slots) {
 template <bool F32>
 struct Share {
   static constexpr int E = F32 ? 4 : 8;      // elements
-  typedef i4 Raw;
 };
 
 template <bool F32>

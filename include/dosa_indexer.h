@@ -294,7 +294,7 @@ int dosa_indexer_topk_noalloc(const void* q, int32_t q_dtype, const float* q_sca
  *
  * The *_workspace_size functions return the bytes a call with these arguments
  * needs (over the cache: with queries of either type), and 0 for arguments that
- * a call (of either type) would refuse.
+ * a call (of either type) would refuse, the limit of a launch aside.
  */
 
 /* Causal attention of packed sequences over contiguous keys and values.
