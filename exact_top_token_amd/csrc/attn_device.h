@@ -16,6 +16,13 @@ typedef __bf16 b8 __attribute__((ext_vector_type(8)));
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 
+// Exponents are taken as s c - m c in one multiply-add, c = scale log2(e), with
+// m c rounded to fp32.  Up to this magnitude that shifts an exponent by 2^-15 at
+// most, no more than fp32 scores of the size are off; beyond it the shift would
+// grow into the weights (2^31: into infinity), and m is subtracted first.  The
+// weights calls do the same with the normaliser in m's place.
+constexpr float kFar = 1024.f;
+
 __device__ __forceinline__ int lane64() { return (int)__lane_id(); }
 
 // The record of the launch that unit `u` belongs to: `first` of the records
@@ -73,6 +80,13 @@ __device__ __forceinline__ void split3(float x, float* t) {
   const float r = x - t[0];
   t[1] = top_bits(r);
   t[2] = r - t[1];
+}
+
+// exp(scale s - lse): the normaliser is taken off before the change of base, so
+// that its own rounding to fp32 is all that a large one costs.  lse = INFINITY:
+// a row that gives nothing.
+__device__ __forceinline__ float weight_of(float s, float scale, float lse) {
+  return __builtin_amdgcn_exp2f(fmaf(s, scale, -lse) * kLog2e);
 }
 
 // Maximum / sum over the four 16-lane groups (lanes l, l^16, l^32, l^48).

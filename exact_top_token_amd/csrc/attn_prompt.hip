@@ -184,7 +184,15 @@ __global__ __launch_bounds__(64 * NW, 2) void prompt_kernel(const AttnArgs p) {
 #pragma unroll
         for (int e = 0; e < 16; ++e) o[j][e] *= f;
     }
-    const float mc = m == -INFINITY ? 0.f : m * c;
+    float mc = m * c;
+    if (__any(fabsf(mc) > kFar)) {         // or a row that has seen nothing
+      const float off = m == -INFINITY ? 0.f : m;
+#pragma unroll
+      for (int a = 0; a < 2; ++a)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) sc[a][e] -= off;
+      mc = 0.f;
+    }
     // the tile after the wavefront's last is read too (it is there or never
     // filled; its scores are not used), so that this is one block of code
     scores(next, t + 1);

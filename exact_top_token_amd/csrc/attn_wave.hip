@@ -46,7 +46,10 @@ struct SrcTraits {
   static constexpr bool MX = SRC == A_MX || SRC == A_MX32;
   static constexpr int KT = MX ? 4 / HP : (SRC == A_BF16 ? 2 : 1);   // 16-key tiles per step
   static constexpr int TERMS = SRC == A_MX32 ? 3 : 1;             // bf16 terms of queries and weights
-  static constexpr int NB = MX && RT * HP == 1 ? 3 : 2;                // steps in registers: one used, the others loading
+  // steps in registers: one used, the others loading.  Three where they fit: with
+  // fp32 queries they spill at d = 128 (decode of 32 x 2 queries over 870K keys in
+  // pages of 16: 278 against 237 us, 2048 selected keys a query: 62 against 49)
+  static constexpr int NB = MX && RT * HP == 1 && TERMS == 1 ? 3 : 2;
   static constexpr bool F32IO = SRC == A_F32 || SRC == A_MX32;    // type of q and out
 };
 
@@ -465,7 +468,15 @@ __global__ __launch_bounds__(64 * kWaves) void attn_kernel(const AttnArgs p) {
 #pragma unroll
           for (int r = 0; r < 4; ++r) o[i][j][r] *= f;
       }
-      const float mc = m[i] == -INFINITY ? 0.f : m[i] * c;
+      float mc = m[i] * c;
+      if (__any(fabsf(mc) > kFar)) {         // or a row that has seen nothing
+        const float off = m[i] == -INFINITY ? 0.f : m[i];
+#pragma unroll
+        for (int a = 0; a < KT; ++a)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) sc[i][a][r] -= off;
+        mc = 0.f;
+      }
 #pragma unroll
       for (int a = 0; a < KT; ++a)
 #pragma unroll

@@ -48,7 +48,6 @@ __global__ __launch_bounds__(64 * kWaves) void weights_kernel(const WeightArgs p
   const int all = sq.n_part * kWaves, w = part * kWaves + wave;
   const int nh = cv.Hkv < all ? cv.Hkv : all;
   const int slices = all / nh;
-  const float c = p.scale * kLog2e;
   f4 acc[4];
 #pragma unroll
   for (int a = 0; a < 4; ++a) acc[a] = f4{0.f, 0.f, 0.f, 0.f};
@@ -87,7 +86,7 @@ __global__ __launch_bounds__(64 * kWaves) void weights_kernel(const WeightArgs p
         const int64_t tok = sq.q_row0 + query;
         const float lse = p.lse[tok * p.Hq + qh];
         // a row without a normaliser (it saw no key) gives nothing
-        const float lc = ok && lse > -INFINITY ? lse * kLog2e : INFINITY;
+        const float ls = ok && lse > -INFINITY ? lse : INFINITY;
         b8 qf[TERMS][NS];
         const int64_t at = tok * p.q_stride + (int64_t)qh * D + g * (D / 4);
         const f4* src = reinterpret_cast<const f4*>(static_cast<const float*>(p.q) + at);
@@ -122,7 +121,7 @@ __global__ __launch_bounds__(64 * kWaves) void weights_kernel(const WeightArgs p
 #pragma unroll
         for (int a = 0; a < 4; ++a)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) acc[a][e] += __builtin_amdgcn_exp2f(fmaf(s4[a][e], c, -lc));
+          for (int e = 0; e < 4; ++e) acc[a][e] += weight_of(s4[a][e], p.scale, ls);
       }
     }
   }

@@ -986,3 +986,80 @@ def test_read_of_every_code_and_scale():
         for y in (k, v):
             bad = np.argwhere(y.double().cpu().numpy() != want)
             assert len(bad) == 0, bad[:4].tolist()
+
+
+def far_scores(rng, n, h, d, dtype):
+    """Small whole numbers: products, their sums and 4-bit codes are exact, and equal scores occur."""
+    return torch.from_numpy(rng.integers(-3, 4, (n, h, d)).astype(np.float32)).to(torch.bfloat16 if dtype == "bf16" else torch.float32)
+
+
+def check_far(out, lse, ref, bf16):
+    """Scores so far apart that only a row's largest count, each with the same weight: the mean of their
+    values, n * U for its sum, the division and, with bf16, the rounding of the result (weights of 1 are
+    exact); lse the largest score."""
+    o, l, ab = ref[0], ref[1], ref[2]
+    got = out.double().cpu().numpy()
+    tol = (1000 * U + (1.01 * 2.0 ** -8 if bf16 else 0)) * ab
+    assert np.all(np.abs(got - o) <= tol), float((np.abs(got - o) - tol).max())
+    assert np.all(np.abs(lse.double().cpu().numpy() - l) <= 4 * U * np.abs(l))
+
+
+@pytest.mark.parametrize("scale", [2.0 ** 20, 2.0 ** 34, 2.0 ** 100])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_attention_of_scores_far_beyond_the_exponential(dtype, d, scale):
+    """|scale q.k| up to 2^110: the largest score's weight is 1 however large it is."""
+    rng = np.random.default_rng(95 + d)
+    hq, hk = 4, 2
+    for ql, kl in (([70, 3], [150, 600]), ([1, 2], [900, 64])):
+        say("far scores", dtype, d, scale, ql)
+        q, k, v = (far_scores(rng, n, h, d, dtype) for n, h in ((sum(ql), hq), (sum(kl), hk), (sum(kl), hk)))
+        out, lse = run_prompt(q.cuda(), k.cuda(), v.cuda(), ql, kl, scale=scale)
+        check_far(out, lse, A.prompt(host(q), host(k), host(v), ql, kl, scale), dtype == "bf16")
+        for page in (64, 48):
+            t, pages = table(rng, kl, page)
+            c = E.Cache.empty(pages, page, hk, d, torch.from_numpy(t).cuda())
+            for x in (c.k_codes, c.k_scales, c.v_codes, c.v_scales):
+                x.fill_(0xFF)
+            E.dsa_cache_append(c, k.cuda(), v.cuda(), kl, kl)
+            h = {n: getattr(c, n).cpu().numpy() for n in ("k_codes", "k_scales", "v_codes", "v_scales")}
+            h["table"] = t
+            out, lse = run_cache(c, q.cuda(), ql, kl, scale=scale)
+            ref = A.cache_attention(host(q), h, ql, kl, scale)
+            check_far(out, lse, ref, dtype == "bf16")
+            idx = rng.integers(0, min(kl), (sum(ql), 90)).astype(np.int32)
+            o2, l2 = run_cache(c, q.cuda(), ql, kl, torch.from_numpy(idx).cuda(), scale=scale)
+            check_far(o2, l2, A.cache_attention(host(q), h, ql, kl, scale, idx), dtype == "bf16")
+
+
+@pytest.mark.parametrize("scale", [2.0 ** 20, 2.0 ** 34, 2.0 ** 100])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_weights_of_scores_far_beyond_the_exponential(dtype, d, scale):
+    """With such scores a key's weight is the number of rows whose largest score is its own, since a
+    normaliser of that size is the largest score itself in fp32."""
+    rng = np.random.default_rng(97 + d)
+    hq, hk, page = 4, 2, 64
+    for ql, kl in (([70, 3], [150, 600]), ([1, 2], [900, 64])):
+        say("far weights", dtype, d, scale, ql)
+        q, k = far_scores(rng, sum(ql), hq, d, dtype), far_scores(rng, sum(kl), hk, d, dtype)
+        t, pages = table(rng, kl, page)
+        c = E.Cache.empty(pages, page, hk, d, torch.from_numpy(t).cuda())
+        E.dsa_cache_append(c, k.cuda(), k.cuda(), kl, kl)
+        lse, want = np.zeros((sum(ql), hq), np.float32), np.zeros((pages * page))
+        r = k0 = 0
+        for b in range(len(ql)):
+            at = A.slots(t, b, kl[b], page, pages)
+            for i in range(ql[b]):
+                for h in range(hq):
+                    s = host(k)[k0:k0 + kl[b] - ql[b] + i + 1, h // 2].astype(np.float64) @ host(q)[r, h].astype(np.float64)
+                    lse[r, h] = s.max() * scale
+                    np.add.at(want, at[:len(s)][s == s.max()], 1.0)
+                r += 1
+            k0 += kl[b]
+        assert np.abs(lse).min() > 1e6
+        acc = torch.zeros(pages, page, device="cuda")
+        E.dsa_cache_weights(c, q.cuda(), torch.from_numpy(lse).cuda(), ql, kl, None, acc, scale=scale,
+                            workspace=space(E.weights_workspace_size(ql, kl, hq, hk, d)))
+        torch.cuda.synchronize()
+        assert np.array_equal(acc.cpu().numpy().reshape(-1), want)
