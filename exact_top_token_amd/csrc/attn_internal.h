@@ -53,8 +53,13 @@ struct AttnArgs {
   AttnSeq s[kAttnSeqs];
 };
 
-// 16-row tiles one wavefront may hold: what fits its 256 registers next to the
-// keys in flight (bf16 rows beyond 16 go to the tiled kernel).
+// 16-row tiles one wavefront may hold next to the keys in flight (bf16 rows
+// beyond 16 go to the tiled kernel).  Two tiles of bf16 rows over the cache take
+// all 256 registers at d = 128 and spill 1 of them, 26 to 30 with a page look-up
+// per key, and are the faster for it: 32 sequences x 4 queries in groups of 8
+// over 871K keys 242 us, 330 us as one tile of a head pair (which does not
+// spill).  A launch takes what its largest sequence needs: one such sequence
+// among 31 of 2 queries costs 241 instead of 207 us.
 constexpr int attn_max_rt(int src, int d) { return src == A_MX || (src == A_F32 && d == 64) ? 2 : 1; }
 
 // Bf16 prompts over LDS tiles: units are row tiles of kPromptWaves * 32 rows of

@@ -21,16 +21,19 @@
 //
 // 4-bit rows become bf16 in the converter (exact), 32-dimension blocks match
 // a lane's share of a key row.  The weights are rounded to bf16 before the
-// second product (2^-9 relative on average sqrt-summed over keys; the sum in
-// the denominator is taken before the rounding); with fp32 queries both the
+// second product (2^-9 relative at most each, which averages out over keys; the
+// sum in the denominator is taken before the rounding; two bf16 terms would
+// double that product); with fp32 queries both the
 // queries and the weights go as three bf16 terms, which keeps fp32 products.
 //
 // Bound, over a long cache, by the cache lines a CU may wait for at once (a
 // wavefront's requests are 64 bytes a row; see HP): decode of 64 sequences x 2
 // queries, 64 heads on 8, d = 128, over 2.35M cached keys, 2.56 GB: 0.48 ms, 5.3
 // TB/s, and 14 us of join.  2048 selected keys for each of 64 queries, 144 MB
-// in 64-byte rows: 38 us and 8 us of join.  One token over 4133 keys (fp32, d =
-// 64): 6 + 5 us, latency.
+// in 64-byte rows: 38 us and 8 us of join, no unit busy more than two fifths of
+// it: a wavefront has eight steps, and waits for an index, a page and a row in
+// turn before the first.  One token over 4133 keys (fp32, d = 64): 6 + 6 us,
+// latency.
 #include <type_traits>
 
 #include "attn_device.h"

@@ -93,9 +93,9 @@ __device__ __forceinline__ void block_scan(int* cnt, int n, int* sh) {
 // it: as many of one as of the other, holes first, so one list holds both.
 // Only if not all keys that equal the threshold stay does another prefix sum
 // number those.
-// Bound by latency for short sequences (16 of 4160 keys: 15 us, a few dependent
+// Bound by latency for short sequences (16 of 4160 keys: 16 us, a few dependent
 // loads and about twenty barriers), by the one CU's instructions for long ones
-// (4 of up to 65536 keys: 85 us).
+// (4 of up to 65536 keys: 86 us).
 template <int PER>
 __global__ __launch_bounds__(kThreads) void evict_select_kernel(const EvictArgs p) {
   __shared__ uint32_t hist[256 * 32];
