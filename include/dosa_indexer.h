@@ -279,9 +279,10 @@ int dosa_indexer_topk_noalloc(const void* q, int32_t q_dtype, const float* q_sca
  * over the keys below 2^119 (outputs are divided by the softmax sum last, and
  * weights before that reach 2^8).  Scores, maxima, sums and outputs accumulate
  * in fp32.  The calls allocate nothing, copy nothing to the device and wait for
- * nothing; they may be captured.  Calls that share a workspace must be ordered
- * (one stream, or graphs replayed one after the other).  Results do
- * not change from run to run.
+ * nothing; they may be captured.  What a call writes overlaps nothing else it
+ * is given, unless said.  Calls that share a workspace must be ordered (one
+ * stream, or graphs replayed one after the other).  Results do not change from
+ * run to run.
  *
  * Supported: d in {64, 128}; Hkv <= 128, Hq <= 1024, Hq a multiple of Hkv;
  * types DOSA_F32 and DOSA_BF16; at most 2^31 - 2^16 tokens in a batch and slots
@@ -327,7 +328,7 @@ int dsa_prompt_attention(const void* q, int64_t q_stride, const void* k, int64_t
  * read back as zeros).  Slots past a sequence's kv_len may hold anything.
  * Sequences may share pages they only read (dsa_cache_read,
  * dsa_cache_attention); a call that writes to a page (append, weights,
- * eviction) must find it in one sequence only. */
+ * eviction) must find it once, in one sequence. */
 typedef struct {
   void* k_codes;
   void* k_scales;
