@@ -20,7 +20,8 @@ constexpr float kLn2 = 0.69314718055994530942f;
 // m c rounded to fp32.  Up to this magnitude that shifts an exponent by 2^-15 at
 // most, no more than fp32 scores of the size are off; beyond it the shift would
 // grow into the weights (2^31: into infinity), and m is subtracted first.  The
-// weights calls do the same with the normaliser in m's place.
+// accumulated weights of bf16 prompts do the same with the normaliser in m's
+// place; the other weights kernels always subtract first.
 constexpr float kFar = 1024.f;
 
 __device__ __forceinline__ int lane64() { return (int)__lane_id(); }
