@@ -21,10 +21,10 @@
 // the next tile: one block of code in which products, their LDS reads and the
 // vector work alternate.  32K causal prompt, 32 heads on 8, d = 128: 7.6 to 8.1
 // ms on different boards, 1090 to 1150 TFLOP/s, nine tenths of what a large
-// library product reaches here; 2% slower with the two one after the other.  Splitting the wavefronts of a SIMD
-// into one that multiplies and one that does softmax, with a barrier at each
-// change, took 8.8 ms: one wavefront alone issues vector work at two thirds
-// of the rate of two.
+// library product reaches here; 2% slower with the two one after the other.
+// Splitting the wavefronts of a SIMD into one that multiplies and one that does
+// softmax, with a barrier at each change, took 8.8 ms: one wavefront alone
+// issues vector work at two thirds of the rate of two.
 //
 // The running maximum is only moved when a score exceeds it by more than 8 in
 // the exponent: weights then reach 2^8 and sums 2^8 n, both far inside fp32,

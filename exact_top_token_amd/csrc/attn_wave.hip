@@ -19,12 +19,12 @@
 // dimensions of its keys and swaps halves with v_perm, so value rows stay
 // row-major in memory and are read with whole-row bursts.
 //
-// 4-bit rows become bf16 in the converter (exact), 32-dimension blocks match
-// a lane's share of a key row.  The weights are rounded to bf16 before the
-// second product (2^-9 relative at most each, which averages out over keys; the
-// sum in the denominator is taken before the rounding; two bf16 terms would
-// double that product); with fp32 queries both the
-// queries and the weights go as three bf16 terms, which keeps fp32 products.
+// 4-bit rows become bf16 in the converter (exact), 32-dimension blocks match a
+// lane's share of a key row.  The weights are rounded to bf16 before the second
+// product (2^-9 relative at most each, which averages out over keys; the sum in
+// the denominator is taken before the rounding; two bf16 terms would double
+// that product); with fp32 queries both the queries and the weights go as three
+// bf16 terms, which keeps fp32 products.
 //
 // Bound, over a long cache, by the cache lines a CU may wait for at once (a
 // wavefront's requests are 64 bytes a row; see HP): decode of 64 sequences x 2

@@ -11,19 +11,19 @@
 // same), and no rounding of the normaliser comes with it.
 //
 // Many bf16 rows (a prompt): a wavefront holds 64 keys of a head as matrix
-// operands, eight of them make 512 keys, and the query rows go past them in
-// LDS tiles of 64 rows loaded one ahead, S^T = K Q^T on the 32x32x16 product:
-// a lane has one row and adds the weights of 32 keys, one normaliser a lane.
+// operands, eight of them make 512 keys, and the query rows go past them in LDS
+// tiles of 64 rows loaded one ahead, S^T = K Q^T on the 32x32x16 product: a
+// lane has one row and adds the weights of 32 keys, one normaliser a lane.
 // Prompts of 8192 and 1031 queries, 32 heads on 8: 0.39 ms, 760 TFLOP/s.  The
 // vector units are busy 57% of it, the matrix units 30%, and the two hardly
 // overlap: 200 registers leave one workgroup a CU, whose two wavefronts a SIMD
 // run in step between barriers, and wait for them and for query tiles 31% of
-// their time.  Of 190 vector instructions per 16 products (64 keys x 32 rows) 96
-// are the weights, the others addresses (with divisions by the group) and masks.  The
-// chunks' work is uneven (the causal mask), so the rows are cut into more shares
-// than the GPU holds at once: 0.46 ms with a quarter of them.  Computing a
-// block's weights under the next block's scores, or four row tiles in flight,
-// did not help.
+// their time.  Of 190 vector instructions per 16 products (64 keys x 32 rows)
+// 96 are the weights, the others addresses (with divisions by the group) and
+// masks.  The chunks' work is uneven (the causal mask), so the rows are cut
+// into more shares than the GPU holds at once: 0.46 ms with a quarter of them.
+// Computing a block's weights under the next block's scores, or four row tiles
+// in flight, did not help.
 #include "attn_device.h"
 
 namespace dosa {
