@@ -11,6 +11,9 @@ functions mirror the C entry points of include/dosa_indexer.h:
     dsa_prompt_attention, dsa_cache_append, dsa_cache_read, dsa_cache_attention,
     dsa_cache_weights, dsa_cache_evict and their workspace sizes: attention next
     to the indexer (attention.py)
+    dsa_pages_assign, dsa_pages_release, dsa_pages_append, dsa_pages_attention,
+    dsa_block_select, dsa_block_attention and their workspace sizes: paged keys
+    and values in 16 or 32 bits (pages.py)
 
 Importing the package never falls back to anything: if the shared library is
 missing, :func:`lib` raises.
@@ -42,7 +45,9 @@ EXPORTS = ("dosa_default_config", "dosa_workspace_size", "dosa_indexer_topk", "d
            "dosa_indexer_topk_noalloc", "dosa_status_string", "dosa_version", "dosa_profile_begin",
            "dosa_profile_end", "dsa_prompt_workspace_size", "dsa_prompt_attention", "dsa_cache_append",
            "dsa_cache_read", "dsa_cache_workspace_size", "dsa_cache_attention", "dsa_weights_workspace_size",
-           "dsa_cache_weights", "dsa_evict_workspace_size", "dsa_cache_evict")
+           "dsa_cache_weights", "dsa_evict_workspace_size", "dsa_cache_evict", "dsa_pages_assign",
+           "dsa_pages_release", "dsa_pages_append", "dsa_pages_workspace_size", "dsa_pages_attention",
+           "dsa_block_select", "dsa_block_workspace_size", "dsa_block_attention")
 
 NOALLOC_SCRATCH_BYTES = 128 << 20   # DOSA_NOALLOC_SCRATCH_BYTES
 
@@ -142,9 +147,10 @@ def lib():
         L.dosa_profile_begin.restype = ctypes.c_int
         L.dosa_profile_end.argtypes = [ctypes.POINTER(DosaKernelTime), i32]
         L.dosa_profile_end.restype = ctypes.c_int
-        from . import attention
+        from . import attention, pages
 
         attention.declare(L)
+        pages.declare(L)
         _lib = L
     return _lib
 
@@ -268,4 +274,18 @@ from .attention import (  # noqa: E402,F401
     evict_workspace_size,
     prompt_workspace_size,
     weights_workspace_size,
+)
+from .pages import (  # noqa: E402,F401
+    Blocks,
+    DsaBlocks,
+    DsaPages,
+    Pages,
+    block_workspace_size,
+    dsa_block_attention,
+    dsa_block_select,
+    dsa_pages_append,
+    dsa_pages_assign,
+    dsa_pages_attention,
+    dsa_pages_release,
+    pages_workspace_size,
 )

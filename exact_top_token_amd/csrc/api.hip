@@ -29,7 +29,9 @@ const char* const kPassNames[P_COUNT] = {"key_norms", "score_seed", "select_seed
                                          "score_survivor_tiles", "score_survivor_lists", "score_dense",
                                          "select_final", "prep", "probe", "seed_extra", "prompt_attention",
                                          "cache_attention", "attention_join", "cache_append", "cache_read",
-                                         "cache_weights", "weights_join", "evict_select", "evict_move"};
+                                         "cache_weights", "weights_join", "evict_select", "evict_move", "pages_assign",
+                                         "pages_release", "pages_append", "pages_attention", "block_select",
+                                         "block_attention"};
 
 // ---------------------------------------------------------------------------
 // The certificate stages of a call with a probe run on a side stream of the

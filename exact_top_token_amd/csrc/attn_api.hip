@@ -4,101 +4,13 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
-#include <cmath>
 #include <string>
-#include <vector>
 
-#include "attn_internal.h"
-#include "host_common.h"
+#include "attn_host.h"
 
 using namespace dosa;
 
 namespace {
-
-constexpr int64_t kMaxInt = (int64_t(1) << 31) - 1;
-constexpr int64_t kMaxTokens = (int64_t(1) << 31) - (1 << 16);   // positions a tile or two ahead stay int32
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-// Lengths, with a <= b for every sequence; total of each.
-int check_lens(int32_t batch, const int32_t* a, const int32_t* b, const char* an, const char* bn, int64_t* ta,
-               int64_t* tb) {
-  if (batch < 0 || (batch > 0 && (a == nullptr || b == nullptr)))
-    return fail(DOSA_ERR_INVALID_ARG, std::string("batch < 0 or ") + an + "/" + bn + " NULL");
-  *ta = *tb = 0;
-  for (int i = 0; i < batch; ++i) {
-    if (a[i] < 0 || b[i] < 0 || a[i] > b[i])
-      return fail(DOSA_ERR_INVALID_ARG, "sequence " + std::to_string(i) + ": need 0 <= " + an + " <= " + bn);
-    *ta += a[i];
-    *tb += b[i];
-  }
-  if (*ta > kMaxTokens || *tb > kMaxTokens) return fail(DOSA_ERR_UNSUPPORTED, "more than 2^31 - 2^16 tokens in a batch");
-  return DOSA_OK;
-}
-
-int check_heads(int32_t Hq, int32_t Hkv, int32_t d) {
-  if (Hq <= 0 || Hkv <= 0 || d <= 0 || Hq % Hkv != 0)
-    return fail(DOSA_ERR_INVALID_ARG, "Hq must be a positive multiple of Hkv, d positive");
-  if ((d != 64 && d != 128) || Hkv > 128 || Hq > 1024)
-    return fail(DOSA_ERR_UNSUPPORTED, "d must be 64 or 128, Hkv at most 128, Hq at most 1024");
-  return DOSA_OK;
-}
-
-// Rows of a sequence (queries times group heads) are int32 in the kernels.
-int check_row_count(int32_t batch, const int32_t* q_lens, int32_t Hq, int32_t Hkv) {
-  for (int b = 0; b < batch; ++b)
-    if ((int64_t)q_lens[b] * (Hq / Hkv) > (int64_t(1) << 30))
-      return fail(DOSA_ERR_UNSUPPORTED, "sequence " + std::to_string(b) + ": more than 2^30 query rows per kv head");
-  return DOSA_OK;
-}
-
-// The GPU counts a launch's threads in 32 bits.
-constexpr int64_t kLaunchThreads = int64_t(1) << 32;
-
-int check_launch(const char* what, int64_t threads) {
-  if (threads >= kLaunchThreads)
-    return fail(DOSA_ERR_UNSUPPORTED, std::string(what) + ": a launch of 2^32 threads or more, split the call");
-  return DOSA_OK;
-}
-
-int check_scale(float scale) {
-  // a subnormal scale would be flushed, and 0 times a masked score's -inf is not
-  // 0; the kernels multiply by scale * log2(e), and infinity times an equal
-  // maximum's difference of 0 is not 0 either
-  if (!(scale > 0.f) || !std::isnormal(scale) || !std::isfinite(scale * 1.44269504f))
-    return fail(DOSA_ERR_INVALID_ARG, "scale must be positive, not subnormal, and scale * log2(e) finite in fp32");
-  return DOSA_OK;
-}
-
-int check_float(int32_t dtype) {
-  if (dtype != DOSA_F32 && dtype != DOSA_BF16) return fail(DOSA_ERR_UNSUPPORTED, "dtype must be fp32 or bf16");
-  return DOSA_OK;
-}
-
-// A packed operand [tokens, H, d] with a stride between tokens: 16-byte rows,
-// offsets within 64 tokens in 31 bits.
-int check_rows(const char* name, const void* p, int64_t stride, int32_t H, int32_t d, int32_t dtype, int64_t tokens) {
-  if (tokens == 0) return DOSA_OK;
-  const int64_t size = dtype == DOSA_F32 ? 4 : 2;
-  if (p == nullptr) return fail(DOSA_ERR_INVALID_ARG, std::string(name) + " is NULL");
-  if (stride < (int64_t)H * d || (stride * size) % 16 != 0 || !aligned(p, 16))
-    return fail(DOSA_ERR_INVALID_ARG, std::string(name) + ": token rows must not overlap and must be 16-byte aligned");
-  if (stride > (int64_t(1) << 23)) return fail(DOSA_ERR_UNSUPPORTED, std::string(name) + ": token stride above 2^23");
-  return DOSA_OK;
-}
-
-int check_pages(const int32_t* table, int32_t num_pages, int32_t page_size, int32_t max_pages, int32_t batch,
-                const int32_t* kv_lens) {
-  if (page_size <= 0 || page_size % 16 != 0 || num_pages <= 0 || max_pages < 0)
-    return fail(DOSA_ERR_INVALID_ARG, "page_size must be a positive multiple of 16, num_pages positive");
-  if ((int64_t)num_pages * page_size > kMaxTokens) return fail(DOSA_ERR_UNSUPPORTED, "more than 2^31 - 2^16 cache slots");
-  for (int b = 0; b < batch; ++b) {
-    if (kv_lens[b] > 0 && table == nullptr) return fail(DOSA_ERR_INVALID_ARG, "page_table is NULL");
-    if ((int64_t)max_pages * page_size < kv_lens[b])
-      return fail(DOSA_ERR_INVALID_ARG, "sequence " + std::to_string(b) + ": its page table row ends before its keys");
-  }
-  return DOSA_OK;
-}
 
 int check_cache(const dsa_cache* c, int32_t batch, const int32_t* kv_lens) {
   if (c == nullptr || c->k_codes == nullptr || c->k_scales == nullptr || c->v_codes == nullptr ||
@@ -115,8 +27,6 @@ CacheView view(const dsa_cache* c) {
                    static_cast<uint8_t*>(c->v_codes), static_cast<uint8_t*>(c->v_scales),
                    c->page_table, c->page_size, c->max_pages, c->num_pages, c->Hkv};
 }
-
-size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
 // ---------------------------------------------------------------------------
 // Work split of the attention kernels.  A unit is one row tile of one kv head
@@ -140,10 +50,14 @@ struct AttnChunk {
 // times group heads) go to the tiled kernel, whose 256 rows share what is read
 // of the keys; all else to the wavefront kernel.
 constexpr int64_t kTiledRows = 16;
+constexpr int64_t kTiledPageRows = 32;   // over pages of rows: the wavefront kernel holds two tiles there
 constexpr int64_t kTiledResident = 256;  // workgroups of the tiled kernel: one a CU
 constexpr int64_t kTiledMinKeys = 512;
 
-bool takes_tiled(int src, int64_t rows) { return src == A_BF16 && rows > kTiledRows; }
+bool takes_tiled(int src, int64_t rows, bool sel) {
+  return !sel && ((src == A_BF16 && rows > kTiledRows) || (src == A_P16 && rows > kTiledPageRows));
+}
+int attn_classes(int src, int32_t topk) { return src == A_BF16 || (src == A_P16 && topk == 0) ? 2 : 1; }
 
 // Sequences b0.. of the batch that the kernel takes, at most kAttnSeqs with
 // queries; returns the sequence after the last one seen, or -1 if the launch
@@ -160,7 +74,7 @@ int plan_attn(AttnChunk& ch, int src, int d, bool tiled, int b0, int32_t batch, 
   int b = b0;
   int64_t most = 0;
   for (; b < batch && a.n_seq < kAttnSeqs; ++b) {
-    if (q_lens[b] > 0 && takes_tiled(src, (int64_t)q_lens[b] * a.group) == tiled) {
+    if (q_lens[b] > 0 && takes_tiled(src, (int64_t)q_lens[b] * a.group, sel) == tiled) {
       AttnSeq& s = a.s[a.n_seq++];
       s = AttnSeq{};
       s.q_row0 = (int32_t)*q_row;
@@ -231,12 +145,14 @@ int64_t attn_threads(const AttnChunk& ch, bool tiled) {
   return ch.a.n_units * int64_t(tiled ? 64 * kPromptWaves : 64);
 }
 
-// Bytes of partial results the call's launches need (each launch reuses them);
-// 0 if a launch would be too large.  threads: those of the largest launch.
+}  // namespace
+
+namespace dosa {
+
 size_t attn_workspace(int src, int32_t batch, const int32_t* q_lens, const int32_t* kv_lens, int32_t Hq, int32_t Hkv,
-                      int32_t d, int32_t topk, int64_t* threads = nullptr) {
+                      int32_t d, int32_t topk, int64_t* threads) {
   size_t most = 256;
-  for (int tiled = 0; tiled < (src == A_BF16 ? 2 : 1); ++tiled) {
+  for (int tiled = 0; tiled < attn_classes(src, topk); ++tiled) {
     int64_t qr = 0, kr = 0;
     for (int b = 0; b < batch;) {
       AttnChunk ch;
@@ -255,7 +171,7 @@ int run_attn(int src, const AttnArgs& base, int32_t batch, const int32_t* q_lens
   AttnChunk head[2];
   int next[2];
   int64_t qr[2] = {0, 0}, kr[2] = {0, 0}, threads = 0;
-  const int classes = src == A_BF16 ? 2 : 1;
+  const int classes = attn_classes(src, base.topk);
   size_t need = 256;
   for (int tiled = 0; tiled < classes; ++tiled) {
     head[tiled].a = base;
@@ -282,8 +198,10 @@ int run_attn(int src, const AttnArgs& base, int32_t batch, const int32_t* q_lens
       a.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + up256(rows * d * sizeof(float)));
       hipError_t e;
       if (a.n_units > 0) {
-        PassScope ps(src == A_F32 || src == A_BF16 ? P_PROMPT : P_ATTEND, stream);
-        e = tiled ? launch_prompt(d, a, stream) : launch_attn(src, d, a, stream);
+        PassScope ps(paged_rows(src) ? (a.idx != nullptr ? P_BLOCK_ATTEND : P_PAGES_ATTEND)
+                                     : (src == A_F32 || src == A_BF16 ? P_PROMPT : P_ATTEND), stream);
+        e = tiled ? launch_prompt(src, d, a, stream)
+                  : (paged_rows(src) ? launch_pages(src, d, a, stream) : launch_attn(src, d, a, stream));
         if (e != hipSuccess) return fail_hip(e, "attention kernel launch");
       }
       if (a.n_join > 0) {
@@ -298,6 +216,10 @@ int run_attn(int src, const AttnArgs& base, int32_t batch, const int32_t* q_lens
   }
   return DOSA_OK;
 }
+
+}  // namespace dosa
+
+namespace {
 
 // ---------------------------------------------------------------------------
 // Work split of the weights kernels.
@@ -480,26 +402,6 @@ size_t evict_workspace(int32_t batch, const int32_t* kv_lens, const int32_t* new
   int64_t n = 0;
   for (int b = 0; b < batch; ++b) n += evict_ints(kv_lens[b], new_lens[b]);
   return up256((size_t)std::max<int64_t>(n, 1) * sizeof(int32_t));
-}
-
-template <class F>
-int guarded(F f) {
-  try {
-    return f();
-  } catch (...) {
-    g_err = "internal error";
-    return DOSA_ERR_HIP;
-  }
-}
-
-template <class F>
-size_t guarded_size(F f) {
-  try {
-    return f();
-  } catch (...) {
-    g_err = "internal error";
-    return 0;
-  }
 }
 
 }  // namespace

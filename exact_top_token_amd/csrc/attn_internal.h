@@ -20,9 +20,22 @@ struct CacheView {
 };
 
 // Where an attention kernel finds its keys and values, and its queries' type:
-// contiguous fp32 or bf16 rows, or the 4-bit cache read for bf16 or for fp32
-// queries.
-enum AttnSrc : int { A_F32 = 0, A_BF16 = 1, A_MX = 2, A_MX32 = 3 };
+// contiguous fp32 or bf16 rows, the 4-bit cache read for bf16 or for fp32
+// queries, or pages of fp32 or bf16 rows.
+enum AttnSrc : int { A_F32 = 0, A_BF16 = 1, A_MX = 2, A_MX32 = 3, A_P32 = 4, A_P16 = 5 };
+constexpr bool paged_rows(int src) { return src == A_P32 || src == A_P16; }
+
+// Division by a positive 32-bit number: the high half of a product falls short
+// of the quotient by at most 1.
+struct Div {
+  uint32_t by, mul;
+  __host__ __device__ Div() : by(1), mul(0xffffffffu) {}
+  __host__ explicit Div(uint32_t d) : by(d), mul(d == 1 ? 0xffffffffu : (uint32_t)((uint64_t(1) << 32) / d)) {}
+  __device__ __forceinline__ uint32_t quot(uint32_t n) const {
+    const uint32_t q = __umulhi(n, mul);
+    return n - q * by >= by ? q + 1 : q;
+  }
+};
 
 struct AttnSeq {
   int32_t unit0;      // first unit (wavefront task) of the sequence in this launch
@@ -38,10 +51,10 @@ struct AttnSeq {
 
 struct AttnArgs {
   const void* q;
-  const void* k;      // contiguous sources
+  const void* k;      // contiguous sources; pools of paged rows
   const void* v;
-  CacheView cache;    // cache sources
-  const int32_t* idx; // selected keys [total_q, topk], or NULL
+  CacheView cache;    // cache sources; page table and geometry of paged rows
+  const int32_t* idx; // selected keys [total_q, topk], blocks [total_q, Hkv, topk / block], or NULL
   void* out;          // [total_q, Hq, d] of q's type
   float* lse;         // [total_q, Hq] or NULL
   float* part_o;      // partial outputs [parts, 16 * row tiles, d]
@@ -49,6 +62,8 @@ struct AttnArgs {
   int64_t q_stride, k_stride, v_stride;   // elements between token rows
   int32_t topk, Hq, Hkv, group;           // group = Hq / Hkv
   float scale;
+  int32_t block;                          // keys of a selected block (a power of two), paged rows only
+  Div page_div;                           // by page_size, paged rows only
   int32_t n_seq, n_units, n_join, rt, hp; // rt: 16-row tiles per unit and head, hp: heads per unit
   AttnSeq s[kAttnSeqs];
 };
@@ -60,17 +75,20 @@ struct AttnArgs {
 // over 871K keys 242 us, 330 us as one tile of a head pair (which does not
 // spill).  A launch takes what its largest sequence needs: one such sequence
 // among 31 of 2 queries costs 241 instead of 207 us.
-constexpr int attn_max_rt(int src, int d) { return src == A_MX || (src == A_F32 && d == 64) ? 2 : 1; }
+constexpr int attn_max_rt(int src, int d) {
+  return src == A_MX || src == A_P16 || ((src == A_F32 || src == A_P32) && d == 64) ? 2 : 1;
+}
 
 // Bf16 prompts over LDS tiles: units are row tiles of kPromptWaves * 32 rows of
 // one kv head, over all their keys.
 constexpr int kPromptWaves = 8;
-hipError_t launch_prompt(int d, const AttnArgs& p, hipStream_t s);
+hipError_t launch_prompt(int src, int d, const AttnArgs& p, hipStream_t s);
 
 // Heads one wavefront takes together: pairs where the rows of the call are one
 // tile, so that the registers are there.
 constexpr int attn_heads(int src, int rt, int Hkv) { return src == A_MX && rt == 1 && Hkv % 2 == 0 ? 2 : 1; }
 hipError_t launch_attn(int src, int d, const AttnArgs& p, hipStream_t s);
+hipError_t launch_pages(int src, int d, const AttnArgs& p, hipStream_t s);
 hipError_t launch_attn_join(int src, int d, const AttnArgs& p, hipStream_t s);
 
 // Cache write and read-back.

@@ -64,8 +64,13 @@ __device__ __forceinline__ int v_chunk(int r, int c) {
   return D == 128 ? c ^ ((r & 3) << 2) : c ^ (((r >> 1) & 1) << 2);
 }
 
-template <int D, int NW>
+// Where the keys are: contiguous rows, pages of a multiple of 64 rows (a tile
+// lies in one page), pages of any multiple of 16.
+enum Place : int { L_ROWS = 0, L_PAGES64 = 1, L_PAGES16 = 2 };
+
+template <int D, int NW, int PLACE>
 __global__ __launch_bounds__(64 * NW, 2) void prompt_kernel(const AttnArgs p) {
+  constexpr bool PAGED = PLACE != L_ROWS;
   constexpr int CH = D / 8;              // 16-byte chunks of a row
   constexpr int TILE = kKeys * D * 2;    // bytes of a tile
   constexpr int NS = D / 16, NT = D / 32;
@@ -109,8 +114,8 @@ __global__ __launch_bounds__(64 * NW, 2) void prompt_kernel(const AttnArgs p) {
   float m = -INFINITY, l = 0.f;
   const float c = p.scale * kLog2e;
 
-  const uint16_t* kg = static_cast<const uint16_t*>(p.k) + sq.key_base * p.k_stride + head * D;
-  const uint16_t* vg = static_cast<const uint16_t*>(p.v) + sq.key_base * p.v_stride + head * D;
+  const uint16_t* kg = static_cast<const uint16_t*>(p.k) + (PAGED ? 0 : sq.key_base) * p.k_stride + head * D;
+  const uint16_t* vg = static_cast<const uint16_t*>(p.v) + (PAGED ? 0 : sq.key_base) * p.v_stride + head * D;
   // a wavefront instruction fills 1 KB: 64 / CH rows
   constexpr int RPI = 64 / CH, PER = kKeys / RPI / NW;
   const int lr = lane / CH, lc = lane % CH;
@@ -125,6 +130,69 @@ __global__ __launch_bounds__(64 * NW, 2) void prompt_kernel(const AttnArgs p) {
       const int ch = which == 0 ? k_chunk<D>(row, lc) : v_chunk<D>(row, lc);
       __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(from + src * (int)stride + 8 * ch),
                                        (__attribute__((address_space(3))) void*)(&lds[which][i & 1][at * D * 2]), 16, 0, 0);
+    }
+  };
+
+  // The same over pages.  A tile's page numbers (one of 64 rows, or of each 16)
+  // are looked up through the scalar cache a turn before its keys are fetched and
+  // kept until its values have been.  A wavefront's rows of a tile lie in 16
+  // rows, `part`; those past the last visible key repeat it.  Rows without a page
+  // are read from page 0: their scores are masked, and their values, which a
+  // weight of 0 is still multiplied by, become zeros in LDS.
+  typedef __attribute__((address_space(4))) const int32_t scalar_i32;
+  struct Pages {
+    int32_t page[PLACE == L_PAGES16 ? 4 : 1];
+    int32_t off;                        // of this wavefront's rows in their page
+    int32_t gone;                       // bit i: rows 16i.. have no page
+  };
+  constexpr int N16 = PLACE == L_PAGES16 ? 4 : 1;
+  const int part = wave * PER * RPI / 16;
+  scalar_i32* const table = PAGED ? (scalar_i32*)(p.cache.table + (int64_t)sq.b * p.cache.max_pages) : nullptr;
+  auto look = [&](int i) -> Pages {
+    Pages x;
+    const int key0 = key_lo + i * kKeys, end = wg_end - 1;
+    x.off = 0;
+#pragma unroll
+    for (int a = 0; a < N16; ++a) {
+      // 16 (64) rows past the last key: those that hold it
+      const int at = key0 + 16 * a, here = at <= end ? at : end & ~(64 / N16 - 1);
+      const int pg = p.page_div.quot(here);
+      x.page[a] = table[pg];
+      if (N16 == 1 || a == part) x.off = here - pg * p.cache.page_size;
+    }
+    return x;
+  };
+  auto judge = [&](Pages& x) {
+    x.gone = 0;
+#pragma unroll
+    for (int a = 0; a < N16; ++a) {
+      const bool bad = (uint32_t)x.page[a] >= (uint32_t)p.cache.num_pages;
+      x.gone |= bad ? (N16 == 1 ? 15 : 1 << a) : 0;
+      x.page[a] = bad ? 0 : x.page[a];
+    }
+  };
+  auto fetch_page = [&](int which, const uint16_t* base, int64_t stride, int i, const Pages& pg) {
+    int page = pg.page[0];
+#pragma unroll
+    for (int a = 1; a < N16; ++a) page = a == part ? pg.page[a] : page;
+    const int first_row = N16 == 1 ? 0 : 16 * part;     // of the rows that `off` points at
+    const int key0 = key_lo + i * kKeys + first_row, end = wg_end - 1;
+    const int lim = end - (key0 <= end ? key0 : end & ~(64 / N16 - 1));
+    const uint16_t* from = base + ((int64_t)page * p.cache.page_size + pg.off) * stride;
+#pragma unroll
+    for (int x = 0; x < PER; ++x) {
+      const int at = (wave * PER + x) * RPI, row = at + lr, r = row - first_row, src = r < lim ? r : lim;
+      const int ch = which == 0 ? k_chunk<D>(row, lc) : v_chunk<D>(row, lc);
+      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(from + src * (int)stride + 8 * ch),
+                                       (__attribute__((address_space(3))) void*)(&lds[which][i & 1][at * D * 2]), 16, 0, 0);
+    }
+  };
+  // values without a page of tile i, which have arrived, become zeros
+  auto clear = [&](int i, const Pages& pg) {
+    if ((pg.gone >> part) & 1) {
+#pragma unroll
+      for (int x = 0; x < PER; ++x)
+        *reinterpret_cast<i4*>(&lds[1][i & 1][(wave * PER + x) * RPI * D * 2 + 16 * lane]) = i4{0, 0, 0, 0};
     }
   };
 
@@ -158,14 +226,17 @@ __global__ __launch_bounds__(64 * NW, 2) void prompt_kernel(const AttnArgs p) {
   };
   // One tile: the maximum of its scores, then its weights while the matrix
   // unit works on the next tile's scores, then its weighted values.
-  auto step = [&](f16v* sc, f16v* next, int t) {
+  auto step = [&](f16v* sc, f16v* next, int t, int gone) {
     const int key0 = key_lo + t * kKeys;
-    if (key0 + kKeys > first || key0 + kKeys > wg_end) {
+    if (key0 + kKeys > first || key0 + kKeys > wg_end || (PAGED && gone != 0)) {
 #pragma unroll
       for (int a = 0; a < 2; ++a)
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-          sc[a][e] = key0 + 32 * a + 8 * (e >> 2) + 4 * h + (e & 3) >= stop ? -INFINITY : sc[a][e];
+        for (int e = 0; e < 16; ++e) {
+          bool hide = key0 + 32 * a + 8 * (e >> 2) + 4 * h + (e & 3) >= stop;
+          if constexpr (PAGED) hide = hide || ((gone >> (2 * a + (e >> 3))) & 1) != 0;
+          sc[a][e] = hide ? -INFINITY : sc[a][e];
+        }
     }
     float top = sc[0][0];
 #pragma unroll
@@ -241,7 +312,38 @@ __global__ __launch_bounds__(64 * NW, 2) void prompt_kernel(const AttnArgs p) {
     __syncthreads();
   };
 
-  if (tiles > 0) {
+  if constexpr (PAGED) {
+    if (tiles > 0) {
+      f16v sa[2], sb[2];
+      // pages of the tile whose values are used, of the next one, of the one after
+      Pages p0 = look(0), p1 = look(1), p2 = look(2);
+      judge(p0);
+      judge(p1);
+      fetch_page(0, kg, p.k_stride, 0, p0);
+      ready();
+      if (tiles > 1) fetch_page(0, kg, p.k_stride, 1, p1);
+      fetch_page(1, vg, p.v_stride, 0, p0);
+      if (mine > 0) scores(sa, 0);
+      auto turn = [&](f16v* sc, f16v* next, int t) {
+        __builtin_amdgcn_s_waitcnt(0x0f70);
+        clear(t, p0);
+        __syncthreads();
+        judge(p2);
+        if (t + 2 < tiles) fetch_page(0, kg, p.k_stride, t + 2, p2);
+        if (t + 1 < tiles) fetch_page(1, vg, p.v_stride, t + 1, p1);
+        const int gone = p0.gone;
+        p0 = p1;
+        p1 = p2;
+        p2 = look(t + 3);
+        if (t < mine) step(sc, next, t, gone);
+      };
+#pragma unroll 1
+      for (int t = 0; t < tiles; t += 2) {
+        turn(sa, sb, t);
+        if (t + 1 < tiles) turn(sb, sa, t + 1);
+      }
+    }
+  } else if (tiles > 0) {
     f16v sa[2], sb[2];
     fetch(0, kg, p.k_stride, 0);
     ready();
@@ -252,7 +354,7 @@ __global__ __launch_bounds__(64 * NW, 2) void prompt_kernel(const AttnArgs p) {
       ready();
       if (t + 2 < tiles) fetch(0, kg, p.k_stride, t + 2);
       if (t + 1 < tiles) fetch(1, vg, p.v_stride, t + 1);
-      if (t < mine) step(sc, next, t);
+      if (t < mine) step(sc, next, t, 0);
     };
 #pragma unroll 1
     for (int t = 0; t < tiles; t += 2) {
@@ -283,8 +385,9 @@ __global__ __launch_bounds__(64 * NW, 2) void prompt_kernel(const AttnArgs p) {
   }
   if (!ok) return;
   const int64_t row = (int64_t)(sq.q_row0 + query) * p.Hq + qh;
-  if (p.lse != nullptr && h == 0) p.lse[row] = fmaf(m, p.scale, __builtin_amdgcn_logf(l) * kLn2);
-  const float inv = 1.f / l;
+  const bool none = PAGED && !(l > 0.f);     // every key that the row would see is without a page
+  if (p.lse != nullptr && h == 0) p.lse[row] = none ? -INFINITY : fmaf(m, p.scale, __builtin_amdgcn_logf(l) * kLn2);
+  const float inv = none ? 0.f : 1.f / l;
   uint16_t* dst = static_cast<uint16_t*>(p.out) + row * D;
 #pragma unroll
   for (int j = 0; j < NT; ++j)
@@ -299,12 +402,22 @@ __global__ __launch_bounds__(64 * NW, 2) void prompt_kernel(const AttnArgs p) {
 
 }  // namespace
 
-hipError_t launch_prompt(int d, const AttnArgs& p, hipStream_t s) {
-  if (p.n_units == 0) return hipSuccess;
+namespace {
+
+template <int PLACE>
+hipError_t go(int d, const AttnArgs& p, hipStream_t s) {
   const dim3 grid((unsigned)p.n_units), block(64 * kPromptWaves);
-  if (d == 128) prompt_kernel<128, kPromptWaves><<<grid, block, 0, s>>>(p);
-  else prompt_kernel<64, kPromptWaves><<<grid, block, 0, s>>>(p);
+  if (d == 128) prompt_kernel<128, kPromptWaves, PLACE><<<grid, block, 0, s>>>(p);
+  else prompt_kernel<64, kPromptWaves, PLACE><<<grid, block, 0, s>>>(p);
   return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_prompt(int src, int d, const AttnArgs& p, hipStream_t s) {
+  if (p.n_units == 0) return hipSuccess;
+  if (!paged_rows(src)) return go<L_ROWS>(d, p, s);
+  return p.cache.page_size % kKeys == 0 ? go<L_PAGES64>(d, p, s) : go<L_PAGES16>(d, p, s);
 }
 
 }  // namespace dosa

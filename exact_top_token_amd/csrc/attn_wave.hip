@@ -763,7 +763,7 @@ hipError_t join(const AttnArgs& p, hipStream_t s) {
 
 hipError_t launch_attn_join(int src, int d, const AttnArgs& p, hipStream_t s) {
   if (p.n_join == 0) return hipSuccess;
-  const bool f32 = src == A_F32 || src == A_MX32;
+  const bool f32 = src == A_F32 || src == A_MX32 || src == A_P32;
   if (d == 128) return f32 ? join<true, 128>(p, s) : join<false, 128>(p, s);
   return f32 ? join<true, 64>(p, s) : join<false, 64>(p, s);
 }

@@ -15,7 +15,8 @@ extern thread_local std::string g_err;
 
 enum PassId { P_NORMS = 0, P_SCORE_SEED, P_SELECT_SEED, P_PLAN, P_BOUND, P_COMPACT, P_SURV_TILES, P_SURV_LISTS,
               P_SCORE_DENSE, P_SELECT_FINAL, P_PREP, P_PROBE, P_SEED_EXTRA, P_PROMPT, P_ATTEND, P_ATTEND_JOIN,
-              P_APPEND, P_READ, P_WEIGHTS, P_WEIGHTS_JOIN, P_EVICT_SELECT, P_EVICT_MOVE, P_COUNT };
+              P_APPEND, P_READ, P_WEIGHTS, P_WEIGHTS_JOIN, P_EVICT_SELECT, P_EVICT_MOVE, P_PAGES_ASSIGN,
+              P_PAGES_RELEASE, P_PAGES_APPEND, P_PAGES_ATTEND, P_BLOCK_SELECT, P_BLOCK_ATTEND, P_COUNT };
 
 struct Profiler {
   bool on = false;

@@ -424,6 +424,120 @@ int dsa_cache_evict(const float* acc, const int32_t* pos, const int32_t* page_ta
                     int32_t prefix, int32_t window, const dsa_evict_array* arrays, int32_t n_arrays,
                     int32_t* out_src, int32_t out_stride, void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Paged keys and values in 16 or 32 bits: page tables and slot maps from the
+ * sequences' lengths, the write of new rows, attention of the new tokens over
+ * the pages, and block attention: a few blocks per query and kv head, chosen
+ * by a cheap score on summaries of the blocks, and attention over their keys.
+ * What is common to the calls above holds here too (packed operands, host
+ * lengths, page tables, streams, workspaces, sums in fp32).
+ */
+
+/* Page tables and slot maps.  Sequence b grows by q_lens[b] tokens to
+ * kv_lens[b]; the pages that it needs beyond the ceil((kv_len - q_len) /
+ * page_size) that it has are taken from the end of the free list, in the order
+ * of the sequences and their pages.
+ *   page_table [batch, max_pages] int32: entries of the new pages are written,
+ *              no others
+ *   free_pages [num_pages] int32: its first *free_count entries are pages that
+ *              nobody holds; not written
+ *   free_count HOST: pages left, updated by the call.  Fewer than needed:
+ *              DOSA_ERR_INVALID_ARG, and nothing changes
+ *   slots      [total_q] int32 or NULL: the pool slot of each new token, page *
+ *              page_size + place in the page, -1 where the page is none of
+ *              0..num_pages-1 (rows the user writes, such as the indexer's keys)
+ *   positions  [total_q] int32 or NULL: its position, kv_len - q_len + i
+ * Counts are host numbers like lengths: a captured graph keeps them. */
+int dsa_pages_assign(int32_t* page_table, int32_t max_pages, int32_t page_size, int32_t num_pages,
+                     const int32_t* free_pages, int32_t* free_count, const int32_t* q_lens, const int32_t* kv_lens,
+                     int32_t batch, int32_t* slots, int32_t* positions, void* stream);
+
+/* The pages behind the first ceil(new_len / page_size) of each sequence go back
+ * to the end of the free list, the last page first, and their table entries
+ * become -1 (0 <= new_len <= kv_len; a finished sequence's new_len is 0).  A
+ * page that sequences share must be given back once. */
+int dsa_pages_release(int32_t* page_table, int32_t max_pages, int32_t page_size, int32_t num_pages, int32_t* free_pages,
+                      int32_t* free_count, const int32_t* new_lens, const int32_t* kv_lens, int32_t batch, void* stream);
+
+/* Keys and values in pages, k and v [num_pages, page_size, Hkv, d] of dtype
+ * (DOSA_F32, DOSA_BF16), 16-byte aligned; addressed as dsa_cache is, and with
+ * the same rules for table entries that name no page, slots past a kv_len, and
+ * pages that sequences share. */
+typedef struct {
+  void* k;
+  void* v;
+  const int32_t* page_table;   /* DEVICE [batch, max_pages] */
+  int32_t dtype;
+  int32_t num_pages, page_size, max_pages;
+  int32_t Hkv, d;
+} dsa_pages;
+
+/* Summaries of blocks of `block` consecutive positions (16, 32, 64 or 128; it
+ * divides page_size).  A block's summary is the mean of its keys in 8 bits:
+ *   codes  [num_pages, page_size / block, Hkv, d] integers -127..127, 16-byte
+ *          aligned
+ *   scales [num_pages, page_size / block, Hkv] bytes: byte e scales a row by
+ *          2^(e-127), the smallest e in 1..254 for which every element of the
+ *          mean is below 127.5 scales in magnitude; codes are rounded to the
+ *          nearest, ties to even.  The mean is summed in 64 bits. */
+typedef struct {
+  int8_t* codes;
+  uint8_t* scales;
+  int32_t num_pages, page_size, block;
+  int32_t Hkv, d;
+  int32_t reserved;            /* set to 0 */
+} dsa_blocks;
+
+/* Write the q_lens[b] newest tokens of each sequence, k, v [total_q, Hkv, d] of
+ * the pages' dtype, into their slots, bit for bit.  blocks (of the same pages)
+ * or NULL: the summaries of the blocks that these tokens make complete are
+ * written too, earlier keys of theirs read from the pages.  After an eviction
+ * (which moves keys between blocks) summaries are those of the old order. */
+int dsa_pages_append(const dsa_pages* pages, const dsa_blocks* blocks, const void* k, int64_t k_stride, const void* v,
+                     int64_t v_stride, const int32_t* q_lens, const int32_t* kv_lens, int32_t batch, void* stream);
+
+/* Attention of the q_lens[b] newest tokens over the pages, themselves included
+ * (append first): chunks of prompts and single tokens mix.  q, out [total_q, Hq,
+ * d] of the pages' dtype; out, lse as dsa_cache_attention.  bf16: softmax weights
+ * are rounded to bf16 for their product with v.  A page that the table does not
+ * name is not seen. */
+size_t dsa_pages_workspace_size(int32_t batch, const int32_t* q_lens, const int32_t* kv_lens, int32_t Hq, int32_t Hkv,
+                                int32_t d, int32_t dtype);
+int dsa_pages_attention(const dsa_pages* pages, const void* q, int64_t q_stride, const int32_t* q_lens,
+                        const int32_t* kv_lens, int32_t batch, int32_t Hq, float scale, void* out, float* lse,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
+/* Choose topn blocks for each query and kv head.  A query in block o (its
+ * position / block) gets the first `sinks` blocks, the latest `local` up to and
+ * with o, and of the others in front of them those of largest score, ties to the
+ * lower index; all of them where there are no more than topn.
+ *   idx   [total_q, Hkv, topn] int32: ascending block indices, -1 behind
+ *   score of block j for the group's query heads h:
+ *         2^(e_j - 142) * max_h 2^max(f_h - f, -100) * (a_h . c_j)
+ *         with c_j, e_j the block's codes and scale byte, a_h the codes of query
+ *         head h rounded as a summary with scale 2^f_h (f_h in -126..127), f =
+ *         max_h f_h, rounded to fp32 once.  All but that rounding, which only
+ *         subnormal results need, is exact: the choice does not depend on how
+ *         sums are ordered.  A block whose table entry names no page scores -inf.
+ * 0 <= sinks, 1 <= local, sinks + local <= topn <= 4096; at most 32768 blocks in
+ * a sequence.  q [total_q, Hq, d] of q_dtype.  Blocks in front of o must have
+ * been complete when they were last appended to (they are, after appends with
+ * these summaries). */
+int dsa_block_select(const dsa_blocks* blocks, const int32_t* page_table, int32_t max_pages, const void* q,
+                     int64_t q_stride, int32_t q_dtype, const int32_t* q_lens, const int32_t* kv_lens, int32_t batch,
+                     int32_t Hq, int32_t sinks, int32_t local, int32_t* idx, int32_t topn, void* stream);
+
+/* Attention over listed blocks: query row t of kv head h reads the keys of the
+ * blocks idx[t, h, 0..topn-1] that are not behind its position.  Entries that
+ * are negative or behind the query's own block are skipped, a block listed twice
+ * counts twice.  topn * block <= 2^20.  Otherwise as dsa_pages_attention. */
+size_t dsa_block_workspace_size(int32_t batch, const int32_t* q_lens, const int32_t* kv_lens, int32_t Hq, int32_t Hkv,
+                                int32_t d, int32_t dtype, int32_t block, int32_t topn);
+int dsa_block_attention(const dsa_pages* pages, const void* q, int64_t q_stride, const int32_t* q_lens,
+                        const int32_t* kv_lens, int32_t batch, int32_t Hq, const int32_t* idx, int32_t topn,
+                        int32_t block, float scale, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                        void* stream);
+
 /* Per-pass timing (tracing for benchmarks).  Between dosa_profile_begin()
  * and dosa_profile_end(), every kernel the calling thread enqueues through
  * this library is bracketed by two HIP events recorded on the kernel's own
@@ -434,7 +548,8 @@ int dsa_cache_evict(const float* acc, const int32_t* pos, const int32_t* page_ta
  * Pass names: prep, key_norms, score_seed, select_seed, plan, bound, compact,
  * score_survivor_tiles, score_survivor_lists, score_dense, select_final,
  * prompt_attention, cache_attention, attention_join, cache_append,
- * cache_read, cache_weights, weights_join, evict_select, evict_move. */
+ * cache_read, cache_weights, weights_join, evict_select, evict_move, pages_assign,
+ * pages_release, pages_append, pages_attention, block_select, block_attention. */
 typedef struct {
   const char* name;   /* static string */
   int32_t launches;
