@@ -54,16 +54,19 @@ constexpr int64_t kTiledPageRows = 32;   // over pages of rows: the wavefront ke
 constexpr int64_t kTiledResident = 256;  // workgroups of the tiled kernel: one a CU
 constexpr int64_t kTiledMinKeys = 512;
 
+constexpr int64_t kTiledBlockRows = 64;  // over listed blocks: half a workgroup's rows
+
 bool takes_tiled(int src, int64_t rows, bool sel) {
-  return !sel && ((src == A_BF16 && rows > kTiledRows) || (src == A_P16 && rows > kTiledPageRows));
+  if (sel) return src == A_P16 && rows > kTiledBlockRows;
+  return (src == A_BF16 && rows > kTiledRows) || (src == A_P16 && rows > kTiledPageRows);
 }
-int attn_classes(int src, int32_t topk) { return src == A_BF16 || (src == A_P16 && topk == 0) ? 2 : 1; }
+int attn_classes(int src) { return src == A_BF16 || src == A_P16 ? 2 : 1; }
 
 // Sequences b0.. of the batch that the kernel takes, at most kAttnSeqs with
 // queries; returns the sequence after the last one seen, or -1 if the launch
 // would be too large.
 int plan_attn(AttnChunk& ch, int src, int d, bool tiled, int b0, int32_t batch, const int32_t* q_lens, const int32_t* kv_lens,
-              int32_t Hq, int32_t Hkv, int32_t topk, int64_t* q_row, int64_t* k_row) {
+              int32_t Hq, int32_t Hkv, int32_t topk, int32_t block, int64_t* q_row, int64_t* k_row) {
   AttnArgs& a = ch.a;
   const bool sel = topk > 0;
   a.Hq = Hq;
@@ -87,18 +90,22 @@ int plan_attn(AttnChunk& ch, int src, int d, bool tiled, int b0, int32_t batch, 
     *q_row += q_lens[b];
     *k_row += kv_lens[b];
   }
-  a.rt = tiled ? 2 * kPromptWaves : (most > 16 ? attn_max_rt(src, d) : 1);
+  a.rt = tiled ? (sel ? 1 : 2 * kPromptWaves) : (most > 16 ? attn_max_rt(src, d) : 1);
   a.hp = tiled ? 1 : attn_heads(src, a.rt, Hkv);
   const int64_t tile = 16 * a.rt, heads = Hkv / a.hp;
+  const int64_t per = tiled && sel ? kBlockTileWaves : 1;      // row tiles of a unit
+  a.tok = per > 1 ? std::max(1, std::min((int32_t)tile / a.group, kBlockTok)) : 1;
+  const int64_t gran = std::max(64, block);
   auto tiles = [&](const AttnSeq& s) -> int64_t {
-    return sel ? (int64_t)s.q_len * ((a.group + tile - 1) / tile) : ((int64_t)s.q_len * a.group + tile - 1) / tile;
+    return sel ? ((int64_t)s.q_len + a.tok - 1) / a.tok * ((a.group + tile - 1) / tile)
+               : ((int64_t)s.q_len * a.group + tile - 1) / tile;
   };
   auto keys = [&](const AttnSeq& s) -> int64_t { return sel ? topk : s.kv_len; };
   std::stable_sort(a.s, a.s + a.n_seq, [&](const AttnSeq& x, const AttnSeq& y) { return keys(x) > keys(y); });
-  const int64_t cap = kRounds * (tiled ? kTiledResident : kResident);
+  const int64_t cap = kRounds * (tiled ? (sel ? 2 * kTiledResident : kTiledResident) : kResident);
   auto units_at = [&](int64_t len) {
     int64_t n = 0;
-    for (int i = 0; i < a.n_seq; ++i) n += tiles(a.s[i]) * heads * ((keys(a.s[i]) + len - 1) / len);
+    for (int i = 0; i < a.n_seq; ++i) n += (tiles(a.s[i]) + per - 1) / per * heads * ((keys(a.s[i]) + len - 1) / len);
     return n;
   };
   // shortest range length in steps of 64 that keeps to the cap, or one range each
@@ -114,7 +121,7 @@ int plan_attn(AttnChunk& ch, int src, int d, bool tiled, int b0, int32_t batch, 
     AttnSeq& s = a.s[i];
     const int64_t k = keys(s), nrt = tiles(s);
     int64_t n = std::max<int64_t>(1, (k + len - 1) / len);
-    const int64_t sl = ((k + n - 1) / n + 63) / 64 * 64;
+    const int64_t sl = ((k + n - 1) / n + gran - 1) / gran * gran;
     n = (k + sl - 1) / sl;
     if (nrt * n * Hkv > kMaxInt || units + nrt * n * Hkv > kMaxInt) return -1;
     s.n_rt = (int32_t)nrt;
@@ -123,7 +130,7 @@ int plan_attn(AttnChunk& ch, int src, int d, bool tiled, int b0, int32_t batch, 
     s.unit0 = (int32_t)units;
     s.join0 = (int32_t)join;
     s.part0 = (int32_t)parts;
-    units += nrt * n * heads;
+    units += (nrt + per - 1) / per * n * heads;
     if (n > 1) {
       join += (int64_t)s.q_len * Hq;
       parts += nrt * n * Hkv;
@@ -132,13 +139,20 @@ int plan_attn(AttnChunk& ch, int src, int d, bool tiled, int b0, int32_t batch, 
   }
   a.n_units = (int32_t)units;
   a.n_join = (int32_t)join;
+  // entries of a unit's lists, over the longest range
+  a.merged_stride = 0;
+  if (per > 1)
+    for (int i = 0; i < a.n_seq; ++i)
+      a.merged_stride = std::max(a.merged_stride, (int32_t)(per * a.tok * (a.s[i].split_len / block)) + kBlockEnds);
   ch.parts = parts;
   return b;
 }
 
+size_t merged_bytes(const AttnChunk& ch) { return up256((size_t)ch.a.n_units * ch.a.merged_stride * sizeof(int4)); }
+
 size_t part_bytes(const AttnChunk& ch, int d) {
   const size_t rows = (size_t)ch.parts * 16 * ch.a.rt;
-  return up256(rows * d * sizeof(float)) + up256(rows * 2 * sizeof(float));
+  return merged_bytes(ch) + up256(rows * d * sizeof(float)) + up256(rows * 2 * sizeof(float));
 }
 
 int64_t attn_threads(const AttnChunk& ch, bool tiled) {
@@ -150,13 +164,13 @@ int64_t attn_threads(const AttnChunk& ch, bool tiled) {
 namespace dosa {
 
 size_t attn_workspace(int src, int32_t batch, const int32_t* q_lens, const int32_t* kv_lens, int32_t Hq, int32_t Hkv,
-                      int32_t d, int32_t topk, int64_t* threads) {
+                      int32_t d, int32_t topk, int32_t block, int64_t* threads) {
   size_t most = 256;
-  for (int tiled = 0; tiled < attn_classes(src, topk); ++tiled) {
+  for (int tiled = 0; tiled < attn_classes(src); ++tiled) {
     int64_t qr = 0, kr = 0;
     for (int b = 0; b < batch;) {
       AttnChunk ch;
-      b = plan_attn(ch, src, d, tiled != 0, b, batch, q_lens, kv_lens, Hq, Hkv, topk, &qr, &kr);
+      b = plan_attn(ch, src, d, tiled != 0, b, batch, q_lens, kv_lens, Hq, Hkv, topk, block, &qr, &kr);
       if (b < 0) return 0;
       most = std::max(most, part_bytes(ch, d));
       if (threads != nullptr) *threads = std::max(*threads, attn_threads(ch, tiled != 0));
@@ -171,21 +185,21 @@ int run_attn(int src, const AttnArgs& base, int32_t batch, const int32_t* q_lens
   AttnChunk head[2];
   int next[2];
   int64_t qr[2] = {0, 0}, kr[2] = {0, 0}, threads = 0;
-  const int classes = attn_classes(src, base.topk);
+  const int classes = attn_classes(src);
   size_t need = 256;
   for (int tiled = 0; tiled < classes; ++tiled) {
     head[tiled].a = base;
     next[tiled] = plan_attn(head[tiled], src, d, tiled != 0, 0, batch, q_lens, kv_lens, base.Hq, base.Hkv, base.topk,
-                            &qr[tiled], &kr[tiled]);
+                            base.block, &qr[tiled], &kr[tiled]);
     if (next[tiled] < 0) return fail(DOSA_ERR_UNSUPPORTED, "too many row tiles and key ranges for one launch");
     need = std::max(need, part_bytes(head[tiled], d));
     threads = std::max(threads, attn_threads(head[tiled], tiled != 0));
   }
   if (next[0] < batch || next[classes - 1] < batch) {
-    need = attn_workspace(src, batch, q_lens, kv_lens, base.Hq, base.Hkv, d, base.topk, &threads);
+    need = attn_workspace(src, batch, q_lens, kv_lens, base.Hq, base.Hkv, d, base.topk, base.block, &threads);
     if (need == 0) return fail(DOSA_ERR_UNSUPPORTED, "too many row tiles and key ranges for one launch");
   }
-  const int st = check_launch("attention", threads + 64 * 8);   // its last workgroup may be partly empty
+  const int st = check_launch("attention", threads + 64 * 8 * 8);   // its last workgroups may be partly empty
   if (st != DOSA_OK) return st;
   if (workspace == nullptr || workspace_bytes < need || !aligned(workspace, 16))
     return fail(DOSA_ERR_WORKSPACE, "workspace needs " + std::to_string(need) + " bytes, 16-byte aligned");
@@ -194,13 +208,20 @@ int run_attn(int src, const AttnArgs& base, int32_t batch, const int32_t* q_lens
     AttnArgs& a = ch.a;
     for (int b = next[tiled];;) {
       const size_t rows = (size_t)ch.parts * 16 * a.rt;
-      a.part_o = static_cast<float*>(workspace);
-      a.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + up256(rows * d * sizeof(float)));
+      char* at = static_cast<char*>(workspace);
+      a.merged = reinterpret_cast<int4*>(at);
+      at += merged_bytes(ch);
+      a.part_o = reinterpret_cast<float*>(at);
+      a.part_ml = reinterpret_cast<float*>(at + up256(rows * d * sizeof(float)));
       hipError_t e;
       if (a.n_units > 0) {
         PassScope ps(paged_rows(src) ? (a.idx != nullptr ? P_BLOCK_ATTEND : P_PAGES_ATTEND)
                                      : (src == A_F32 || src == A_BF16 ? P_PROMPT : P_ATTEND), stream);
-        e = tiled ? launch_prompt(src, d, a, stream)
+        if (tiled && a.idx != nullptr) {
+          e = launch_block_merge(a, stream);
+          if (e != hipSuccess) return fail_hip(e, "block merge launch");
+        }
+        e = tiled ? (a.idx != nullptr ? launch_block_tiles(d, a, stream) : launch_prompt(src, d, a, stream))
                   : (paged_rows(src) ? launch_pages(src, d, a, stream) : launch_attn(src, d, a, stream));
         if (e != hipSuccess) return fail_hip(e, "attention kernel launch");
       }
@@ -210,8 +231,8 @@ int run_attn(int src, const AttnArgs& base, int32_t batch, const int32_t* q_lens
         if (e != hipSuccess) return fail_hip(e, "attention join launch");
       }
       if (b >= batch) break;
-      b = plan_attn(ch, src, d, tiled != 0, b, batch, q_lens, kv_lens, base.Hq, base.Hkv, base.topk, &qr[tiled],
-                    &kr[tiled]);
+      b = plan_attn(ch, src, d, tiled != 0, b, batch, q_lens, kv_lens, base.Hq, base.Hkv, base.topk, base.block,
+                    &qr[tiled], &kr[tiled]);
     }
   }
   return DOSA_OK;

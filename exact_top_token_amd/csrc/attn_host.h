@@ -96,10 +96,11 @@ inline int check_pages(const int32_t* table, int32_t num_pages, int32_t page_siz
 }
 
 // Bytes of partial results the call's launches need (each launch reuses them);
-// 0 if a launch would be too large.  topk: selected keys of a row, or 0.
+// 0 if a launch would be too large.  topk: selected keys of a row, or 0; block:
+// keys of a selected block, 0 where keys are selected one by one.
 // threads: those of the largest launch.
 size_t attn_workspace(int src, int32_t batch, const int32_t* q_lens, const int32_t* kv_lens, int32_t Hq, int32_t Hkv,
-                      int32_t d, int32_t topk, int64_t* threads = nullptr);
+                      int32_t d, int32_t topk, int32_t block = 0, int64_t* threads = nullptr);
 // The attention of base (operands, heads, scale) planned, checked against the
 // workspace and enqueued.
 int run_attn(int src, const AttnArgs& base, int32_t batch, const int32_t* q_lens, const int32_t* kv_lens, int32_t d,

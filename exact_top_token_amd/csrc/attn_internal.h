@@ -63,6 +63,9 @@ struct AttnArgs {
   int32_t topk, Hq, Hkv, group;           // group = Hq / Hkv
   float scale;
   int32_t block;                          // keys of a selected block (a power of two), paged rows only
+  int4* merged;                           // merged blocks of the units, merged_stride each
+  int32_t merged_stride;
+  int32_t tok;                            // queries of a row tile (1 but for merged blocks)
   Div page_div;                           // by page_size, paged rows only
   int32_t n_seq, n_units, n_join, rt, hp; // rt: 16-row tiles per unit and head, hp: heads per unit
   AttnSeq s[kAttnSeqs];
@@ -89,6 +92,16 @@ hipError_t launch_prompt(int src, int d, const AttnArgs& p, hipStream_t s);
 constexpr int attn_heads(int src, int rt, int Hkv) { return src == A_MX && rt == 1 && Hkv % 2 == 0 ? 2 : 1; }
 hipError_t launch_attn(int src, int d, const AttnArgs& p, hipStream_t s);
 hipError_t launch_pages(int src, int d, const AttnArgs& p, hipStream_t s);
+
+// Listed blocks of many bf16 queries: units are kBlockTileWaves 16-row tiles of
+// one kv head, which share the blocks that they list.
+constexpr int kBlockTileWaves = 8;
+// Records of a unit's merged blocks: one for every entry of its queries' lists
+// and kBlockEnds behind (so many are read ahead).
+constexpr int kBlockEnds = 8;
+constexpr int kBlockTok = 8;           // queries of a row tile at most: 64 of a unit
+hipError_t launch_block_merge(const AttnArgs& p, hipStream_t s);
+hipError_t launch_block_tiles(int d, const AttnArgs& p, hipStream_t s);
 hipError_t launch_attn_join(int src, int d, const AttnArgs& p, hipStream_t s);
 
 // Cache write and read-back.

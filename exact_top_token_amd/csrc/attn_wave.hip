@@ -627,8 +627,8 @@ __global__ __launch_bounds__(256) void attn_join_kernel(const AttnArgs p, int se
   const int query = (unit - sq.join0) / p.Hq, qh = (unit - sq.join0) % p.Hq;
   const int head = qh / p.group, gh = qh % p.group, rows_u = 16 * p.rt;
   const int tiles_q = (p.group + rows_u - 1) / rows_u;
-  const int r = sel ? gh : query * p.group + gh;
-  const int rt0 = r / rows_u + (sel ? query * tiles_q : 0), r_in = r % rows_u;
+  const int r = (sel ? query % p.tok : query) * p.group + gh;
+  const int rt0 = r / rows_u + (sel ? query / p.tok * tiles_q : 0), r_in = r % rows_u;
   const float c = p.scale * kLog2e;
   const int64_t first = sq.part0 + (int64_t)(sq.n_rt - 1 - rt0) * sq.n_split * p.Hkv + head;
   float M = -INFINITY, L = 0.f, o[PER] = {};

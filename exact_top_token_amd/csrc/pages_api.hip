@@ -327,7 +327,7 @@ size_t dsa_block_workspace_size(int32_t batch, const int32_t* q_lens, const int3
         check_float(dtype) != DOSA_OK || check_block(block, block) != DOSA_OK)
       return 0;
     if (topn < 1 || (int64_t)topn * block > (1 << 20)) return 0;
-    return attn_workspace(source(dtype), batch, q_lens, kv_lens, Hq, Hkv, d, topn * block);
+    return attn_workspace(source(dtype), batch, q_lens, kv_lens, Hq, Hkv, d, topn * block, block);
   });
 }
 

@@ -29,6 +29,10 @@ namespace {
 
 constexpr int kWaves = 8;   // largest wavefronts per workgroup
 
+// Exponent by which a score may exceed the running maximum: weights reach 2^8
+// at most, and most steps skip the rescaling of the outputs.
+constexpr float kSlack = 8.f;
+
 template <bool F32, int D>
 struct Row {
   static constexpr int SIZE = F32 ? 4 : 2;
@@ -247,7 +251,7 @@ __global__ __launch_bounds__(64 * kWaves) void pages_kernel(const AttnArgs p) {
 #pragma unroll
         for (int r = 0; r < 4; ++r) top = fmaxf(top, sc[i][a][r]);
       top = max_groups(top);
-      if (__any(top > m[i])) {
+      if (__any((top - m[i]) * c > kSlack)) {     // (-inf) - (-inf) compares false
         const float m_new = fmaxf(m[i], top);
         // a row that has seen nothing yet: weight 1 on empty sums
         const float f = m_new == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((m[i] - m_new) * c);

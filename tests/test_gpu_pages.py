@@ -484,6 +484,11 @@ def test_select_many_sequences():
     (1, 1, 16, 16, 1, [1], [1]),
     (4, 2, 32, 16, 3, [0, 3, 20], [9, 40, 100]),
     (8, 1, 64, 64, 4, [5, 1], [400, 333]),
+    (8, 2, 64, 64, 4, [40, 1, 300], [1400, 333, 310]),
+    (5, 1, 32, 16, 6, [100, 37], [700, 60]),
+    (3, 3, 64, 32, 3, [200], [500]),
+    (32, 1, 256, 128, 3, [70], [900]),
+    (48, 1, 16, 16, 5, [33, 8], [300, 8]),
     (6, 3, 96, 32, 5, [3, 2], [300, 500]),
     (20, 1, 128, 128, 2, [4], [700]),
     (40, 2, 64, 16, 7, [2, 1], [200, 33]),
@@ -523,6 +528,27 @@ def test_block_attention_oddities(dtype):
         out, lse = run_pages(p, q, ql, kl, idx=ints(idx), block=block)
         ref = P.pages_attention(host(q), kp, vp, t, ql, kl, d ** -0.5, idx, block)
         check_attention(out, lse, ref, d, 70, dtype == "bf16")
+        assert torch.all(out[torch.from_numpy(np.isinf(ref[1])).cuda()] == 0) and np.isinf(ref[1]).any()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hq,hk,page,block", [(8, 1, 32, 16), (4, 2, 64, 64), (16, 1, 128, 128), (40, 1, 32, 32), (1, 1, 48, 16)])
+def test_block_attention_oddities_of_many_rows(d, hq, hk, page, block):
+    """The same for chunks of queries whose lists are merged: lists in any order, entries twice, garbage, rows that
+    list nothing, long lists, pages that are not there; page 0 and every unused slot hold NaN."""
+    rng = np.random.default_rng(hq + d)
+    ql, kl = [130, 1, 75], [5 * page + 7, 40, 76]
+    for topn, gone in ((3, ()), (5, ((0, 0), (0, 3), (2, 1))), (150, ((0, 1),))):
+        say("block oddities, many rows", d, hq, page, block, topn)
+        p, kp, vp, t = filled(rng, kl, page, hk, d, "bf16", gone)
+        q = rows(rng, sum(ql), hq, d, "bf16").cuda()
+        idx = rng.integers(-2, max(kl) // block + 3, (sum(ql), hk, topn)).astype(np.int32)
+        idx[rng.random(sum(ql)) < 0.5] = np.sort(idx, -1)[0]
+        idx[3:9] = -1
+        idx[20, 0, 0], idx[21, 0, 1] = 0x7fffffff, -(1 << 31)
+        out, lse = run_pages(p, q, ql, kl, idx=ints(idx), block=block)
+        ref = P.pages_attention(host(q), kp, vp, t, ql, kl, d ** -0.5, idx, block)
+        check_attention(out, lse, ref, d, min(topn * block, 3 * max(kl)), True)
         assert torch.all(out[torch.from_numpy(np.isinf(ref[1])).cuda()] == 0) and np.isinf(ref[1]).any()
 
 
