@@ -14,9 +14,10 @@
 // of two by repeating the last (which leaves the maximum alone), are the rows of
 // 16x16x64 products of 8-bit integers, the blocks their columns; the scores go to
 // LDS as unsigned numbers of the same order.  Then a wavefront takes a token:
-// the threshold is built bit by bit from above until exactly the wanted number of
-// scores reaches it, and the chosen blocks are written in ascending order by
-// counting lanes.  Of scores equal to the threshold the lowest blocks are taken.
+// a lower bound of the threshold from the lanes' largest scores leaves few
+// candidates, one a lane, among which the threshold is built bit by bit; the
+// chosen blocks are written in ascending order by counting lanes.  Of scores equal
+// to the threshold the lowest blocks are taken.
 #include "attn_device.h"
 #include "pages_internal.h"
 
@@ -24,9 +25,8 @@ namespace dosa {
 
 namespace {
 
-constexpr int kWavesS = 4;
+constexpr int kMaxWaves = 16;
 constexpr int kCols = 4;                 // column tiles a wavefront has in flight
-constexpr int kRegs = 16;                // scores of a lane in registers
 
 __device__ __forceinline__ uint32_t ordered(float x) {
   const uint32_t b = __float_as_uint(x);
@@ -36,10 +36,21 @@ __device__ __forceinline__ int below(uint64_t mask) {        // lanes of the mas
   return __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0u));
 }
 
+// The value of lane l^16 (l^32).
+__device__ __forceinline__ float other_half16(float x) {
+  const uint32_t u = __float_as_uint(x);
+  auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  return (lane64() & 16) != 0 ? __uint_as_float(r[0]) : __uint_as_float(r[1]);
+}
+__device__ __forceinline__ float other_half32(float x) {
+  const uint32_t u = __float_as_uint(x);
+  auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  return (lane64() & 32) != 0 ? __uint_as_float(r[0]) : __uint_as_float(r[1]);
+}
+
 // 16 elements of a query row as floats.
-template <bool F32>
-__device__ __forceinline__ void row16(const void* q, int64_t at, float* x) {
-  if constexpr (F32) {
+__device__ __forceinline__ void row16(bool f32, const void* q, int64_t at, float* x) {
+  if (f32) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const f4 y = reinterpret_cast<const f4*>(static_cast<const float*>(q) + at)[i];
@@ -59,14 +70,35 @@ __device__ __forceinline__ void row16(const void* q, int64_t at, float* x) {
   }
 }
 
-template <bool F32, int D, int MT>
-__global__ __launch_bounds__(64 * kWavesS) void select_kernel(const SelectArgs p) {
+// The largest number that `need` scores reach, built bit by bit from above;
+// count(x): scores that reach x; reach: how many reach 0.  Stops where exactly
+// `need` reach what there is of it.
+template <class Count>
+__device__ __forceinline__ uint32_t kth(Count count, int need, int reach) {
+  uint32_t t = 0;
+  for (int b = 31; b >= 0; --b) {
+    const int c = count(t | (1u << b));
+    if (c >= need) {
+      t |= 1u << b;
+      reach = c;
+      if (reach == need) break;
+    }
+  }
+  return t;
+}
+
+// MT: 16-row tiles of the workgroup; PAD: rows of a token; MANY: groups of more than 16 heads, several
+// products of one tile.
+template <int D, int MT, int PAD, bool MANY>
+__global__ __launch_bounds__(64 * (MT == 1 ? 16 : 8)) void select_kernel(const SelectArgs p) {
   constexpr int KS = D / 64;
   extern __shared__ uint32_t scores[];
+  __shared__ i4 qcodes[MANY ? 1 : MT][KS][64];
+  __shared__ __attribute__((aligned(16))) float qfactor[MANY ? 1 : MT][16];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int lane = lane64(), n = lane & 15, g = lane >> 4;
+  const int lane = lane64(), n = lane & 15, g = lane >> 4, waves = blockDim.x >> 6;
   const SelectSeq& sq = p.s[find_seq(p.s, p.n_seq, (int)blockIdx.x, [](const SelectSeq& s) { return s.unit0; })];
-  const int per = 16 / p.pad, TW = per * MT;
+  constexpr int PER = 16 / PAD, TW = PER * MT;
   const int u = (int)blockIdx.x - sq.unit0, head = u % p.Hkv;
   const int tiles = (sq.q_len + TW - 1) / TW, tok0 = (tiles - 1 - u / p.Hkv) * TW;   // last tokens first: they see the most blocks
   const int n_tok = min(TW, sq.q_len - tok0), pos0 = sq.kv_len - sq.q_len + tok0;
@@ -76,15 +108,15 @@ __global__ __launch_bounds__(64 * kWavesS) void select_kernel(const SelectArgs p
   if (own_last >= p.topn) {
     // ---- scores of blocks col0..col_end-1 ----
     auto q_at = [&](int i, int pass) -> int64_t {
-      const int tok = min(i * per + n / p.pad, n_tok - 1), h = min(16 * pass + n % p.pad, p.group - 1);
+      const int tok = min(i * PER + n / PAD, n_tok - 1), h = min(16 * pass + n % PAD, p.group - 1);
       return (int64_t)(sq.q_row0 + tok0 + tok) * p.q_stride + (int64_t)(head * p.group + h) * D + 16 * g;
     };
-    // exponent of row n of tile i
+    // exponent of row n of tile i, its elements
     auto exponent = [&](int i, int pass, float x[KS][16]) -> int {
       float top = 0.f;
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
-        row16<F32>(p.q, q_at(i, pass) + 64 * s, x[s]);
+        row16(p.f32 != 0, p.q, q_at(i, pass) + 64 * s, x[s]);
 #pragma unroll
         for (int e = 0; e < 16; ++e) top = fmaxf(top, fabsf(x[s][e]));
       }
@@ -92,39 +124,63 @@ __global__ __launch_bounds__(64 * kWavesS) void select_kernel(const SelectArgs p
       const int e = (int)((__float_as_uint(top) + (1u << 16)) >> 23) - 127 - 6;
       return e < -126 ? -126 : e;
     };
-    int most[MT];                        // largest exponent of the token's heads
+    auto round8 = [&](const float x[KS][16], int e, i4* codes) {
+      const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      most[i] = -126;
+      for (int s = 0; s < KS; ++s)
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          uint32_t y = 0;
+#pragma unroll
+          for (int b = 0; b < 4; ++b) y |= ((uint32_t)(int)rintf(x[s][4 * w + b] * inv) & 255u) << (8 * b);
+          codes[s][w] = (int)y;
+        }
+    };
+    auto factor = [&](int e, int most) -> float {      // of a head whose exponent is e
+      const int rel = e - most;
+      return __uint_as_float((uint32_t)(127 + (rel < -100 ? -100 : rel)) << 23);
+    };
+    int most = -126;                     // MANY: largest exponent of the token's heads
+    if constexpr (MANY) {
       for (int pass = 0; pass < p.passes; ++pass) {
         float x[KS][16];
-        most[i] = max(most[i], exponent(i, pass, x));
+        most = max(most, exponent(0, pass, x));
       }
-      for (int w = 1; w < p.pad; w <<= 1) most[i] = max(most[i], __shfl_xor(most[i], w));
-    }
-    for (int pass = 0; pass < p.passes; ++pass) {
-      i4 qa[MT][KS];
-      float rs[MT][4];
-#pragma unroll
-      for (int i = 0; i < MT; ++i) {
+      for (int w = 1; w < 16; w <<= 1) most = max(most, __shfl_xor(most, w));
+    } else {
+      // a wavefront rounds the rows of a tile for all of them
+      for (int i = wave; i < MT; i += waves) {
         float x[KS][16];
-        const int e = exponent(i, pass, x);
-        const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+        i4 codes[KS];
+        const int e = exponent(i, 0, x);
+        int m = e;
+        for (int w = 1; w < PAD; w <<= 1) m = max(m, __shfl_xor(m, w));
+        round8(x, e, codes);
 #pragma unroll
-        for (int s = 0; s < KS; ++s)
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            uint32_t y = 0;
-#pragma unroll
-            for (int b = 0; b < 4; ++b) y |= ((uint32_t)(int)rintf(x[s][4 * w + b] * inv) & 255u) << (8 * b);
-            qa[i][s][w] = (int)y;
-          }
-        const int rel = e - most[i];
-        const float f = __uint_as_float((uint32_t)(127 + (rel < -100 ? -100 : rel)) << 23);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) rs[i][r] = __shfl(f, 4 * g + r);
+        for (int s = 0; s < KS; ++s) qcodes[i][s][lane] = codes[s];
+        if (g == 0) qfactor[i][n] = factor(e, m);
       }
-      for (int ct = col0 + 16 * kCols * wave; ct < col_end; ct += 16 * kCols * kWavesS) {
+      __syncthreads();
+    }
+    for (int pass = 0; pass < (MANY ? p.passes : 1); ++pass) {
+      i4 qa[MT][KS];
+      f4 rs[MT];
+      if constexpr (MANY) {
+        float x[KS][16];
+        const int e = exponent(0, pass, x);
+        round8(x, e, qa[0]);
+        const float f = factor(e, most);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) rs[0][r] = __shfl(f, 4 * g + r);
+      } else {
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+#pragma unroll
+          for (int s = 0; s < KS; ++s) qa[i][s] = qcodes[i][s][lane];
+          rs[i] = *reinterpret_cast<const f4*>(&qfactor[i][4 * g]);
+        }
+      }
+      for (int ct = col0 + 16 * kCols * wave; ct < col_end; ct += 16 * kCols * waves) {
         i4 kb[kCols][KS];
         int sb[kCols];
         bool bad[kCols];
@@ -139,31 +195,34 @@ __global__ __launch_bounds__(64 * kWavesS) void select_kernel(const SelectArgs p
 #pragma unroll
           for (int s = 0; s < KS; ++s) kb[c][s] = *reinterpret_cast<const i4*>(p.codes + at * D + 64 * s + 16 * g);
         }
+        i4 acc[kCols][MT];
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+#pragma unroll
+          for (int c = 0; c < kCols; ++c)
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+              acc[c][i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(qa[i][s], kb[c][s], s == 0 ? i4{0, 0, 0, 0} : acc[c][i], 0, 0, 0);
+        // rows 4g..4g+3 of a tile, block j: the maximum over a token's rows
 #pragma unroll
         for (int c = 0; c < kCols; ++c) {
           const int j = ct + 16 * c + n;
-          if (ct + 16 * c >= col_end) break;
 #pragma unroll
           for (int i = 0; i < MT; ++i) {
-            i4 acc = {0, 0, 0, 0};
-#pragma unroll
-            for (int s = 0; s < KS; ++s) acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(qa[i][s], kb[c][s], acc, 0, 0, 0);
-            // rows 4g..4g+3 of the tile, block j: the maximum over a token's rows
             float v[4];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) v[r] = (float)acc[r] * rs[i][r];
-            if (p.pad >= 2) v[0] = fmaxf(v[0], v[1]), v[2] = fmaxf(v[2], v[3]);
-            if (p.pad >= 4) v[0] = fmaxf(v[0], v[2]);
-            if (p.pad >= 8) v[0] = fmaxf(v[0], __shfl_xor(v[0], 16));
-            if (p.pad >= 16) v[0] = fmaxf(v[0], __shfl_xor(v[0], 32));
+            for (int r = 0; r < 4; ++r) v[r] = (float)acc[c][i][r] * rs[i][r];
+            if constexpr (PAD >= 2) v[0] = fmaxf(v[0], v[1]), v[2] = fmaxf(v[2], v[3]);
+            if constexpr (PAD >= 4) v[0] = fmaxf(v[0], v[2]);
+            if constexpr (PAD >= 8) v[0] = fmaxf(v[0], other_half16(v[0]));
+            if constexpr (PAD >= 16) v[0] = fmaxf(v[0], other_half32(v[0]));
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              if ((r & (p.pad - 1)) != 0) continue;
+            for (int r = 0; r < 4; r += (PAD < 4 ? PAD : 4)) {
               const float x = bad[c] ? -INFINITY : ldexpf(v[r], sb[c] - 142) + 0.f;     // -0 is 0
               uint32_t key = ordered(x);
-              uint32_t* to = scores + (i * per + (4 * g + r) / p.pad) * p.stride + (j - col0);
-              if (((4 * g + r) & (p.pad - 1)) == 0 && j < col_end) {
-                if (pass > 0) key = max(key, *to);
+              uint32_t* to = scores + (i * PER + (4 * g + r) / PAD) * p.stride + (j - col0);
+              if ((PAD <= 4 || ((4 * g) & (PAD - 1)) == 0) && j < col_end) {
+                if (MANY && pass > 0) key = max(key, *to);
                 *to = key;
               }
             }
@@ -175,7 +234,8 @@ __global__ __launch_bounds__(64 * kWavesS) void select_kernel(const SelectArgs p
   __syncthreads();
 
   // ---- a wavefront a token ----
-  for (int tok = wave; tok < n_tok; tok += kWavesS) {
+  __shared__ uint32_t few[kMaxWaves][2][64];       // scores that may be chosen, and their blocks
+  for (int tok = wave; tok < n_tok; tok += waves) {
     const int own = (pos0 + tok) >> p.lb;
     int32_t* out = p.idx + ((int64_t)(sq.q_row0 + tok0 + tok) * p.Hkv + head) * p.topn;
     if (own < p.topn) {
@@ -183,72 +243,100 @@ __global__ __launch_bounds__(64 * kWavesS) void select_kernel(const SelectArgs p
       continue;
     }
     const int lo = p.sinks, hi = own - p.local + 1, need = p.topn - p.sinks - p.local, chunks = (hi - lo + 63) >> 6;
+    for (int i = lane; i < p.sinks; i += 64) out[i] = i;
+    for (int i = lane; i < p.local; i += 64) out[p.topn - p.local + i] = own - p.local + 1 + i;
+    if (need == 0) continue;
+    out += p.sinks;
     const uint32_t* row = scores + tok * p.stride + (lo - col0) + lane;
-    uint32_t v[kRegs];
-#pragma unroll
-    for (int i = 0; i < kRegs; ++i) v[i] = lo + 64 * i + lane < hi ? row[64 * i] : 0u;     // 0 is below every score
-    auto at = [&](int i) -> uint32_t { return lo + 64 * i + lane < hi ? row[64 * i] : 0u; };
-    auto count = [&](uint32_t least) -> int {
-      int c = 0;
-#pragma unroll
-      for (int i = 0; i < kRegs; ++i)
-        if (i < chunks) c += __popcll(__ballot(v[i] >= least));
-      for (int i = kRegs; i < chunks; ++i) c += __popcll(__ballot(at(i) >= least));
-      return c;
-    };
-    uint32_t least = 0;                  // the largest number that `need` scores reach
-    int reach = hi - lo;
-    for (int b = 31; b >= 0 && reach != need; --b) {
-      const int c = count(least | (1u << b));
-      if (c >= need) {
-        least |= 1u << b;
-        reach = c;
+    auto at = [&](int i) -> uint32_t { return lo + 64 * i + lane < hi ? row[64 * i] : 0u; };   // 0 is below every score
+    // Of the lanes' largest scores the need-th largest is reached by `need` scores at least: a lower bound of
+    // the threshold, and one that few others reach.
+    uint32_t least = 0;
+    if (need <= 64) {
+      uint32_t top = 0;
+      for (int i = 0; i < chunks; ++i) top = max(top, at(i));
+      least = kth([&](uint32_t x) -> int { return __popcll(__ballot(top >= x)); }, need, need);
+    }
+    if (least != 0) {
+      int n_few = 0;
+      for (int i = 0; i < chunks && n_few <= 64; ++i) {
+        const uint32_t x = at(i);
+        const uint64_t in = __ballot(x >= least);
+        const int to = n_few + below(in);
+        if (x >= least && to < 64) {
+          few[wave][0][to] = x;
+          few[wave][1][to] = (uint32_t)(lo + 64 * i + lane);
+        }
+        n_few += __popcll(in);
+      }
+      if (n_few <= 64) {
+        wave_sync();
+        const uint32_t x = lane < n_few ? few[wave][0][lane] : 0u, blk = few[wave][1][lane];
+        wave_sync();
+        const uint32_t t = kth([&](uint32_t y) -> int { return __popcll(__ballot(x >= y)); }, need, n_few);
+        const int more = __popcll(__ballot(x > t));
+        const uint64_t eq = __ballot(x == t);
+        const bool take = x > t || (x == t && below(eq) < need - more);
+        const uint64_t all = __ballot(take);
+        if (take) out[below(all)] = (int32_t)blk;
+        continue;
       }
     }
-    int ties = reach == need ? need : need - count(least + 1);     // of the scores equal to `least`
-    int done = p.sinks;
-    auto put = [&](uint32_t x, int i) {
-      const uint64_t eq = __ballot(x == least && x != 0u);
-      const bool take = x > least || (x == least && x != 0u && below(eq) < ties);
+    // many blocks to choose, or many equal scores
+    auto count = [&](uint32_t y) -> int {
+      int c = 0;
+      for (int i = 0; i < chunks; ++i) c += __popcll(__ballot(at(i) >= y));
+      return c;
+    };
+    const uint32_t t = kth(count, need, hi - lo);
+    int ties = need - (t == 0xffffffffu ? 0 : count(t + 1)), done = 0;
+    for (int i = 0; i < chunks; ++i) {
+      const uint32_t x = at(i);
+      const uint64_t eq = __ballot(x == t);
+      const bool take = x > t || (x == t && below(eq) < ties);
       const uint64_t all = __ballot(take);
       if (take) out[done + below(all)] = lo + 64 * i + lane;
       done += __popcll(all);
       ties -= __popcll(eq);
-    };
-    if (need > 0) {
-#pragma unroll
-      for (int i = 0; i < kRegs; ++i)
-        if (i < chunks) put(v[i], i);
-      for (int i = kRegs; i < chunks; ++i) put(at(i), i);
     }
-    for (int i = lane; i < p.sinks; i += 64) out[i] = i;
-    for (int i = lane; i < p.local; i += 64) out[p.topn - p.local + i] = own - p.local + 1 + i;
   }
 }
 
-template <bool F32, int D, int MT>
+template <int D, int MT, int PAD, bool MANY>
 hipError_t go(const SelectArgs& p, hipStream_t s) {
-  const unsigned lds = (unsigned)(16 / p.pad * MT) * (unsigned)p.stride * 4u;
-  if (lds > (64u << 10)) {
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&select_kernel<F32, D, MT>),
+  const unsigned lds = (unsigned)(16 / PAD * MT) * (unsigned)p.stride * 4u;
+  constexpr int waves = MT == 1 ? 16 : 8;      // few tokens: the wavefronts are there for the loads
+  if (lds > (32u << 10)) {
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&select_kernel<D, MT, PAD, MANY>),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
     if (e != hipSuccess) return e;
   }
-  select_kernel<F32, D, MT><<<dim3((unsigned)p.n_units), dim3(64 * kWavesS), lds, s>>>(p);
+  select_kernel<D, MT, PAD, MANY><<<dim3((unsigned)p.n_units), dim3(64 * waves), lds, s>>>(p);
   return hipGetLastError();
 }
 
-template <bool F32, int D>
+template <int D, int MT>
+hipError_t go_pad(const SelectArgs& p, hipStream_t s) {
+  switch (p.pad) {
+    case 1: return go<D, MT, 1, false>(p, s);
+    case 2: return go<D, MT, 2, false>(p, s);
+    case 4: return go<D, MT, 4, false>(p, s);
+    case 8: return go<D, MT, 8, false>(p, s);
+    default: return go<D, MT, 16, false>(p, s);
+  }
+}
+
+template <int D>
 hipError_t go_tiles(int tiles, const SelectArgs& p, hipStream_t s) {
-  return tiles == 4 ? go<F32, D, 4>(p, s) : tiles == 2 ? go<F32, D, 2>(p, s) : go<F32, D, 1>(p, s);
+  if (p.passes > 1) return go<D, 1, 16, true>(p, s);
+  return tiles == 2 ? go_pad<D, 2>(p, s) : go_pad<D, 1>(p, s);
 }
 
 }  // namespace
 
-hipError_t launch_block_select(bool f32, int d, int tiles, const SelectArgs& p, hipStream_t s) {
+hipError_t launch_block_select(int d, int tiles, const SelectArgs& p, hipStream_t s) {
   if (p.n_units == 0) return hipSuccess;
-  if (f32) return d == 128 ? go_tiles<true, 128>(tiles, p, s) : go_tiles<true, 64>(tiles, p, s);
-  return d == 128 ? go_tiles<false, 128>(tiles, p, s) : go_tiles<false, 64>(tiles, p, s);
+  return d == 128 ? go_tiles<128>(tiles, p, s) : go_tiles<64>(tiles, p, s);
 }
 
 }  // namespace dosa

@@ -109,7 +109,7 @@ int move_pages(bool assign, int32_t* table, int32_t max_pages, int32_t page_size
 // ---------------------------------------------------------------------------
 constexpr int64_t kSelectLds = 64 << 10;
 constexpr int64_t kSelectBlocks = 32768;
-constexpr int64_t kSelectTiles = 4;
+constexpr int64_t kSelectTiles = 2;
 
 int64_t select_stride(const SelectArgs& a, int32_t kv_len) {
   const int64_t own = ((int64_t)kv_len - 1) >> a.lb;
@@ -275,11 +275,12 @@ int dsa_block_select(const dsa_blocks* blocks, const int32_t* page_table, int32_
     a.sinks = sinks;
     a.local = local;
     a.passes = (a.group + 15) / 16;
+    a.f32 = q_dtype == DOSA_F32;
     for (int b = 0; b < batch; ++b) {
       if (q_lens[b] == 0) continue;
       if (((int64_t)kv_lens[b] + blocks->block - 1) / blocks->block > kSelectBlocks)
         return fail(DOSA_ERR_UNSUPPORTED, "sequence " + std::to_string(b) + ": more than " + std::to_string(kSelectBlocks) + " blocks");
-      st = check_launch("block selection", (int64_t)q_lens[b] * a.Hkv * 256);
+      st = check_launch("block selection", (int64_t)q_lens[b] * a.Hkv * 1024);
       if (st != DOSA_OK) return st;
     }
     int64_t row = 0;
@@ -287,7 +288,7 @@ int dsa_block_select(const dsa_blocks* blocks, const int32_t* page_table, int32_
       // the sequences of a launch, then its tokens a workgroup, then its workgroups
       a.n_seq = 0;
       int64_t most_q = 0, stride = 16, most_units = 0;
-      for (; b < batch && a.n_seq < kAttnSeqs && (most_units + (int64_t)q_lens[b] * a.Hkv) * 256 < kLaunchThreads; ++b) {
+      for (; b < batch && a.n_seq < kAttnSeqs && (most_units + (int64_t)q_lens[b] * a.Hkv) * 1024 < kLaunchThreads; ++b) {
         if (q_lens[b] > 0) {
           a.s[a.n_seq++] = SelectSeq{0, (int32_t)row, q_lens[b], kv_lens[b], b};
           most_q = std::max<int64_t>(most_q, q_lens[b]);
@@ -297,9 +298,11 @@ int dsa_block_select(const dsa_blocks* blocks, const int32_t* page_table, int32_
         row += q_lens[b];
       }
       if (a.n_seq == 0) continue;
+      // most blocks first
+      std::stable_sort(a.s, a.s + a.n_seq, [](const SelectSeq& x, const SelectSeq& y) { return x.kv_len > y.kv_len; });
       a.pad = 1;
       while (a.pad < 16 && a.pad < a.group) a.pad *= 2;
-      int64_t tiles = kSelectTiles;
+      int64_t tiles = a.passes > 1 ? 1 : kSelectTiles;
       auto lds = [&]() { return 16 / a.pad * tiles * stride * 4; };
       while (tiles > 1 && (lds() > kSelectLds || 16 / a.pad * (tiles / 2) >= most_q)) tiles /= 2;
       while (a.pad < 16 && lds() > kSelectLds) a.pad *= 2;
@@ -311,7 +314,7 @@ int dsa_block_select(const dsa_blocks* blocks, const int32_t* page_table, int32_
         a.n_units += (int32_t)((a.s[i].q_len + tw - 1) / tw * a.Hkv);
       }
       PassScope ps(P_BLOCK_SELECT, static_cast<hipStream_t>(stream));
-      const hipError_t e = launch_block_select(q_dtype == DOSA_F32, blocks->d, (int)tiles, a, static_cast<hipStream_t>(stream));
+      const hipError_t e = launch_block_select(blocks->d, (int)tiles, a, static_cast<hipStream_t>(stream));
       if (e != hipSuccess) return fail_hip(e, "block selection launch");
     }
     return DOSA_OK;

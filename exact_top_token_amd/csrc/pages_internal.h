@@ -69,6 +69,7 @@ struct SelectArgs {
   Div div;            // by the blocks of a page
   int32_t max_pages, num_pages, Hkv, Hq, group;
   int32_t lb;         // log2 of the block
+  int32_t f32;        // queries' type
   int32_t topn, sinks, local;
   int32_t pad;        // rows of the product a token takes: a power of two up to 16
   int32_t passes;     // products of 16 rows a token takes, groups above 16
@@ -77,6 +78,6 @@ struct SelectArgs {
   SelectSeq s[kAttnSeqs];
 };
 // Tokens of a workgroup: (16 / pad) * tiles.
-hipError_t launch_block_select(bool f32, int d, int tiles, const SelectArgs& p, hipStream_t s);
+hipError_t launch_block_select(int d, int tiles, const SelectArgs& p, hipStream_t s);
 
 }  // namespace dosa
