@@ -167,11 +167,12 @@ class _On:
             _bad(f"tensors are on {self.device}, not on a GPU")
         if getattr(self.stream, "device", self.device) != self.device:
             _bad(f"stream is of {self.stream.device}, the tensors are on {self.device}")
-        if torch.cuda.current_device() != self.device.index:
+        if torch._C._cuda_getDevice() != self.device.index:
             self.back = torch.cuda.device(self.device)
             self.back.__enter__()
-        st = torch.cuda.current_stream() if self.stream is None else self.stream
-        return int(getattr(st, "cuda_stream", st))
+        if self.stream is None:     # the handle of torch.cuda.current_stream(), without the object
+            return torch._C._cuda_getCurrentRawStream(self.device.index)
+        return int(getattr(self.stream, "cuda_stream", self.stream))
 
     def __exit__(self, *exc):
         if self.back is not None:

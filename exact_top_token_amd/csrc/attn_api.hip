@@ -62,6 +62,35 @@ bool takes_tiled(int src, int64_t rows, bool sel) {
 }
 int attn_classes(int src) { return src == A_BF16 || src == A_P16 ? 2 : 1; }
 
+// Range length of the tiled kernel where a launch is less than two rounds of
+// the GPU and its units differ: the one for which the longest unit or the mean
+// load of a CU, whichever is more, and the join come to the least.  A tile of 64
+// keys takes a workgroup 1.8 us, as long as 9 MB of memory, and a unit about four
+// tiles to begin and end.  A scheduler's step of chunks of 1024 and 700 queries
+// over 9216 and 700 keys: 128 long units alone take 256 us, as two ranges each 150.
+int64_t balanced_len(const AttnArgs& a, int64_t len, int64_t tile) {
+  int64_t most = 0;
+  for (int i = 0; i < a.n_seq; ++i) most = std::max<int64_t>(most, a.s[i].kv_len);
+  double best = 0.;
+  for (int64_t n = 1; n <= 8; ++n) {
+    const int64_t l = std::max(kTiledMinKeys, ((most + n - 1) / n + 63) / 64 * 64);
+    double sum = 0., joined = 0.;
+    for (int i = 0; i < a.n_seq; ++i) {
+      const AttnSeq& s = a.s[i];
+      const int64_t rows = (int64_t)s.q_len * a.group, nrt = (rows + tile - 1) / tile, parts = (s.kv_len + l - 1) / l;
+      const double before = s.kv_len - s.q_len, seen = before + 0.5 * (s.q_len + std::min<double>(s.q_len, (double)tile / a.group));
+      sum += (double)nrt * a.Hkv * (seen / 64. + 4. * parts);
+      if (parts > 1) joined += (double)rows * a.Hkv * parts * 128. * 8.;
+    }
+    const double cost = std::max(std::min<double>(l, most) / 64. + 4., sum / kTiledResident) + joined / 9e6;
+    if (n == 1 || cost < best) {
+      best = cost;
+      len = l;
+    }
+  }
+  return len;
+}
+
 // Sequences b0.. of the batch that the kernel takes, at most kAttnSeqs with
 // queries; returns the sequence after the last one seen, or -1 if the launch
 // would be too large.
@@ -111,11 +140,13 @@ int plan_attn(AttnChunk& ch, int src, int d, bool tiled, int b0, int32_t batch, 
   // shortest range length in steps of 64 that keeps to the cap, or one range each
   int64_t lo = (tiled ? kTiledMinKeys : kMinKeys) / 64, hi = lo;
   for (int i = 0; i < a.n_seq; ++i) hi = std::max(hi, (keys(a.s[i]) + 63) / 64);
+  const int64_t one = hi;            // one range each
   while (lo < hi) {
     const int64_t mid = (lo + hi) / 2;
     if (units_at(64 * mid) <= cap) hi = mid; else lo = mid + 1;
   }
-  const int64_t len = 64 * lo;
+  int64_t len = 64 * lo;
+  if (tiled && src == A_P16 && !sel && units_at(64 * one) < 2 * kTiledResident) len = balanced_len(a, len, tile);
   int64_t units = 0, join = 0, parts = 0;
   for (int i = 0; i < a.n_seq; ++i) {
     AttnSeq& s = a.s[i];

@@ -613,9 +613,7 @@ __global__ __launch_bounds__(64 * kWaves) void attn_kernel(const AttnArgs p) {
 // the ranges in turn, kBatch at a time: outputs, maxima and sums are loaded
 // together, since the chain of dependent loads is what the launch waits for.
 // The outputs of ranges that saw no key (l = 0) are not used.
-constexpr int kBatch = 16;
-
-template <bool F32IO, int D, int WPR>
+template <bool F32IO, int D, int WPR, int kBatch>
 __global__ __launch_bounds__(256) void attn_join_kernel(const AttnArgs p, int sel) {
   constexpr int PER = D / 64;
   __shared__ float so[4][D];
@@ -754,8 +752,11 @@ hipError_t join(const AttnArgs& p, hipStream_t s) {
   int most = 0;
   for (int i = 0; i < p.n_seq; ++i) most = most > p.s[i].n_split ? most : p.s[i].n_split;
   const int sel = p.idx != nullptr;
-  if (most <= kBatch) attn_join_kernel<F32IO, D, 1><<<dim3((unsigned)(p.n_join + 3) / 4), dim3(256), 0, s>>>(p, sel);
-  else attn_join_kernel<F32IO, D, 4><<<dim3((unsigned)p.n_join), dim3(256), 0, s>>>(p, sel);
+  // (a batch loads its last range again in place of those that are not there: 32768 rows of 2 ranges 32 us
+  // sixteen at a time)
+  if (most <= 4) attn_join_kernel<F32IO, D, 1, 4><<<dim3((unsigned)(p.n_join + 3) / 4), dim3(256), 0, s>>>(p, sel);
+  else if (most <= 16) attn_join_kernel<F32IO, D, 1, 16><<<dim3((unsigned)(p.n_join + 3) / 4), dim3(256), 0, s>>>(p, sel);
+  else attn_join_kernel<F32IO, D, 4, 16><<<dim3((unsigned)p.n_join), dim3(256), 0, s>>>(p, sel);
   return hipGetLastError();
 }
 

@@ -26,7 +26,7 @@ namespace dosa {
 namespace {
 
 constexpr int kMaxWaves = 16;
-constexpr int kCols = 4;                 // column tiles a wavefront has in flight
+constexpr int kCols = 4;                 // column tiles a wavefront has in flight, one block a lane
 
 __device__ __forceinline__ uint32_t ordered(float x) {
   const uint32_t b = __float_as_uint(x);
@@ -181,49 +181,55 @@ __global__ __launch_bounds__(64 * (MT == 1 ? 16 : 8)) void select_kernel(const S
         }
       }
       for (int ct = col0 + 16 * kCols * wave; ct < col_end; ct += 16 * kCols * waves) {
+        // a lane a block: its page and scale, which the lanes of its column then get
         i4 kb[kCols][KS];
         int sb[kCols];
-        bool bad[kCols];
+        {
+          const int j = min(ct + lane, col_end - 1), pg = p.div.quot(j);
+          const int page = p.table[(int64_t)sq.b * p.max_pages + pg];
+          const bool there = (uint32_t)page < (uint32_t)p.num_pages;
+          const int at = (there ? page : 0) * (int)p.div.by + (j - pg * (int)p.div.by);
+          const int e = there ? (int)p.scales[(int64_t)at * p.Hkv + head] : -1;
 #pragma unroll
-        for (int c = 0; c < kCols; ++c) {
-          const int j = min(ct + 16 * c + n, col_end - 1), pg = p.div.quot(j);
-          int page = p.table[(int64_t)sq.b * p.max_pages + pg];
-          bad[c] = (uint32_t)page >= (uint32_t)p.num_pages;
-          page = bad[c] ? 0 : page;
-          const int64_t at = ((int64_t)page * p.div.by + (j - pg * (int)p.div.by)) * p.Hkv + head;
-          sb[c] = p.scales[at];
+          for (int c = 0; c < kCols; ++c) {
+            const int64_t row = (int64_t)__shfl(at, 16 * c + n) * p.Hkv + head;
+            sb[c] = __shfl(e, 16 * c + n);
 #pragma unroll
-          for (int s = 0; s < KS; ++s) kb[c][s] = *reinterpret_cast<const i4*>(p.codes + at * D + 64 * s + 16 * g);
+            for (int s = 0; s < KS; ++s) kb[c][s] = *reinterpret_cast<const i4*>(p.codes + row * D + 64 * s + 16 * g);
+          }
         }
-        i4 acc[kCols][MT];
 #pragma unroll
-        for (int s = 0; s < KS; ++s)
+        for (int c0 = 0; c0 < kCols; c0 += 2) {
+          i4 acc[2][MT];
 #pragma unroll
-          for (int c = 0; c < kCols; ++c)
+          for (int s = 0; s < KS; ++s)
 #pragma unroll
-            for (int i = 0; i < MT; ++i)
-              acc[c][i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(qa[i][s], kb[c][s], s == 0 ? i4{0, 0, 0, 0} : acc[c][i], 0, 0, 0);
-        // rows 4g..4g+3 of a tile, block j: the maximum over a token's rows
+            for (int c = 0; c < 2; ++c)
 #pragma unroll
-        for (int c = 0; c < kCols; ++c) {
-          const int j = ct + 16 * c + n;
+              for (int i = 0; i < MT; ++i)
+                acc[c][i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(qa[i][s], kb[c0 + c][s], s == 0 ? i4{0, 0, 0, 0} : acc[c][i], 0, 0, 0);
+          // rows 4g..4g+3 of a tile, block j: the maximum over a token's rows
 #pragma unroll
-          for (int i = 0; i < MT; ++i) {
-            float v[4];
+          for (int c = 0; c < 2; ++c) {
+            const int j = ct + 16 * (c0 + c) + n;
 #pragma unroll
-            for (int r = 0; r < 4; ++r) v[r] = (float)acc[c][i][r] * rs[i][r];
-            if constexpr (PAD >= 2) v[0] = fmaxf(v[0], v[1]), v[2] = fmaxf(v[2], v[3]);
-            if constexpr (PAD >= 4) v[0] = fmaxf(v[0], v[2]);
-            if constexpr (PAD >= 8) v[0] = fmaxf(v[0], other_half16(v[0]));
-            if constexpr (PAD >= 16) v[0] = fmaxf(v[0], other_half32(v[0]));
+            for (int i = 0; i < MT; ++i) {
+              float v[4];
 #pragma unroll
-            for (int r = 0; r < 4; r += (PAD < 4 ? PAD : 4)) {
-              const float x = bad[c] ? -INFINITY : ldexpf(v[r], sb[c] - 142) + 0.f;     // -0 is 0
-              uint32_t key = ordered(x);
-              uint32_t* to = scores + (i * PER + (4 * g + r) / PAD) * p.stride + (j - col0);
-              if ((PAD <= 4 || ((4 * g) & (PAD - 1)) == 0) && j < col_end) {
-                if (MANY && pass > 0) key = max(key, *to);
-                *to = key;
+              for (int r = 0; r < 4; ++r) v[r] = (float)acc[c][i][r] * rs[i][r];
+              if constexpr (PAD >= 2) v[0] = fmaxf(v[0], v[1]), v[2] = fmaxf(v[2], v[3]);
+              if constexpr (PAD >= 4) v[0] = fmaxf(v[0], v[2]);
+              if constexpr (PAD >= 8) v[0] = fmaxf(v[0], other_half16(v[0]));
+              if constexpr (PAD >= 16) v[0] = fmaxf(v[0], other_half32(v[0]));
+#pragma unroll
+              for (int r = 0; r < 4; r += (PAD < 4 ? PAD : 4)) {
+                const float x = sb[c0 + c] < 0 ? -INFINITY : ldexpf(v[r], sb[c0 + c] - 142) + 0.f;     // -0 is 0
+                uint32_t key = ordered(x);
+                uint32_t* to = scores + (i * PER + (4 * g + r) / PAD) * p.stride + (j - col0);
+                if ((PAD <= 4 || ((4 * g) & (PAD - 1)) == 0) && j < col_end) {
+                  if (MANY && pass > 0) key = max(key, *to);
+                  *to = key;
+                }
               }
             }
           }

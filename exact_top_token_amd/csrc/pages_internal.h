@@ -15,7 +15,7 @@ struct AssignSeq {
   int32_t pos0;       // position of that token (index of that page)
   int32_t new0;       // new pages of the launch's earlier sequences
 };
-constexpr int kAssignSeqs = 256;
+constexpr int kAssignSeqs = 328;        // what 4 KB of kernel arguments hold
 struct AssignArgs {
   int32_t* table;
   int32_t* free_pages;

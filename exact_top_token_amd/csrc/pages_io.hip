@@ -7,13 +7,30 @@ namespace dosa {
 
 namespace {
 
+// The record of each lane's token (page).  Most workgroups lie in one sequence;
+// the others search among the records that they span.
+__device__ __forceinline__ int seq_of(const AssignArgs& p, int t) {
+  const int first = blockIdx.x * 256, last = min(first + 255, p.n_tok - 1);
+  auto tok0 = [](const AssignSeq& s) { return s.tok0; };
+  int lo = find_seq(p.s, p.n_seq, first, tok0), hi = find_seq(p.s, p.n_seq, last, tok0);
+  if (lo == hi) return lo;
+  __shared__ int starts[kAssignSeqs];
+  for (int i = lo + (int)threadIdx.x; i <= hi; i += 256) starts[i] = p.s[i].tok0;
+  __syncthreads();
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (starts[mid] <= t) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
 // A thread a token.  A sequence's n-th new page is read from the free list
 // where it is used, so no token waits for another's table write; the token
 // that opens a page writes its entry.
 __global__ __launch_bounds__(256) void assign_kernel(const AssignArgs p) {
   const int t = blockIdx.x * 256 + threadIdx.x;
+  const int i = seq_of(p, t);
   if (t >= p.n_tok) return;
-  const int i = find_seq(p.s, p.n_seq, t, [](const AssignSeq& s) { return s.tok0; });
   const AssignSeq s = p.s[i];
   const int size = p.page_div.by, pos = s.pos0 + (t - s.tok0);
   const int pg = p.page_div.quot(pos), in = pos - pg * size;
@@ -28,8 +45,8 @@ __global__ __launch_bounds__(256) void assign_kernel(const AssignArgs p) {
 // A thread a page.
 __global__ __launch_bounds__(256) void release_kernel(const AssignArgs p) {
   const int t = blockIdx.x * 256 + threadIdx.x;
+  const int i = seq_of(p, t);
   if (t >= p.n_tok) return;
-  const int i = find_seq(p.s, p.n_seq, t, [](const AssignSeq& s) { return s.tok0; });
   int32_t* entry = p.table + (int64_t)(p.b0 + i) * p.max_pages + p.s[i].pos0 + (t - p.s[i].tok0);
   p.free_pages[p.top - 1 - t] = *entry;
   *entry = -1;
