@@ -71,9 +71,11 @@ int attn_classes(int src) { return src == A_BF16 || src == A_P16 ? 2 : 1; }
 int64_t balanced_len(const AttnArgs& a, int64_t len, int64_t tile) {
   int64_t most = 0;
   for (int i = 0; i < a.n_seq; ++i) most = std::max<int64_t>(most, a.s[i].kv_len);
+  const int64_t shortest = len;
   double best = 0.;
-  for (int64_t n = 1; n <= 8; ++n) {
+  for (int64_t n = 1; n <= 64; ++n) {
     const int64_t l = std::max(kTiledMinKeys, ((most + n - 1) / n + 63) / 64 * 64);
+    if (n > 1 && l < std::min(shortest, most / 8)) break;
     double sum = 0., joined = 0.;
     for (int i = 0; i < a.n_seq; ++i) {
       const AttnSeq& s = a.s[i];

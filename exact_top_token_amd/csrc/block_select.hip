@@ -15,7 +15,7 @@
 // 16x16x64 products of 8-bit integers, the blocks their columns; the scores go to
 // LDS as unsigned numbers of the same order.  Then a wavefront takes a token:
 // a lower bound of the threshold from the lanes' largest scores leaves few
-// candidates, one a lane, among which the threshold is built bit by bit; the
+// candidates, a few a lane, among which the threshold is built bit by bit; the
 // chosen blocks are written in ascending order by counting lanes.  Of scores equal
 // to the threshold the lowest blocks are taken.
 #include "attn_device.h"
@@ -25,7 +25,7 @@ namespace dosa {
 
 namespace {
 
-constexpr int kMaxWaves = 16;
+constexpr int kFew = 256;                // scores that a wavefront chooses from in registers
 constexpr int kCols = 4;                 // column tiles a wavefront has in flight, one block a lane
 
 __device__ __forceinline__ uint32_t ordered(float x) {
@@ -87,16 +87,20 @@ __device__ __forceinline__ uint32_t kth(Count count, int need, int reach) {
   return t;
 }
 
+// Wavefronts of a workgroup of MT row tiles: with few tokens they are there for
+// the loads.
+constexpr int select_waves(int mt) { return mt == 1 ? 16 : 8; }
+
 // MT: 16-row tiles of the workgroup; PAD: rows of a token; MANY: groups of more than 16 heads, several
 // products of one tile.
 template <int D, int MT, int PAD, bool MANY>
-__global__ __launch_bounds__(64 * (MT == 1 ? 16 : 8)) void select_kernel(const SelectArgs p) {
-  constexpr int KS = D / 64;
+__global__ __launch_bounds__(64 * select_waves(MT)) void select_kernel(const SelectArgs p) {
+  constexpr int KS = D / 64, kWaves = select_waves(MT);
   extern __shared__ uint32_t scores[];
   __shared__ i4 qcodes[MANY ? 1 : MT][KS][64];
   __shared__ __attribute__((aligned(16))) float qfactor[MANY ? 1 : MT][16];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int lane = lane64(), n = lane & 15, g = lane >> 4, waves = blockDim.x >> 6;
+  const int lane = lane64(), n = lane & 15, g = lane >> 4, waves = kWaves;
   const SelectSeq& sq = p.s[find_seq(p.s, p.n_seq, (int)blockIdx.x, [](const SelectSeq& s) { return s.unit0; })];
   constexpr int PER = 16 / PAD, TW = PER * MT;
   const int u = (int)blockIdx.x - sq.unit0, head = u % p.Hkv;
@@ -183,21 +187,22 @@ __global__ __launch_bounds__(64 * (MT == 1 ? 16 : 8)) void select_kernel(const S
       for (int ct = col0 + 16 * kCols * wave; ct < col_end; ct += 16 * kCols * waves) {
         // a lane a block: its page and scale, which the lanes of its column then get
         i4 kb[kCols][KS];
-        int sb[kCols];
+        int sb[kCols], e;
         {
           const int j = min(ct + lane, col_end - 1), pg = p.div.quot(j);
           const int page = p.table[(int64_t)sq.b * p.max_pages + pg];
           const bool there = (uint32_t)page < (uint32_t)p.num_pages;
           const int at = (there ? page : 0) * (int)p.div.by + (j - pg * (int)p.div.by);
-          const int e = there ? (int)p.scales[(int64_t)at * p.Hkv + head] : -1;
+          e = there ? (int)p.scales[(int64_t)at * p.Hkv + head] : -1;
 #pragma unroll
           for (int c = 0; c < kCols; ++c) {
             const int64_t row = (int64_t)__shfl(at, 16 * c + n) * p.Hkv + head;
-            sb[c] = __shfl(e, 16 * c + n);
 #pragma unroll
             for (int s = 0; s < KS; ++s) kb[c][s] = *reinterpret_cast<const i4*>(p.codes + row * D + 64 * s + 16 * g);
           }
         }
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) sb[c] = __shfl(e, 16 * c + n);
 #pragma unroll
         for (int c0 = 0; c0 < kCols; c0 += 2) {
           i4 acc[2][MT];
@@ -240,7 +245,8 @@ __global__ __launch_bounds__(64 * (MT == 1 ? 16 : 8)) void select_kernel(const S
   __syncthreads();
 
   // ---- a wavefront a token ----
-  __shared__ uint32_t few[kMaxWaves][2][64];       // scores that may be chosen, and their blocks
+  __shared__ uint32_t few[kWaves][kFew];           // scores that may be chosen
+  __shared__ uint16_t few_at[kWaves][kFew];        // their blocks, from `lo` on
   for (int tok = wave; tok < n_tok; tok += waves) {
     const int own = (pos0 + tok) >> p.lb;
     int32_t* out = p.idx + ((int64_t)(sq.q_row0 + tok0 + tok) * p.Hkv + head) * p.topn;
@@ -255,43 +261,70 @@ __global__ __launch_bounds__(64 * (MT == 1 ? 16 : 8)) void select_kernel(const S
     out += p.sinks;
     const uint32_t* row = scores + tok * p.stride + (lo - col0) + lane;
     auto at = [&](int i) -> uint32_t { return lo + 64 * i + lane < hi ? row[64 * i] : 0u; };   // 0 is below every score
+    auto each = [&](auto use) {          // four reads under way
+      for (int i0 = 0; i0 < chunks; i0 += 4) {
+        uint32_t x[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) x[u] = at(i0 + u);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) use(x[u], i0 + u);
+      }
+    };
     // Of the lanes' largest scores the need-th largest is reached by `need` scores at least: a lower bound of
     // the threshold, and one that few others reach.
     uint32_t least = 0;
     if (need <= 64) {
       uint32_t top = 0;
-      for (int i = 0; i < chunks; ++i) top = max(top, at(i));
+      each([&](uint32_t x, int) { top = max(top, x); });
       least = kth([&](uint32_t x) -> int { return __popcll(__ballot(top >= x)); }, need, need);
     }
+    int n_few = 0;
     if (least != 0) {
-      int n_few = 0;
-      for (int i = 0; i < chunks && n_few <= 64; ++i) {
-        const uint32_t x = at(i);
+      each([&](uint32_t x, int i) {
         const uint64_t in = __ballot(x >= least);
         const int to = n_few + below(in);
-        if (x >= least && to < 64) {
-          few[wave][0][to] = x;
-          few[wave][1][to] = (uint32_t)(lo + 64 * i + lane);
+        if (x >= least && to < kFew) {
+          few[wave][to] = x;
+          few_at[wave][to] = (uint16_t)(64 * i + lane);
         }
         n_few += __popcll(in);
+      });
+    }
+    if (least != 0 && n_few <= kFew) {
+      wave_sync();
+      uint32_t v[kFew / 64], blk[kFew / 64];
+#pragma unroll
+      for (int i = 0; i < kFew / 64; ++i) {
+        const bool in = 64 * i + lane < n_few;
+        v[i] = in ? few[wave][64 * i + lane] : 0u;
+        blk[i] = in ? few_at[wave][64 * i + lane] : 0u;
       }
-      if (n_few <= 64) {
-        wave_sync();
-        const uint32_t x = lane < n_few ? few[wave][0][lane] : 0u, blk = few[wave][1][lane];
-        wave_sync();
-        const uint32_t t = kth([&](uint32_t y) -> int { return __popcll(__ballot(x >= y)); }, need, n_few);
-        const int more = __popcll(__ballot(x > t));
-        const uint64_t eq = __ballot(x == t);
-        const bool take = x > t || (x == t && below(eq) < need - more);
+      wave_sync();
+      auto reach = [&](uint32_t y) -> int {
+        int c = __popcll(__ballot(v[0] >= y));
+#pragma unroll
+        for (int i = 1; i < kFew / 64; ++i)
+          if (n_few > 64 * i) c += __popcll(__ballot(v[i] >= y));
+        return c;
+      };
+      const uint32_t t = kth(reach, need, n_few);
+      int ties = need - (t == 0xffffffffu ? 0 : reach(t + 1)), done = 0;
+#pragma unroll
+      for (int i = 0; i < kFew / 64; ++i) {
+        if (n_few <= 64 * i) break;
+        const uint64_t eq = __ballot(v[i] == t);
+        const bool take = v[i] > t || (v[i] == t && below(eq) < ties);
         const uint64_t all = __ballot(take);
-        if (take) out[below(all)] = (int32_t)blk;
-        continue;
+        if (take) out[done + below(all)] = lo + (int)blk[i];
+        done += __popcll(all);
+        ties -= __popcll(eq);
       }
+      continue;
     }
     // many blocks to choose, or many equal scores
     auto count = [&](uint32_t y) -> int {
       int c = 0;
-      for (int i = 0; i < chunks; ++i) c += __popcll(__ballot(at(i) >= y));
+      each([&](uint32_t x, int) { c += __popcll(__ballot(x >= y)); });
       return c;
     };
     const uint32_t t = kth(count, need, hi - lo);
@@ -311,13 +344,12 @@ __global__ __launch_bounds__(64 * (MT == 1 ? 16 : 8)) void select_kernel(const S
 template <int D, int MT, int PAD, bool MANY>
 hipError_t go(const SelectArgs& p, hipStream_t s) {
   const unsigned lds = (unsigned)(16 / PAD * MT) * (unsigned)p.stride * 4u;
-  constexpr int waves = MT == 1 ? 16 : 8;      // few tokens: the wavefronts are there for the loads
   if (lds > (32u << 10)) {
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&select_kernel<D, MT, PAD, MANY>),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
     if (e != hipSuccess) return e;
   }
-  select_kernel<D, MT, PAD, MANY><<<dim3((unsigned)p.n_units), dim3(64 * waves), lds, s>>>(p);
+  select_kernel<D, MT, PAD, MANY><<<dim3((unsigned)p.n_units), dim3(64 * select_waves(MT)), lds, s>>>(p);
   return hipGetLastError();
 }
 

@@ -289,13 +289,20 @@ __global__ __launch_bounds__(64 * kWaves) void pages_kernel(const AttnArgs p) {
 #pragma unroll
           for (int i = 0; i < RT; ++i) o[i][j] = mfma_f32(__uint_as_float(st.v[r][j]), sc[i][0][r], o[i][j]);
     } else {
-      // weights go to bf16 for this product: 2^-9 of each at most on average, and their
-      // sum was taken before; two bf16 terms would double the product
-      b8 pf[RT];
+      // one row tile: weights as two bf16 terms, 16 significant bits.  The matrix unit waits for memory here, and
+      // the result's rounding stays the only one that shows.  Two row tiles have no registers for that (32
+      // sequences x 4 queries in groups of 8 over 871K keys 811 against 746 us): weights rounded to bf16, off by
+      // 2^-9 at most, their sum taken before
+      constexpr int TERMS = RT == 1 ? 2 : 1;
+      b8 pf[RT][TERMS];
 #pragma unroll
       for (int i = 0; i < RT; ++i)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) pf[i][e] = (__bf16)sc[i][e >> 2][e & 3];
+        for (int e = 0; e < 8; ++e) {
+          const float x = sc[i][e >> 2][e & 3];
+          pf[i][0][e] = (__bf16)x;
+          if constexpr (TERMS == 2) pf[i][1][e] = (__bf16)(x - (float)pf[i][0][e]);
+        }
 #pragma unroll
       for (int b = 0; b < NV; ++b) {
         uint32_t x[8];
@@ -306,10 +313,12 @@ __global__ __launch_bounds__(64 * kWaves) void pages_kernel(const AttnArgs p) {
         const b8 hi = __builtin_bit_cast(b8, i4{(int)highs(x[0], x[1]), (int)highs(x[2], x[3]), (int)highs(x[4], x[5]),
                                                 (int)highs(x[6], x[7])});
 #pragma unroll
-        for (int i = 0; i < RT; ++i) {
-          o[i][2 * b] = mfma_bf16(lo, pf[i], o[i][2 * b]);
-          o[i][2 * b + 1] = mfma_bf16(hi, pf[i], o[i][2 * b + 1]);
-        }
+        for (int i = 0; i < RT; ++i)
+#pragma unroll
+          for (int y = TERMS - 1; y >= 0; --y) {
+            o[i][2 * b] = mfma_bf16(lo, pf[i][y], o[i][2 * b]);
+            o[i][2 * b + 1] = mfma_bf16(hi, pf[i][y], o[i][2 * b + 1]);
+          }
       }
     }
   };

@@ -464,6 +464,24 @@ def test_select_ties_missing_pages_and_extreme_scales():
     assert np.array_equal(got, P.select(host(q), c, scales, t, ql, kl, block, page, 6, 1, 2))
 
 
+@pytest.mark.parametrize("hq", [1, 4, 20])
+def test_select_many_of_many(hq):
+    """Choices of 60 and more among hundreds, and hundreds of equal scores."""
+    rng = np.random.default_rng(30 + hq)
+    ql, kl, d, block, page = [9, 2], [16 * 700 + 3, 16 * 400], 64, 16, 64
+    say("select many of many", hq)
+    b, c, s, t = summarised(rng, kl, page, block, 1, d)
+    q = rows(rng, 11, hq, d, "bf16")
+    for rounds in range(2):
+        for topn in (17, 62, 67, 130, 390):
+            got = run_select(b, t, q.cuda(), ql, kl, topn, 1, 2)
+            assert np.array_equal(got, P.select(host(q), c, s, t, ql, kl, block, page, topn, 1, 2))
+        c[rng.random(c.shape[:3]) < 0.9] = c[0, 0, 0]         # most scores equal, some above and some below
+        b.codes.copy_(torch.from_numpy(c))
+        s[:] = 120
+        b.scales.copy_(torch.from_numpy(s))
+
+
 def test_select_many_sequences():
     rng = np.random.default_rng(14)
     kl = [int(x) for x in rng.integers(1, 500, 150)]
