@@ -146,8 +146,9 @@ int dsa_pages_append(const dsa_pages* pages, const dsa_blocks* blocks, const voi
     int st = check_lens(batch, q_lens, kv_lens, "q_len", "kv_len", &tq, &tk);
     if (st == DOSA_OK) st = check_paged(pages, batch, kv_lens);
     if (st == DOSA_OK) st = check_heads(pages->Hkv, pages->Hkv, pages->d);
-    if (st == DOSA_OK) st = check_rows("k", k, k_stride, pages->Hkv, pages->d, pages->dtype, tq);
-    if (st == DOSA_OK) st = check_rows("v", v, v_stride, pages->Hkv, pages->d, pages->dtype, tq);
+    const bool rows = k != nullptr || v != nullptr || blocks == nullptr;      // else summaries alone
+    if (st == DOSA_OK && rows) st = check_rows("k", k, k_stride, pages->Hkv, pages->d, pages->dtype, tq);
+    if (st == DOSA_OK && rows) st = check_rows("v", v, v_stride, pages->Hkv, pages->d, pages->dtype, tq);
     if (st == DOSA_OK && blocks != nullptr) st = check_blocks(blocks);
     if (st != DOSA_OK) return st;
     if (blocks != nullptr && (blocks->num_pages != pages->num_pages || blocks->page_size != pages->page_size ||

@@ -67,9 +67,9 @@ __device__ __forceinline__ void widen64(i4 a, double* x) {
   }
 }
 
-// Rows of a run of positions: the call's own go to their slots bit by bit;
-// where the run is a block that is complete now, all its keys are summed, the
-// earlier ones read from the page.
+// Rows of a run of positions: the call's own go to their slots bit by bit (none
+// without k); where the run is a block that is complete now, all its keys are
+// summed, those that are not the call's read from the page.
 //
 // The mean is summed in 64 bits: keys of 8 or 24 significant bits add up without
 // rounding unless their exponents lie 38 (23) apart, so the codes do not depend
@@ -90,7 +90,8 @@ __global__ __launch_bounds__(256) void rows_append_kernel(const RowsArgs p) {
   const int64_t slot0 = (int64_t)page * size + (base - pg * size);
   const int piece = slice * kRowLanes + lane;
   const bool on = piece < p.pieces;
-  const int lo = max(s.pos0, base), hi = min(s.end, base + p.run);      // the call's own positions
+  const int lo = max(s.pos0, base), hi = min(s.end, base + p.run);      // the call's positions
+  const int given = p.k != nullptr ? s.pos0 : s.end;                    // rows from here on are the call's own
   const bool whole = p.codes != nullptr && s.end >= base + p.run;
   const int64_t row_b = (int64_t)p.pieces * 16;
   double x[E], sum[E] = {};
@@ -104,14 +105,14 @@ __global__ __launch_bounds__(256) void rows_append_kernel(const RowsArgs p) {
       for (int u = 0; u < U; ++u) {
         const int t = t0 + u * SUBS, c = t < hi ? t : hi - 1;
         const int64_t row = s.row0 + (c - s.pos0);
-        k[u] = *reinterpret_cast<const i4*>(c >= s.pos0 ? p.k + row * p.k_stride + piece * 16 : kp + (c - base) * row_b);
-        if (c >= s.pos0) v[u] = *reinterpret_cast<const i4*>(p.v + row * p.v_stride + piece * 16);
+        k[u] = *reinterpret_cast<const i4*>(c >= given ? p.k + row * p.k_stride + piece * 16 : kp + (c - base) * row_b);
+        if (c >= given) v[u] = *reinterpret_cast<const i4*>(p.v + row * p.v_stride + piece * 16);
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int t = t0 + u * SUBS;
         if (t >= hi) break;
-        if (t >= lo) {
+        if (t >= given) {
           const int64_t at = (slot0 + t - base) * row_b + piece * 16;
           *reinterpret_cast<i4*>(p.k_pages + at) = k[u];
           *reinterpret_cast<i4*>(p.v_pages + at) = v[u];

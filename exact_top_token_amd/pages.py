@@ -129,10 +129,12 @@ class Blocks:
                    torch.empty(*shape, dtype=torch.uint8, device=pages.device), pages.page_size)
 
 
-def _free(page_table, free_pages):
+def _free(page_table, free_pages, free_count):
     torch = _torch()
     if free_pages.dim() != 1:
         _bad("free_pages must be int32 [num_pages]")
+    if not 0 <= free_count <= free_pages.shape[0]:
+        _bad(f"free_count must be in 0..{free_pages.shape[0]}, is {free_count}")
     return _tensor(free_pages, "free_pages", torch.int32, free_pages.shape, page_table.device)
 
 
@@ -144,7 +146,7 @@ def dsa_pages_assign(page_table, page_size: int, free_pages, free_count: int, q_
     L, torch = _lib(), _torch()
     n = _pair(q_lens, kv_lens, "q_lens", "kv_lens")
     dev = page_table.device
-    ptab, pfree = _table(page_table, dev, n), _free(page_table, free_pages)
+    ptab, pfree = _table(page_table, dev, n), _free(page_table, free_pages, free_count)
     nq = sum(q_lens)
     ps, pp = _tensor(slots, "slots", torch.int32, (nq,), dev), _tensor(positions, "positions", torch.int32, (nq,), dev)
     left = _I32(int(free_count))
@@ -160,7 +162,7 @@ def dsa_pages_release(page_table, page_size: int, free_pages, free_count: int, n
     L = _lib()
     n = _pair(new_lens, kv_lens, "new_lens", "kv_lens")
     dev = page_table.device
-    ptab, pfree = _table(page_table, dev, n), _free(page_table, free_pages)
+    ptab, pfree = _table(page_table, dev, n), _free(page_table, free_pages, free_count)
     left = _I32(int(free_count))
     with AT._on(dev, stream) as st:
         _check(L.dsa_pages_release(ptab, page_table.shape[1], page_size, free_pages.shape[0], pfree, ctypes.byref(left),
@@ -170,18 +172,22 @@ def dsa_pages_release(page_table, page_size: int, free_pages, free_count: int, n
 
 def dsa_pages_append(pages: Pages, k, v, q_lens, kv_lens, blocks: Optional[Blocks] = None, stream=None):
     """Write the newest q_lens[b] tokens of each sequence, k, v [total_q, Hkv, d] of the pages' type, and the
-    summaries of the blocks that they complete."""
+    summaries of the blocks that they complete.  k = v = None: the summaries alone, from the pages."""
     L = _lib()
     n = pages._batch(q_lens, kv_lens)
     nq = sum(q_lens)
-    if k.device != pages.device or k.dtype != pages.dtype:
-        _bad(f"k must be {pages.dtype} on {pages.device}")
     if blocks is not None and blocks.device != pages.device:
         _bad(f"blocks must be on {pages.device}")
-    sk, sv = _rows(k, "k", pages.Hkv, pages.d, nq, k), _rows(v, "v", pages.Hkv, pages.d, nq, k)
+    if (k is None) != (v is None) or (k is None and blocks is None):
+        _bad("k and v go together, and without them blocks are needed")
+    rows = (None, 0, None, 0)
+    if k is not None:
+        if k.device != pages.device or k.dtype != pages.dtype:
+            _bad(f"k must be {pages.dtype} on {pages.device}")
+        rows = (k.data_ptr(), _rows(k, "k", pages.Hkv, pages.d, nq, k), v.data_ptr(), _rows(v, "v", pages.Hkv, pages.d, nq, k))
     with AT._on(pages.device, stream) as st:
-        _check(L.dsa_pages_append(ctypes.byref(pages.struct), None if blocks is None else ctypes.byref(blocks.struct),
-                                  k.data_ptr(), sk, v.data_ptr(), sv, _lens(q_lens), _lens(kv_lens), n, st))
+        _check(L.dsa_pages_append(ctypes.byref(pages.struct), None if blocks is None else ctypes.byref(blocks.struct), *rows,
+                                  _lens(q_lens), _lens(kv_lens), n, st))
 
 
 def pages_workspace_size(q_lens, kv_lens, Hq: int, Hkv: int, d: int, dtype) -> int:

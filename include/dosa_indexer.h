@@ -455,7 +455,8 @@ int dsa_pages_assign(int32_t* page_table, int32_t max_pages, int32_t page_size, 
 /* The pages behind the first ceil(new_len / page_size) of each sequence go back
  * to the end of the free list, the last page first, and their table entries
  * become -1 (0 <= new_len <= kv_len; a finished sequence's new_len is 0).  A
- * page that sequences share must be given back once. */
+ * page that sequences share must be given back once.  What an entry holds is
+ * given back as it is, a number that names no page too. */
 int dsa_pages_release(int32_t* page_table, int32_t max_pages, int32_t page_size, int32_t num_pages, int32_t* free_pages,
                       int32_t* free_count, const int32_t* new_lens, const int32_t* kv_lens, int32_t batch, void* stream);
 
@@ -491,15 +492,18 @@ typedef struct {
 /* Write the q_lens[b] newest tokens of each sequence, k, v [total_q, Hkv, d] of
  * the pages' dtype, into their slots, bit for bit.  blocks (of the same pages)
  * or NULL: the summaries of the blocks that these tokens make complete are
- * written too, earlier keys of theirs read from the pages.  After an eviction
- * (which moves keys between blocks) summaries are those of the old order. */
+ * written too, earlier keys of theirs read from the pages.  With blocks and k =
+ * v = NULL only summaries are written, all keys read from the pages: of every
+ * block of a sequence with q_len = kv_len, for instance after an eviction (which
+ * moves keys between blocks and leaves the summaries as they were). */
 int dsa_pages_append(const dsa_pages* pages, const dsa_blocks* blocks, const void* k, int64_t k_stride, const void* v,
                      int64_t v_stride, const int32_t* q_lens, const int32_t* kv_lens, int32_t batch, void* stream);
 
 /* Attention of the q_lens[b] newest tokens over the pages, themselves included
  * (append first): chunks of prompts and single tokens mix.  q, out [total_q, Hq,
- * d] of the pages' dtype; out, lse as dsa_cache_attention.  bf16: softmax weights
- * are rounded to bf16 for their product with v.  A page that the table does not
+ * d] of the pages' dtype; out, lse as dsa_cache_attention.  bf16: for their
+ * product with v softmax weights are rounded to bf16, or with few rows (up to 16
+ * queries times group heads) to two bf16 terms.  A page that the table does not
  * name is not seen. */
 size_t dsa_pages_workspace_size(int32_t batch, const int32_t* q_lens, const int32_t* kv_lens, int32_t Hq, int32_t Hkv,
                                 int32_t d, int32_t dtype);
@@ -520,9 +524,8 @@ int dsa_pages_attention(const dsa_pages* pages, const void* q, int64_t q_stride,
  *         subnormal results need, is exact: the choice does not depend on how
  *         sums are ordered.  A block whose table entry names no page scores -inf.
  * 0 <= sinks, 1 <= local, sinks + local <= topn <= 4096; at most 32768 blocks in
- * a sequence.  q [total_q, Hq, d] of q_dtype.  Blocks in front of o must have
- * been complete when they were last appended to (they are, after appends with
- * these summaries). */
+ * a sequence.  q [total_q, Hq, d] of q_dtype.  The summaries of the blocks in
+ * front of o are read, the keys are not. */
 int dsa_block_select(const dsa_blocks* blocks, const int32_t* page_table, int32_t max_pages, const void* q,
                      int64_t q_stride, int32_t q_dtype, const int32_t* q_lens, const int32_t* kv_lens, int32_t batch,
                      int32_t Hq, int32_t sinks, int32_t local, int32_t* idx, int32_t topn, void* stream);
@@ -530,7 +533,9 @@ int dsa_block_select(const dsa_blocks* blocks, const int32_t* page_table, int32_
 /* Attention over listed blocks: query row t of kv head h reads the keys of the
  * blocks idx[t, h, 0..topn-1] that are not behind its position.  Entries that
  * are negative or behind the query's own block are skipped, a block listed twice
- * counts twice.  topn * block <= 2^20.  Otherwise as dsa_pages_attention. */
+ * counts twice.  Neighbouring queries whose lists ascend read the blocks that
+ * they have in common once.  topn * block <= 2^20; the workspace holds up to 16
+ * bytes for each entry of idx.  Otherwise as dsa_pages_attention. */
 size_t dsa_block_workspace_size(int32_t batch, const int32_t* q_lens, const int32_t* kv_lens, int32_t Hq, int32_t Hkv,
                                 int32_t d, int32_t dtype, int32_t block, int32_t topn);
 int dsa_block_attention(const dsa_pages* pages, const void* q, int64_t q_stride, const int32_t* q_lens,

@@ -663,6 +663,27 @@ def test_serving_run(dtype):
     assert left == pool and sorted(free.tolist()) == list(range(pool))
 
 
+def test_summaries_alone():
+    """Summaries of keys that are in the pages already: after an eviction, of all blocks; of the newest only."""
+    rng = np.random.default_rng(25)
+    hk, d, page, kl, new = 2, 64, 32, [100, 70], [64, 48]
+    p, kp, vp, t = filled(rng, kl, page, hk, d, "bf16")
+    acc = torch.rand(p.num_pages, page, device="cuda")
+    src = torch.empty(2, 64, dtype=torch.int32, device="cuda")
+    E.dsa_cache_evict(acc, p.page_table, kl, new, [(p.k, p.k), (p.v, p.v)], src, workspace=space(E.evict_workspace_size(kl, new)))
+    for ql in (new, [20, 1], [0, 16]):
+        say("summaries alone", ql)
+        b = E.Blocks.empty(p, 16)
+        b.codes.fill_(3)
+        b.scales.fill_(9)
+        k, v = p.k.clone(), p.v.clone()
+        E.dsa_pages_append(p, None, None, ql, new, blocks=b)
+        codes, scales = P.summaries(np.nan_to_num(host(p.k)), t, ql, new, 16, np.full(b.codes.shape, 3), np.full(b.scales.shape, 9))
+        assert np.array_equal(b.codes.cpu().numpy(), codes) and np.array_equal(b.scales.cpu().numpy(), scales)
+        bits = lambda x: x.view(torch.int16)
+        assert torch.equal(bits(k), bits(p.k)) and torch.equal(bits(v), bits(p.v))
+
+
 def test_evicted_pages_and_attention():
     """Eviction moves rows of these pages as of any per-slot array; attention over the smaller cache."""
     rng = np.random.default_rng(22)

@@ -63,6 +63,7 @@ def test_cpu_tensors_refused():
     (dict(count=2), -1),                       # three pages needed
     (dict(count=-1), -1),
     (dict(count=9), -1),                       # more than there are
+    (dict(count=2 ** 32 + 8), -1),
     (dict(ql=[41, 1]), -1),
     (dict(ql=[-1, 1]), -1),
     (dict(kl=[70, 1]), -1),                    # the table row ends before the tokens
@@ -174,7 +175,7 @@ def test_append_refusals():
     for o in (dict(k=k[:2]), dict(v=k.float()), dict(k=torch.zeros(3, 2, 128, dtype=torch.bfloat16)[..., :64]),
               dict(k=torch.zeros(1, 2, 64, dtype=torch.bfloat16).expand(3, 2, 64)),
               dict(blocks=E.Blocks.empty(pages(n=5), 16)), dict(blocks=E.Blocks.empty(pages(page=64), 16)),
-              dict(blocks=E.Blocks.empty(pages(hk=1), 16)), dict(blocks=E.Blocks.empty(pages(d=128), 16))):
+              dict(k=None), dict(v=None), dict(k=None, v=None), dict(blocks=E.Blocks.empty(pages(hk=1), 16)), dict(blocks=E.Blocks.empty(pages(d=128), 16))):
         refused(lambda: call(**o))
     refused(lambda: call(pages=pages(page=48), blocks=E.Blocks.empty(pages(page=48), 48)), -2)
 
