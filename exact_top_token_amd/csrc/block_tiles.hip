@@ -20,6 +20,15 @@
 // reduction slots of O^T = V^T P^T the same way makes its right operand without
 // moving a value between lanes.  V^T comes out of row-major LDS tiles through the
 // transposing LDS read.
+//
+// 4096 and 1500 queries, 64 heads on 8, d = 128, each 16 blocks of 64 of up to
+// 32768 keys, of which neighbours share half (66 different ones of 16 queries):
+// 0.59 ms and 32 us of merging; a wavefront a query takes 1.94 ms, merging two
+// queries in a wavefront without LDS 1.36.  Reading the blocks alone takes two
+// thirds of it (6.3 GB, two thirds from the dies' caches), computing alone as much:
+// a workgroup waits for its slowest wavefront at every block, and the CU holds two.
+// Tiles of 32 keys with three under way took 0.70 ms, sixteen wavefronts of 32
+// queries 0.92, the merge by one of the eight wavefronts 1.24.
 #include <type_traits>
 
 #include "attn_device.h"

@@ -7,49 +7,69 @@ namespace dosa {
 
 namespace {
 
-// The record of each lane's token (page).  Most workgroups lie in one sequence;
-// the others search among the records that they span.
-__device__ __forceinline__ int seq_of(const AssignArgs& p, int t) {
-  const int first = blockIdx.x * 256, last = min(first + 255, p.n_tok - 1);
-  auto tok0 = [](const AssignSeq& s) { return s.tok0; };
-  int lo = find_seq(p.s, p.n_seq, first, tok0), hi = find_seq(p.s, p.n_seq, last, tok0);
-  if (lo == hi) return lo;
-  __shared__ int starts[kAssignSeqs];
-  for (int i = lo + (int)threadIdx.x; i <= hi; i += 256) starts[i] = p.s[i].tok0;
-  __syncthreads();
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (starts[mid] <= t) lo = mid; else hi = mid - 1;
+// A workgroup takes kSpan tokens (pages): enough that its two searches among the
+// records are a small part of it (1.2M tokens of 300 prompts: 10 us, 13 with 256; a
+// decode step of 128 sequences 4 us, latency).
+// Most lie in one sequence; the others search among the records that they span.
+constexpr int kSpan = 1024;
+struct Span {
+  int lo, hi;            // records of the first and the last
+  const int* starts;     // first tokens of the records, in LDS
+  __device__ __forceinline__ int find(int t) const {
+    int a = lo, b = hi;
+    while (a < b) {
+      const int mid = (a + b + 1) >> 1;
+      if (starts[mid] <= t) a = mid; else b = mid - 1;
+    }
+    return a;
   }
-  return lo;
+};
+__device__ __forceinline__ Span span_of(const AssignArgs& p, int* starts) {
+  const int first = blockIdx.x * kSpan, last = min(first + kSpan - 1, p.n_tok - 1);
+  auto tok0 = [](const AssignSeq& s) { return s.tok0; };
+  const Span x{find_seq(p.s, p.n_seq, first, tok0), find_seq(p.s, p.n_seq, last, tok0), starts};
+  if (x.lo < x.hi) {
+    for (int i = x.lo + (int)threadIdx.x; i <= x.hi; i += 256) starts[i] = p.s[i].tok0;
+    __syncthreads();
+  }
+  return x;
 }
 
-// A thread a token.  A sequence's n-th new page is read from the free list
-// where it is used, so no token waits for another's table write; the token
+// A thread a token at a time.  A sequence's n-th new page is read from the free
+// list where it is used, so no token waits for another's table write; the token
 // that opens a page writes its entry.
 __global__ __launch_bounds__(256) void assign_kernel(const AssignArgs p) {
-  const int t = blockIdx.x * 256 + threadIdx.x;
-  const int i = seq_of(p, t);
-  if (t >= p.n_tok) return;
-  const AssignSeq s = p.s[i];
-  const int size = p.page_div.by, pos = s.pos0 + (t - s.tok0);
-  const int pg = p.page_div.quot(pos), in = pos - pg * size;
-  const int first = p.page_div.quot((uint32_t)s.pos0 + (uint32_t)size - 1u);    // first new page
-  int32_t* entry = p.table + (int64_t)(p.b0 + i) * p.max_pages + pg;
-  const int page = pg >= first ? p.free_pages[p.top - 1 - (s.new0 + pg - first)] : *entry;
-  if (pg >= first && in == 0) *entry = page;
-  if (p.slots != nullptr) p.slots[t] = (uint32_t)page < (uint32_t)p.num_pages ? page * size + in : -1;
-  if (p.positions != nullptr) p.positions[t] = pos;
+  __shared__ int starts[kAssignSeqs];
+  const Span span = span_of(p, starts);
+  const int size = p.page_div.by;
+#pragma unroll
+  for (int u = 0; u < kSpan / 256; ++u) {
+    const int t = blockIdx.x * kSpan + u * 256 + threadIdx.x;
+    if (t >= p.n_tok) return;
+    const int i = span.find(t);
+    const AssignSeq s = p.s[i];
+    const int pos = s.pos0 + (t - s.tok0), pg = p.page_div.quot(pos), in = pos - pg * size;
+    const int first = p.page_div.quot((uint32_t)s.pos0 + (uint32_t)size - 1u);    // first new page
+    int32_t* entry = p.table + (int64_t)(p.b0 + i) * p.max_pages + pg;
+    const int page = pg >= first ? p.free_pages[p.top - 1 - (s.new0 + pg - first)] : *entry;
+    if (pg >= first && in == 0) *entry = page;
+    if (p.slots != nullptr) p.slots[t] = (uint32_t)page < (uint32_t)p.num_pages ? page * size + in : -1;
+    if (p.positions != nullptr) p.positions[t] = pos;
+  }
 }
 
-// A thread a page.
+// A thread a page at a time.
 __global__ __launch_bounds__(256) void release_kernel(const AssignArgs p) {
-  const int t = blockIdx.x * 256 + threadIdx.x;
-  const int i = seq_of(p, t);
-  if (t >= p.n_tok) return;
-  int32_t* entry = p.table + (int64_t)(p.b0 + i) * p.max_pages + p.s[i].pos0 + (t - p.s[i].tok0);
-  p.free_pages[p.top - 1 - t] = *entry;
-  *entry = -1;
+  __shared__ int starts[kAssignSeqs];
+  const Span span = span_of(p, starts);
+  for (int u = 0; u < kSpan / 256; ++u) {
+    const int t = blockIdx.x * kSpan + u * 256 + threadIdx.x;
+    if (t >= p.n_tok) return;
+    const int i = span.find(t);
+    int32_t* entry = p.table + (int64_t)(p.b0 + i) * p.max_pages + p.s[i].pos0 + (t - p.s[i].tok0);
+    p.free_pages[p.top - 1 - t] = *entry;
+    *entry = -1;
+  }
 }
 
 // 16 bytes of a row -> its elements in 64 bits.
@@ -67,6 +87,12 @@ __device__ __forceinline__ void widen64(i4 a, double* x) {
   }
 }
 
+// Bound by memory: 31011 tokens of 8 heads, d = 128, bf16, with their summaries,
+// 255 MB, in 43 us (fp32, twice that, 115 us); a decode step's 128 tokens, of which
+// two complete a block, 6 us, latency.  A slice of 32 pieces of 16 bytes and eight
+// tokens at a time give a block of 64 tokens four workgroups and eight loads a
+// thread.
+//
 // Rows of a run of positions: the call's own go to their slots bit by bit (none
 // without k); where the run is a block that is complete now, all its keys are
 // summed, those that are not the call's read from the page.
@@ -160,13 +186,13 @@ __global__ __launch_bounds__(256) void rows_append_kernel(const RowsArgs p) {
 
 hipError_t launch_assign(const AssignArgs& p, hipStream_t s) {
   if (p.n_tok == 0) return hipSuccess;
-  assign_kernel<<<dim3((unsigned)((p.n_tok + 255) / 256)), dim3(256), 0, s>>>(p);
+  assign_kernel<<<dim3((unsigned)(((int64_t)p.n_tok + kSpan - 1) / kSpan)), dim3(256), 0, s>>>(p);
   return hipGetLastError();
 }
 
 hipError_t launch_release(const AssignArgs& p, hipStream_t s) {
   if (p.n_tok == 0) return hipSuccess;
-  release_kernel<<<dim3((unsigned)((p.n_tok + 255) / 256)), dim3(256), 0, s>>>(p);
+  release_kernel<<<dim3((unsigned)(((int64_t)p.n_tok + kSpan - 1) / kSpan)), dim3(256), 0, s>>>(p);
   return hipGetLastError();
 }
 

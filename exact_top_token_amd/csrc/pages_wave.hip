@@ -19,8 +19,13 @@
 // through a buffer descriptor that ends behind the tile's last key: rows
 // behind it, and all rows of a tile without a page, arrive as zeros whatever
 // memory holds there.  (A weight of 0 is still multiplied by a value.)
-#include <type_traits>
-
+//
+// Bound by memory: decode of 48 sequences, 64 heads on 8, d = 128, bf16, over
+// 888K keys, 3.64 GB: 0.62 ms, 5.9 TB/s, and 8 us of join (fp32 keys 6.1 TB/s,
+// d = 64 5.6).  32 listed blocks of 64 keys for each of 64 queries, 535 MB: 80 us
+// and 7 of join; merging the two queries of a sequence, which share half of their
+// blocks, took 10 us more than it saved, since the caches share them anyway.  One
+// fp32 token over 5003 keys, d = 64: 6 + 5 us, latency.
 #include "attn_device.h"
 
 namespace dosa {
