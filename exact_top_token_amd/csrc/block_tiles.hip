@@ -23,10 +23,11 @@
 //
 // 4096 and 1500 queries, 64 heads on 8, d = 128, each 16 blocks of 64 of up to
 // 32768 keys, of which neighbours share half (66 different ones of 16 queries):
-// 0.59 ms and 32 us of merging; a wavefront a query takes 1.94 ms, merging two
-// queries in a wavefront without LDS 1.36.  Reading the blocks alone takes two
-// thirds of it (6.3 GB, two thirds from the dies' caches), computing alone as much:
-// a workgroup waits for its slowest wavefront at every block, and the CU holds two.
+// 0.54 ms and 31 us of merging; a wavefront a query takes 1.94 ms, merging two
+// queries in a wavefront without LDS 1.36.  Reading the blocks alone took 0.46 ms
+// (6.2 GB, two thirds from the dies' caches): a workgroup waits for its slowest
+// wavefront at every block, and the CU holds two.  Addresses worked out anew for
+// every load and scores masked one by one, not rows, cost 0.05 ms.
 // Tiles of 32 keys with three under way took 0.70 ms, sixteen wavefronts of 32
 // queries 0.92, the merge by one of the eight wavefronts 1.24.
 #include <type_traits>
@@ -175,14 +176,14 @@ __global__ __launch_bounds__(64 * kMergeWaves) void block_merge_kernel(const Att
 }
 
 // 16-byte chunk of row `r` that holds logical chunk c.  Key tiles: 16 lanes
-// read one chunk of 16 rows; value tiles: 16 lanes read 32 bytes of 4 rows.
+// read one chunk of 16 rows; value tiles: 32 lanes read 32 bytes of 8 rows.
 template <int D>
 __device__ __forceinline__ int k_chunk(int r, int c) {
   return D == 128 ? c ^ (r & 15) : c ^ ((r >> 1) & 7);
 }
 template <int D>
 __device__ __forceinline__ int v_chunk(int r, int c) {
-  return D == 128 ? c ^ ((r & 3) << 2) : c ^ (((r >> 1) & 1) << 2);
+  return D == 128 ? c ^ ((r & 7) << 1) : c ^ (((r >> 1) & 3) << 1);
 }
 
 // Transposed value operands of four 16-dimension columns and 32 keys: eight
@@ -238,7 +239,7 @@ __global__ __launch_bounds__(64 * NW, 4) void block_tiles_kernel(const AttnArgs 
   const uint32_t bit = 1u << (r / p.group);
   const int before = sq.kv_len - sq.q_len, vis = before + row_q + 1;
   const int vis_first = before + q_first + 1, vis_end = before + sh.q_end;
-  const uint32_t full = (1u << n_tok) - 1u, mask = active ? full : 0u;
+  const uint32_t mask = active ? (1u << n_tok) - 1u : 0u;
   const int of_shift = q_first - sh.q0;
 
   b8 qf[NS];
@@ -289,8 +290,21 @@ __global__ __launch_bounds__(64 * NW, 4) void block_tiles_kernel(const AttnArgs 
 
   // ---- tiles to LDS ----
   const uint16_t *kg = static_cast<const uint16_t*>(p.k) + sh.head * D, *vg = static_cast<const uint16_t*>(p.v) + sh.head * D;
+  // A load fills RPI rows.  Its rows and a lane's chunk of them do not change: a tile whose rows are all visible
+  // needs one scalar base a load, and the vector unit nothing.
   const int lr = lane / CH, lc = lane % CH;
+  uint32_t f_row[LOADS], f_chunk[LOADS], f_off[LOADS];     // row within the run, bytes
+#pragma unroll
+  for (int x = 0; x < LOADS; ++x) {
+    const int i = wave * LOADS + x, which = i / (kKeys / RPI), row = i % (kKeys / RPI) * RPI + lr;
+    f_row[x] = row % RUN;
+    f_chunk[x] = 16 * (which == 0 ? k_chunk<D>(row, lc) : v_chunk<D>(row, lc));
+    f_off[x] = f_row[x] * (uint32_t)p.k_stride * 2 + f_chunk[x];
+  }
   auto fetch = [&](const Tile& tile, int buf) {
+    bool whole = tile.pos[0] >= 0;
+#pragma unroll
+    for (int y = 0; y < RUNS; ++y) whole = whole && tile.pos[y] + RUN <= vis_end;
 #pragma unroll
     for (int x = 0; x < LOADS; ++x) {
       const int i = wave * LOADS + x, which = i / (kKeys / RPI), at = i % (kKeys / RPI) * RPI, run = at / RUN;
@@ -300,11 +314,15 @@ __global__ __launch_bounds__(64 * NW, 4) void block_tiles_kernel(const AttnArgs 
         slot = run == y ? tile.slot[y] : slot;
         pos = run == y ? tile.pos[y] : pos;
       }
-      // rows behind the last visible key, which may hold anything, are read as it (it may lie in front of the tile)
-      const int row = at + lr, in = row % RUN, lim = pos < 0 ? 0 : vis_end - 1 - pos;
-      const int ch = which == 0 ? k_chunk<D>(row, lc) : v_chunk<D>(row, lc);
-      const uint16_t* from = (which == 0 ? kg : vg) + (int64_t)(slot + (in < lim ? in : lim)) * p.k_stride + 8 * ch;
-      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)from,
+      const uint8_t* from = reinterpret_cast<const uint8_t*>((which == 0 ? kg : vg) + (int64_t)slot * p.k_stride);
+      uint32_t off = f_off[x];
+      if (!whole) {
+        // rows behind the last visible key, which may hold anything, are read as it (it may lie in front of the tile)
+        const int lim = pos < 0 ? 0 : vis_end - 1 - pos, back = lim < 0 ? lim : 0;
+        from += (int64_t)back * p.k_stride * 2;
+        off = (uint32_t)(((int)f_row[x] < lim ? (int)f_row[x] : lim) - back) * (uint32_t)p.k_stride * 2 + f_chunk[x];
+      }
+      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(from + off),
                                        (__attribute__((address_space(3))) void*)(&lds[buf][which][at * D * 2]), 16, 0, 0);
     }
   };
@@ -328,12 +346,19 @@ __global__ __launch_bounds__(64 * NW, 4) void block_tiles_kernel(const AttnArgs 
     for (int s = 0; s < NS; ++s)
 #pragma unroll
       for (int a = 0; a < 4; ++a) sc[a] = mfma_bf16(*(lds_b8*)(tile + ka[s] + 16 * a * (D * 2)), qf[s], sc[a]);
+    // A tile of one block, or of a part of one: rows that do not list it keep their maximum, and their weights are
+    // cleared once they are packed.  Scores are masked one by one only where keys are hidden or blocks are smaller.
+    bool on = true;
+    bool edge = RUNS > 1;
+    if constexpr (RUNS == 1) {
+      on = (x.of[0] & bit) != 0;
+      edge = x.pos[0] + kKeys > vis_first;
+    }
+    if (edge) {
 #pragma unroll
-    for (int a = 0; a < 4; ++a) {
-      const uint32_t of = x.of[16 * a / RUN];
-      const int pos = x.pos[16 * a / RUN] + 16 * a % RUN;
-      if (of != full || pos + 16 > vis_first) {
-        const int end = of & bit ? vis - pos : 0;
+      for (int a = 0; a < 4; ++a) {
+        const int pos = x.pos[16 * a / RUN] + 16 * a % RUN;
+        const int end = x.of[16 * a / RUN] & bit ? vis - pos : 0;
 #pragma unroll
         for (int e = 0; e < 4; ++e) sc[a][e] = 4 * g + e >= end ? -INFINITY : sc[a][e];
       }
@@ -344,6 +369,7 @@ __global__ __launch_bounds__(64 * NW, 4) void block_tiles_kernel(const AttnArgs 
 #pragma unroll
       for (int e = 0; e < 4; ++e) top = fmaxf(top, sc[a][e]);
     top = max_groups(top);
+    top = on ? top : -INFINITY;
     if (__any((top - m) * c > kSlack)) {     // (-inf) - (-inf) compares false
       const float mn = fmaxf(m, top);
       const float f = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((m - mn) * c);
@@ -354,8 +380,8 @@ __global__ __launch_bounds__(64 * NW, 4) void block_tiles_kernel(const AttnArgs 
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[j][e] *= f;
     }
-    float mc = m * c;
-    if (__any(fabsf(mc) > kFar)) {         // or a row that has seen nothing
+    float mc = m == -INFINITY ? 0.f : m * c;   // a row that has seen nothing: its scores are -inf, or it does not list the tile
+    if (__any(fabsf(mc) > kFar)) {
       const float off = m == -INFINITY ? 0.f : m;
 #pragma unroll
       for (int a = 0; a < 4; ++a)
@@ -363,21 +389,29 @@ __global__ __launch_bounds__(64 * NW, 4) void block_tiles_kernel(const AttnArgs 
         for (int e = 0; e < 4; ++e) sc[a][e] -= off;
       mc = 0.f;
     }
-    b8 pf[2];
+    union { b8 b[2]; uint32_t w[8]; } pf;
+    float sum = 0.f;
 #pragma unroll
     for (int a = 0; a < 4; ++a)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float w = __builtin_amdgcn_exp2f(fmaf(sc[a][e], c, -mc));
-        l += w;
-        pf[a >> 1][4 * (a & 1) + e] = (__bf16)w;
+        sum += w;
+        pf.b[a >> 1][4 * (a & 1) + e] = (__bf16)w;
       }
+    if constexpr (RUNS == 1) {
+      sum = on ? sum : 0.f;
+      const uint32_t keep = on ? 0xffffffffu : 0u;
+#pragma unroll
+      for (int x = 0; x < 8; ++x) pf.w[x] &= keep;
+    }
+    l += sum;
     auto values = [&](auto sel) {
       constexpr int U = decltype(sel)::value & 1, J = decltype(sel)::value >> 1, AT = BUF * 2 * TILE + TILE + 32 * U * D * 2;
       b8 w[4];
       read_values<AT, AT + 16 * D * 2>(va + 4 * J, w);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) o[4 * J + j] = mfma_bf16(w[j], pf[U], o[4 * J + j]);
+      for (int j = 0; j < 4; ++j) o[4 * J + j] = mfma_bf16(w[j], pf.b[U], o[4 * J + j]);
     };
     values(std::integral_constant<int, 0>{});
     values(std::integral_constant<int, 1>{});
