@@ -157,7 +157,7 @@ __global__ __launch_bounds__(64 * NW, 2) void prompt_kernel(const AttnArgs p) {
 
   // The same over pages (4096 queries over 65536 keys, 32 heads on 8, d = 128:
   // 3.85 to 3.97 ms, 1070 to 1110 TFLOP/s; 1024 over 16384 0.28 ms, in pages of 16
-  // with four look-ups a tile 0.46 ms).  A tile's page numbers (one of 64 rows, or of each 16)
+  // with four look-ups a tile 0.34 ms).  A tile's page numbers (one of 64 rows, or of each 16)
   // are looked up through the scalar cache a turn before its keys are fetched and
   // kept until its values have been.  A wavefront's rows of a tile lie in 16
   // rows, `part`; those past the last visible key repeat it.  Rows without a page

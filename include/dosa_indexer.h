@@ -504,7 +504,8 @@ int dsa_pages_append(const dsa_pages* pages, const dsa_blocks* blocks, const voi
  * d] of the pages' dtype; out, lse as dsa_cache_attention.  bf16: for their
  * product with v softmax weights are rounded to bf16, or with few rows (up to 16
  * queries times group heads) to two bf16 terms.  A page that the table does not
- * name is not seen. */
+ * name is not seen.  q and what the slots below kv_len hold must be finite: a
+ * number that is not may reach every query of the sequence. */
 size_t dsa_pages_workspace_size(int32_t batch, const int32_t* q_lens, const int32_t* kv_lens, int32_t Hq, int32_t Hkv,
                                 int32_t d, int32_t dtype);
 int dsa_pages_attention(const dsa_pages* pages, const void* q, int64_t q_stride, const int32_t* q_lens,
