@@ -28,7 +28,9 @@
 // (6.2 GB, two thirds from the dies' caches): a workgroup waits for its slowest
 // wavefront at every block, and the CU holds two.  Addresses worked out anew for
 // every load and scores masked one by one, not rows, cost 0.05 ms.
-// Tiles of 32 keys with three under way took 0.70 ms, sixteen wavefronts of 32
+// Keys and values in five slots of half a tile, twice as much under way but a
+// barrier for each half, took 0.62 ms, in four slots 0.63 (against 0.56, merging
+// included); tiles of 32 keys with three under way 0.70, sixteen wavefronts of 32
 // queries 0.92, the merge by one of the eight wavefronts 1.24.
 #include <type_traits>
 
