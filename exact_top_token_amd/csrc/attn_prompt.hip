@@ -186,7 +186,7 @@ __global__ __launch_bounds__(64 * NW, 2) void prompt_kernel(const AttnArgs p) {
     }
     return x;
   };
-  auto judge = [&](Pages& x) {
+  auto resolve = [&](Pages& x) {
     x.gone = 0;
 #pragma unroll
     for (int a = 0; a < N16; ++a) {
@@ -357,8 +357,8 @@ __global__ __launch_bounds__(64 * NW, 2) void prompt_kernel(const AttnArgs p) {
       f16v sa[2], sb[2];
       // pages of the tile whose values are used, of the next one, of the one after
       Pages p0 = look(0), p1 = look(1), p2 = look(2);
-      judge(p0);
-      judge(p1);
+      resolve(p0);
+      resolve(p1);
       fetch_page(0, kg, p.k_stride, 0, p0);
       ready();
       if (tiles > 1) fetch_page(0, kg, p.k_stride, 1, p1);
@@ -368,7 +368,7 @@ __global__ __launch_bounds__(64 * NW, 2) void prompt_kernel(const AttnArgs p) {
         __builtin_amdgcn_s_waitcnt(0x0f70);
         clear(t, p0);
         __syncthreads();
-        judge(p2);
+        resolve(p2);
         if (t + 2 < tiles) fetch_page(0, kg, p.k_stride, t + 2, p2);
         if (t + 1 < tiles) fetch_page(1, vg, p.v_stride, t + 1, p1);
         const int gone = p0.gone;

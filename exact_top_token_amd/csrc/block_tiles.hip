@@ -131,12 +131,12 @@ __global__ __launch_bounds__(64 * kMergeWaves) void block_merge_kernel(const Att
   constexpr uint32_t kEnd = 0xffffffffu, kNone = 0xfffffffeu;      // no more entries; an entry to skip
   const uint32_t own = (uint32_t)(sq.kv_len - sq.q_len + sh.q0 + lane) >> lb;
   int at = e_lo;
-  auto judge = [&]() -> uint32_t {
+  auto front = [&]() -> uint32_t {
     if (lane >= n_tok || at >= e_end) return kEnd;
     const uint32_t y = (uint32_t)listed[lane * win + ((at - e_lo) & (win - 1))];
     return y <= own ? y : kNone;
   };
-  uint32_t cur = judge();
+  uint32_t cur = front();
   i4* out = reinterpret_cast<i4*>(p.merged) + (int64_t)unit * p.merged_stride;
   uint32_t blk = 0;
   while (blk != kEnd) {
@@ -158,7 +158,7 @@ __global__ __launch_bounds__(64 * kMergeWaves) void block_merge_kernel(const Att
         }
         wave_sync();
       }
-      if (take) cur = judge();
+      if (take) cur = front();
       if (blk == kNone) continue;
       if (lane == n) {
         mine = (int)blk;
