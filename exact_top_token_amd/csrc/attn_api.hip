@@ -56,11 +56,29 @@ constexpr int64_t kTiledMinKeys = 512;
 
 constexpr int64_t kTiledBlockRows = 64;  // over listed blocks: half a workgroup's rows
 
-bool takes_tiled(int src, int64_t rows, bool sel) {
-  if (sel) return src == A_P16 && rows > kTiledBlockRows;
-  return (src == A_BF16 && rows > kTiledRows) || (src == A_P16 && rows > kTiledPageRows);
+// Sequences that share launches.  Over bf16 pages the wavefront kernel's row
+// tiles decide how softmax weights are rounded, so sequences of one tile and of
+// two are launches of their own: what a sequence gets does not depend on its
+// neighbours.
+enum AttnClass : int { C_WAVES = 0, C_WAVES2 = 1, C_TILED = 2, C_COUNT = 3 };
+
+// The classes there are, in the order of their launches; the others have no sequences.
+struct AttnClasses {
+  AttnClass of[C_COUNT];
+  int n;
+};
+AttnClasses classes_of(int src, bool sel) {
+  if (src == A_P16 && !sel) return {{C_TILED, C_WAVES2, C_WAVES}, 3};
+  if (src == A_P16 || src == A_BF16) return {{C_TILED, C_WAVES}, 2};
+  return {{C_WAVES}, 1};
 }
-int attn_classes(int src) { return src == A_BF16 || src == A_P16 ? 2 : 1; }
+
+AttnClass class_of(int src, int64_t rows, bool sel) {
+  if (src == A_BF16) return rows > kTiledRows ? C_TILED : C_WAVES;
+  if (src != A_P16) return C_WAVES;
+  if (sel) return rows > kTiledBlockRows ? C_TILED : C_WAVES;
+  return rows > kTiledPageRows ? C_TILED : rows > 16 ? C_WAVES2 : C_WAVES;
+}
 
 // Range length of the tiled kernel where a launch is less than two rounds of
 // the GPU and its units differ: the one for which the longest unit or the mean
@@ -93,13 +111,13 @@ int64_t balanced_len(const AttnArgs& a, int64_t len, int64_t tile) {
   return len;
 }
 
-// Sequences b0.. of the batch that the kernel takes, at most kAttnSeqs with
+// Sequences b0.. of the batch that are of the class, at most kAttnSeqs with
 // queries; returns the sequence after the last one seen, or -1 if the launch
 // would be too large.
-int plan_attn(AttnChunk& ch, int src, int d, bool tiled, int b0, int32_t batch, const int32_t* q_lens, const int32_t* kv_lens,
+int plan_attn(AttnChunk& ch, int src, int d, AttnClass cls, int b0, int32_t batch, const int32_t* q_lens, const int32_t* kv_lens,
               int32_t Hq, int32_t Hkv, int32_t topk, int32_t block, int64_t* q_row, int64_t* k_row) {
   AttnArgs& a = ch.a;
-  const bool sel = topk > 0;
+  const bool sel = topk > 0, tiled = cls == C_TILED;
   a.Hq = Hq;
   a.Hkv = Hkv;
   a.group = Hq / Hkv;
@@ -108,7 +126,7 @@ int plan_attn(AttnChunk& ch, int src, int d, bool tiled, int b0, int32_t batch, 
   int b = b0;
   int64_t most = 0;
   for (; b < batch && a.n_seq < kAttnSeqs; ++b) {
-    if (q_lens[b] > 0 && takes_tiled(src, (int64_t)q_lens[b] * a.group, sel) == tiled) {
+    if (q_lens[b] > 0 && class_of(src, (int64_t)q_lens[b] * a.group, sel) == cls) {
       AttnSeq& s = a.s[a.n_seq++];
       s = AttnSeq{};
       s.q_row0 = (int32_t)*q_row;
@@ -199,14 +217,16 @@ namespace dosa {
 size_t attn_workspace(int src, int32_t batch, const int32_t* q_lens, const int32_t* kv_lens, int32_t Hq, int32_t Hkv,
                       int32_t d, int32_t topk, int32_t block, int64_t* threads) {
   size_t most = 256;
-  for (int tiled = 0; tiled < attn_classes(src); ++tiled) {
+  const AttnClasses classes = classes_of(src, topk > 0);
+  for (int i = 0; i < classes.n; ++i) {
+    const AttnClass cls = classes.of[i];
     int64_t qr = 0, kr = 0;
     for (int b = 0; b < batch;) {
       AttnChunk ch;
-      b = plan_attn(ch, src, d, tiled != 0, b, batch, q_lens, kv_lens, Hq, Hkv, topk, block, &qr, &kr);
+      b = plan_attn(ch, src, d, cls, b, batch, q_lens, kv_lens, Hq, Hkv, topk, block, &qr, &kr);
       if (b < 0) return 0;
       most = std::max(most, part_bytes(ch, d));
-      if (threads != nullptr) *threads = std::max(*threads, attn_threads(ch, tiled != 0));
+      if (threads != nullptr) *threads = std::max(*threads, attn_threads(ch, cls == C_TILED));
     }
   }
   return most;
@@ -214,21 +234,23 @@ size_t attn_workspace(int src, int32_t batch, const int32_t* q_lens, const int32
 
 int run_attn(int src, const AttnArgs& base, int32_t batch, const int32_t* q_lens, const int32_t* kv_lens, int32_t d,
              void* workspace, size_t workspace_bytes, hipStream_t stream) {
-  // each kernel's first launch is planned once, for the size check and the run
-  AttnChunk head[2];
-  int next[2];
-  int64_t qr[2] = {0, 0}, kr[2] = {0, 0}, threads = 0;
-  const int classes = attn_classes(src);
+  // each class's first launch is planned once, for the size check and the run
+  const AttnClasses classes = classes_of(src, base.topk > 0);
+  AttnChunk head[C_COUNT];
+  int next[C_COUNT];
+  int64_t qr[C_COUNT] = {}, kr[C_COUNT] = {}, threads = 0;
   size_t need = 256;
-  for (int tiled = 0; tiled < classes; ++tiled) {
-    head[tiled].a = base;
-    next[tiled] = plan_attn(head[tiled], src, d, tiled != 0, 0, batch, q_lens, kv_lens, base.Hq, base.Hkv, base.topk,
-                            base.block, &qr[tiled], &kr[tiled]);
-    if (next[tiled] < 0) return fail(DOSA_ERR_UNSUPPORTED, "too many row tiles and key ranges for one launch");
-    need = std::max(need, part_bytes(head[tiled], d));
-    threads = std::max(threads, attn_threads(head[tiled], tiled != 0));
+  bool more = false;
+  for (int i = 0; i < classes.n; ++i) {
+    head[i].a = base;
+    next[i] = plan_attn(head[i], src, d, classes.of[i], 0, batch, q_lens, kv_lens, base.Hq, base.Hkv, base.topk,
+                        base.block, &qr[i], &kr[i]);
+    if (next[i] < 0) return fail(DOSA_ERR_UNSUPPORTED, "too many row tiles and key ranges for one launch");
+    need = std::max(need, part_bytes(head[i], d));
+    threads = std::max(threads, attn_threads(head[i], classes.of[i] == C_TILED));
+    more = more || next[i] < batch;
   }
-  if (next[0] < batch || next[classes - 1] < batch) {
+  if (more) {
     need = attn_workspace(src, batch, q_lens, kv_lens, base.Hq, base.Hkv, d, base.topk, base.block, &threads);
     if (need == 0) return fail(DOSA_ERR_UNSUPPORTED, "too many row tiles and key ranges for one launch");
   }
@@ -236,10 +258,11 @@ int run_attn(int src, const AttnArgs& base, int32_t batch, const int32_t* q_lens
   if (st != DOSA_OK) return st;
   if (workspace == nullptr || workspace_bytes < need || !aligned(workspace, 16))
     return fail(DOSA_ERR_WORKSPACE, "workspace needs " + std::to_string(need) + " bytes, 16-byte aligned");
-  for (int tiled = classes - 1; tiled >= 0; --tiled) {
-    AttnChunk& ch = head[tiled];
+  for (int i = 0; i < classes.n; ++i) {
+    const bool tiled = classes.of[i] == C_TILED;
+    AttnChunk& ch = head[i];
     AttnArgs& a = ch.a;
-    for (int b = next[tiled];;) {
+    for (int b = next[i];;) {
       const size_t rows = (size_t)ch.parts * 16 * a.rt;
       char* at = static_cast<char*>(workspace);
       a.merged = reinterpret_cast<int4*>(at);
@@ -264,8 +287,8 @@ int run_attn(int src, const AttnArgs& base, int32_t batch, const int32_t* q_lens
         if (e != hipSuccess) return fail_hip(e, "attention join launch");
       }
       if (b >= batch) break;
-      b = plan_attn(ch, src, d, tiled != 0, b, batch, q_lens, kv_lens, base.Hq, base.Hkv, base.topk, base.block,
-                    &qr[tiled], &kr[tiled]);
+      b = plan_attn(ch, src, d, classes.of[i], b, batch, q_lens, kv_lens, base.Hq, base.Hkv, base.topk, base.block,
+                    &qr[i], &kr[i]);
     }
   }
   return DOSA_OK;

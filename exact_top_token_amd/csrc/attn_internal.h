@@ -77,7 +77,8 @@ struct AttnArgs {
 // per key, and are the faster for it: 32 sequences x 4 queries in groups of 8
 // over 871K keys 242 us, 330 us as one tile of a head pair (which does not
 // spill).  A launch takes what its largest sequence needs: one such sequence
-// among 31 of 2 queries costs 241 instead of 207 us.
+// among 31 of 2 queries costs 241 instead of 207 us (bf16 pages, whose rounding
+// follows the tiles, are launches of one kind of sequence).
 constexpr int attn_max_rt(int src, int d) {
   return src == A_MX || src == A_P16 || ((src == A_F32 || src == A_P32) && d == 64) ? 2 : 1;
 }

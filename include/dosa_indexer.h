@@ -502,10 +502,11 @@ int dsa_pages_append(const dsa_pages* pages, const dsa_blocks* blocks, const voi
 /* Attention of the q_lens[b] newest tokens over the pages, themselves included
  * (append first): chunks of prompts and single tokens mix.  q, out [total_q, Hq,
  * d] of the pages' dtype; out, lse as dsa_cache_attention.  bf16: for their
- * product with v softmax weights are rounded to bf16, or with few rows (up to 16
- * queries times group heads) to two bf16 terms.  A page that the table does not
- * name is not seen.  q and what the slots below kv_len hold must be finite: a
- * number that is not may reach every query of the sequence. */
+ * product with v the softmax weights of a sequence of few rows (up to 16 queries
+ * times group heads) are two bf16 terms, whatever else is in the call; those of
+ * other sequences are rounded to bf16.  A page that the table does not name is
+ * not seen.  q and what the slots below kv_len hold must be finite: a number
+ * that is not may reach every query of the sequence. */
 size_t dsa_pages_workspace_size(int32_t batch, const int32_t* q_lens, const int32_t* kv_lens, int32_t Hq, int32_t Hkv,
                                 int32_t d, int32_t dtype);
 int dsa_pages_attention(const dsa_pages* pages, const void* q, int64_t q_stride, const int32_t* q_lens,
@@ -536,7 +537,9 @@ int dsa_block_select(const dsa_blocks* blocks, const int32_t* page_table, int32_
  * are negative or behind the query's own block are skipped, a block listed twice
  * counts twice.  Neighbouring queries whose lists ascend read the blocks that
  * they have in common once.  topn * block <= 2^20; the workspace holds up to 16
- * bytes for each entry of idx.  Otherwise as dsa_pages_attention. */
+ * bytes for each entry of idx.  bf16: softmax weights are two bf16 terms for
+ * sequences of up to 64 rows (queries times group heads) in groups of up to 16
+ * heads, else rounded to bf16.  Otherwise as dsa_pages_attention. */
 size_t dsa_block_workspace_size(int32_t batch, const int32_t* q_lens, const int32_t* kv_lens, int32_t Hq, int32_t Hkv,
                                 int32_t d, int32_t dtype, int32_t block, int32_t topn);
 int dsa_block_attention(const dsa_pages* pages, const void* q, int64_t q_stride, const int32_t* q_lens,

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import exact_top_token_amd as E
-from attention_helpers import B, U, check_attention, rows, table
+from attention_helpers import B, U, check_attention, rows, table, weight_err
 from oracle import attention as A
 from oracle import pages as P
 
@@ -810,3 +810,58 @@ def test_pass_times_are_reported():
     t = E.profile_end()
     assert {"pages_assign", "pages_release", "pages_append", "pages_attention", "block_select", "block_attention"} <= set(t)
     assert all(n >= 1 and ms > 0 for n, ms in t.values())
+
+
+# ----------------------------------------------------------------------------
+# what a sequence gets does not depend on its neighbours
+# ----------------------------------------------------------------------------
+def check_two_terms(out, ref, d, n):
+    """out (bf16, of softmax weights in two bf16 terms) against oracle (out, lse, abs_out, size).  The first term is
+    off by B of the weight at most, the second by B of that: B^2 of each product; then the result's rounding."""
+    o, l, ab, size = ref
+    e = weight_err(size, l, d, n)[..., None]
+    tol = (ab * (2 * e + n * U + B * B) + 4 * U * np.abs(o)) * (1 + B) + B * np.abs(o)
+    bad = np.abs(host(out) - o) - tol
+    assert np.all(bad <= 1e-30), (float(bad.max()), np.argwhere(bad > 0)[:4].tolist())
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("group,few,more", [(8, [1, 2, 2, 1], [3, 4]), (1, [16, 1, 5, 16], [17, 32]), (5, [3, 1, 2, 3], [6, 60])])
+def test_few_rows_keep_two_terms_next_to_more_rows(d, group, few, more):
+    """Sequences of up to 16 rows between sequences of 17 to 32, and of a chunk's."""
+    rng = np.random.default_rng(group + d)
+    hk, page = 2, 64
+    ql, kl = [few[0], more[0], few[1], more[1], few[2], few[3]], [60, 1500, 2900, 700, 63, 333]
+    say("few rows next to more", d, group)
+    p, kp, vp, t = filled(rng, kl, page, hk, d, "bf16")
+    q = rows(rng, sum(ql), group * hk, d, "bf16").cuda()
+    out, lse = run_pages(p, q, ql, kl)
+    ref = P.pages_attention(host(q), kp, vp, t, ql, kl, d ** -0.5)
+    check_attention(out, lse, ref, d, max(kl), True)
+    at = np.cumsum([0] + ql)
+    for i in (0, 2, 4, 5):
+        r = slice(at[i], at[i + 1])
+        check_two_terms(out[r], [x[r] for x in ref], d, kl[i])
+    # one range of keys, alone and in company: the same bits
+    for i in (0, 4):
+        alone = E.Pages(p.k, p.v, p.page_table[i:i + 1])
+        r = slice(at[i], at[i + 1])
+        o, l = run_pages(alone, q[r], ql[i:i + 1], kl[i:i + 1])
+        assert torch.equal(o, out[r]) and torch.equal(l, lse[r])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("group,ql", [(8, [8, 1, 40]), (16, [4, 2, 30]), (1, [64, 7, 100])])
+def test_block_attention_of_few_rows_in_two_terms(d, group, ql):
+    """Sequences of up to 64 rows next to one of more."""
+    rng = np.random.default_rng(group + d)
+    hk, page, block, topn, kl = 2, 64, 32, 6, [900, 1300, 800]
+    say("block attention, few rows", d, group)
+    p, kp, vp, t = filled(rng, kl, page, hk, d, "bf16")
+    q = rows(rng, sum(ql), group * hk, d, "bf16").cuda()
+    idx = np.sort(rng.integers(0, 24, (sum(ql), hk, topn)), -1).astype(np.int32)
+    out, lse = run_pages(p, q, ql, kl, idx=ints(idx), block=block)
+    ref = P.pages_attention(host(q), kp, vp, t, ql, kl, d ** -0.5, idx, block)
+    check_attention(out, lse, ref, d, topn * block, True)
+    n = ql[0] + ql[1]
+    check_two_terms(out[:n], [x[:n] for x in ref], d, topn * block)
