@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <numeric>
 #include <string>
 
 #include "attn_host.h"
@@ -111,6 +112,13 @@ int64_t balanced_len(const AttnArgs& a, int64_t len, int64_t tile) {
   return len;
 }
 
+// Most queries that `per` row tiles in a row hold, counted from a multiple of
+// `per`: tok queries a tile, or tiles_q tiles a query, the first of which began
+// up to tiles_q - gcd tiles in front.
+int64_t unit_queries(int64_t per, int64_t tiles_q, int64_t tok) {
+  return tiles_q == 1 ? per * tok : (tiles_q - std::gcd(tiles_q, per) + per - 1) / tiles_q + 1;
+}
+
 // Sequences b0.. of the batch that are of the class, at most kAttnSeqs with
 // queries; returns the sequence after the last one seen, or -1 if the launch
 // would be too large.
@@ -194,7 +202,8 @@ int plan_attn(AttnChunk& ch, int src, int d, AttnClass cls, int b0, int32_t batc
   a.merged_stride = 0;
   if (per > 1)
     for (int i = 0; i < a.n_seq; ++i)
-      a.merged_stride = std::max(a.merged_stride, (int32_t)(per * a.tok * (a.s[i].split_len / block)) + kBlockEnds);
+      a.merged_stride = std::max(a.merged_stride, (int32_t)(unit_queries(per, (a.group + tile - 1) / tile, a.tok) *
+                                                            (a.s[i].split_len / block)) + kBlockEnds);
   ch.parts = parts;
   return b;
 }

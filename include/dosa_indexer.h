@@ -536,10 +536,14 @@ int dsa_block_select(const dsa_blocks* blocks, const int32_t* page_table, int32_
  * blocks idx[t, h, 0..topn-1] that are not behind its position.  Entries that
  * are negative or behind the query's own block are skipped, a block listed twice
  * counts twice.  Neighbouring queries whose lists ascend read the blocks that
- * they have in common once.  topn * block <= 2^20; the workspace holds up to 16
- * bytes for each entry of idx.  bf16: softmax weights are two bf16 terms for
- * sequences of up to 64 rows (queries times group heads) in groups of up to 16
- * heads, else rounded to bf16.  Otherwise as dsa_pages_attention. */
+ * they have in common once.  topn * block <= 2^20.  bf16: softmax weights are two
+ * bf16 terms for sequences of up to 64 rows (queries times group heads) in groups
+ * of up to 16 heads, else rounded to bf16.  Workspace: bf16 sequences of more than
+ * 64 rows take, for each unit of eight tiles of 16 rows (a tile holds up to eight
+ * queries, or a part of one query's heads), 16 bytes for each entry of the lists
+ * of the unit's queries, as many as a unit may hold, and 128 bytes; partial
+ * results come on top where few units are cut into ranges.  Otherwise as
+ * dsa_pages_attention. */
 size_t dsa_block_workspace_size(int32_t batch, const int32_t* q_lens, const int32_t* kv_lens, int32_t Hq, int32_t Hkv,
                                 int32_t d, int32_t dtype, int32_t block, int32_t topn);
 int dsa_block_attention(const dsa_pages* pages, const void* q, int64_t q_stride, const int32_t* q_lens,

@@ -865,3 +865,22 @@ def test_block_attention_of_few_rows_in_two_terms(d, group, ql):
     check_attention(out, lse, ref, d, topn * block, True)
     n = ql[0] + ql[1]
     check_two_terms(out[:n], [x[:n] for x in ref], d, topn * block)
+
+
+@pytest.mark.parametrize("group,ql", [(48, [30, 9]), (72, [25]), (128, [10, 3]), (160, [9]), (5, [70, 20])])
+def test_block_attention_stays_in_its_workspace(group, ql):
+    """Groups whose heads take several row tiles, units that begin within a query; long lists in any order, and
+    guards on both sides of the workspace."""
+    rng = np.random.default_rng(group)
+    hk, d, page, block, topn, kl = 1, 64, 64, 32, 40, [2000, 1700][:len(ql)]
+    say("block attention workspace", group, ql)
+    p, kp, vp, t = filled(rng, kl, page, hk, d, "bf16")
+    q = rows(rng, sum(ql), group, d, "bf16").cuda()
+    idx = np.stack([rng.permutation(60)[:topn] for _ in range(sum(ql))])[:, None].astype(np.int32)
+    n = E.block_workspace_size(ql, kl, group, hk, d, "bf16", block, topn)
+    ws = torch.full((n + 8192,), 0xA5, dtype=torch.uint8, device="cuda")
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+    E.dsa_block_attention(p, q, ql, kl, ints(idx), block, out, lse, workspace=ws[4096:4096 + n])
+    torch.cuda.synchronize()
+    assert torch.all(ws[:4096] == 0xA5) and torch.all(ws[4096 + n:] == 0xA5)
+    check_attention(out, lse, P.pages_attention(host(q), kp, vp, t, ql, kl, d ** -0.5, idx, block), d, topn * block, True)

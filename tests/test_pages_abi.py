@@ -250,3 +250,27 @@ def test_empty_calls():
         E.dsa_pages_attention(p, q, *lens, torch.empty_like(q), workspace=space(256), stream=STREAM)
         E.dsa_block_select(E.Blocks.empty(p, 16), p.page_table, q, *lens, i32(0, 2, 4), stream=STREAM)
         E.dsa_block_attention(p, q, *lens, i32(0, 2, 4), 16, torch.empty_like(q), workspace=space(256), stream=STREAM)
+
+
+@pytest.mark.parametrize("group", [1, 2, 3, 5, 8, 16, 17, 20, 24, 32, 40, 64, 128, 200, 256])
+def test_block_workspace_holds_the_lists_of_a_units_queries(group):
+    """More than 512 units and so one range of keys, no partial results: units of eight row tiles, each with the lists of its queries and
+    eight records behind them.  The most queries of a unit by counting them."""
+    q, block, topn = 4096, 64, 300
+    tile_q, per_query = max(1, min(16 // group, 8)), -(-group // 16)      # queries of a tile, tiles of a query
+    first = [t // per_query if group > 16 else t * tile_q for t in range(0, 8 * 1000)]
+    most = max(len({first[t + x] for x in range(8)}) * tile_q for t in range(0, len(first), 8))
+    units = -(-(-(-q // tile_q) * per_query) // 8)
+    for hk in (1, 4, 8, 16):
+        if group * hk > 1024 or units * hk <= 512:
+            continue
+        got = E.block_workspace_size([q], [q * 20], group * hk, hk, 128, "bf16", block, topn)
+        assert 0 <= got - units * hk * (most * topn + 8) * 16 < 512
+
+
+def test_block_workspace_of_large_groups():
+    """16 bytes an entry, not 128, where a query's heads fill a unit."""
+    entries = 4096 * 2048
+    for hq in (64, 128):
+        got = E.block_workspace_size([4096], [1 << 20], hq, 1, 128, "bf16", 64, 2048)
+        assert got <= 16 * entries + 128 * 4096 + 512
