@@ -263,7 +263,7 @@ int run_attn(int src, const AttnArgs& base, int32_t batch, const int32_t* q_lens
     need = attn_workspace(src, batch, q_lens, kv_lens, base.Hq, base.Hkv, d, base.topk, base.block, &threads);
     if (need == 0) return fail(DOSA_ERR_UNSUPPORTED, "too many row tiles and key ranges for one launch");
   }
-  const int st = check_launch("attention", threads + 64 * 8 * 8);   // its last workgroups may be partly empty
+  const int st = check_launch("attention", threads + 64 * 8);   // its last workgroup may be partly empty
   if (st != DOSA_OK) return st;
   if (workspace == nullptr || workspace_bytes < need || !aligned(workspace, 16))
     return fail(DOSA_ERR_WORKSPACE, "workspace needs " + std::to_string(need) + " bytes, 16-byte aligned");

@@ -345,3 +345,14 @@ def test_cpu_tensors_refused_and_streams_of_another_device():
         with AT._On(torch.device("cuda", 0), other):
             pass
     assert ei.value.status == -1 and "stream" in str(ei.value)
+
+
+def test_attention_launches_next_to_2_32_threads_are_accepted():
+    """2^26 - 64 wavefronts: refused for their missing workspace, not for their number; 2^26 are too many.  (The
+    addresses are not looked at.)"""
+    L = E.lib()
+    at = 1 << 20
+    for n, status in (((1 << 20) - 1, -3), (1 << 20, -2)):
+        one = AT._lens([n])
+        assert L.dsa_prompt_attention(at, 1024 * 128, at, 128, at, 128, 0, one, one, 1, 1024, 1, 128, 0.1, at, None, None, 0,
+                                      None) == status
