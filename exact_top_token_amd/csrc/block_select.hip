@@ -27,6 +27,8 @@
 // half the wavefronts (125 us).  Decode of 32 sequences x 2 queries, 64 heads on 8, 32
 // of up to 1600 blocks: 16 us, latency: pages, scales and codes in turn.  One query
 // over 16384 blocks 94 us: a kv head is one workgroup's.
+#include <atomic>
+
 #include "attn_device.h"
 #include "pages_internal.h"
 
@@ -354,9 +356,20 @@ template <int D, int MT, int PAD, bool MANY>
 hipError_t go(const SelectArgs& p, hipStream_t s) {
   const unsigned lds = (unsigned)(16 / PAD * MT) * (unsigned)p.stride * 4u;
   if (lds > (32u << 10)) {
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&select_kernel<D, MT, PAD, MANY>),
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    // The limit is the function's, not the launch's: it is raised once on each device, to the most that a launch can
+    // ask for, so that no call lowers what another thread's is about to use.
+    constexpr int most = 16 / PAD * MT == 1 ? (int)(kSelectBlocks + 16) * 4 : (int)kSelectLds;
+    static std::atomic<uint64_t> raised{0};
+    int dev;
+    hipError_t e = hipGetDevice(&dev);
     if (e != hipSuccess) return e;
+    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+    if ((raised.load(std::memory_order_acquire) & bit) == 0) {
+      e = hipFuncSetAttribute(reinterpret_cast<const void*>(&select_kernel<D, MT, PAD, MANY>),
+                              hipFuncAttributeMaxDynamicSharedMemorySize, most);
+      if (e != hipSuccess) return e;
+      raised.fetch_or(bit, std::memory_order_release);
+    }
   }
   select_kernel<D, MT, PAD, MANY><<<dim3((unsigned)p.n_units), dim3(64 * select_waves(MT)), lds, s>>>(p);
   return hipGetLastError();

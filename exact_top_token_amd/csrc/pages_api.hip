@@ -107,8 +107,6 @@ int move_pages(bool assign, int32_t* table, int32_t max_pages, int32_t page_size
 // Work split of the choice of blocks.  LDS holds the scores of a workgroup's
 // tokens: up to kSelectLds bytes where several tokens share a workgroup, more for one.
 // ---------------------------------------------------------------------------
-constexpr int64_t kSelectLds = 64 << 10;
-constexpr int64_t kSelectBlocks = 32768;
 constexpr int64_t kSelectTiles = 2;
 
 int64_t select_stride(const SelectArgs& a, int32_t kv_len) {

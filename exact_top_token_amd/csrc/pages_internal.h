@@ -55,6 +55,8 @@ struct RowsArgs {
 hipError_t launch_rows_append(bool f32, int d, const RowsArgs& p, hipStream_t s);
 
 // ---- choice of blocks ----
+constexpr int64_t kSelectLds = 64 << 10;       // bytes of scores where a workgroup takes several tokens
+constexpr int64_t kSelectBlocks = 32768;       // of a sequence
 struct SelectSeq {
   int32_t unit0;      // first workgroup
   int32_t q_row0, q_len, kv_len, b;

@@ -884,3 +884,53 @@ def test_block_attention_stays_in_its_workspace(group, ql):
     torch.cuda.synchronize()
     assert torch.all(ws[:4096] == 0xA5) and torch.all(ws[4096 + n:] == 0xA5)
     check_attention(out, lse, P.pages_attention(host(q), kp, vp, t, ql, kl, d ** -0.5, idx, block), d, topn * block, True)
+
+
+def test_select_lengths_in_two_threads_and_a_graph():
+    """The scores of 3 tokens, of 30000 blocks and of few, in turn from two host threads on their own streams: the
+    kernel's limit of LDS is one for all of them.  Then the largest captured and replayed."""
+    import threading
+
+    rng = np.random.default_rng(31)
+    hk, d, page, block = 1, 64, 64, 16
+    lens = [16 * 30001, 16 * 9000, 16 * 700]
+    b, c, s, t = summarised(rng, [max(lens)], page, block, hk, d)
+    tab, q = ints(t), rows(rng, 3, 16, d, "bf16").cuda()
+    want = {n: torch.from_numpy(run_select(b, t, q, [3], [n], 9, 1, 2)) for n in lens}
+    for n in lens[1:]:
+        ref = P.select(host(q), c, s, t, [3], [n], block, page, 9, 1, 2)
+        assert np.array_equal(want[n].numpy(), ref)
+    torch.cuda.synchronize()
+    got = [[], []]
+
+    def work(i):
+        st = torch.cuda.Stream()
+        for r in range(30):
+            n = lens[(r + i) % 3]
+            idx = torch.empty(3, hk, 9, dtype=torch.int32, device="cuda")
+            st.wait_stream(torch.cuda.current_stream())
+            E.dsa_block_select(b, tab, q, [3], [n], idx, stream=st)
+            got[i].append((n, idx))
+        st.synchronize()
+
+    say("select from two threads")
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for x in threads:
+        x.start()
+    for x in threads:
+        x.join()
+    torch.cuda.synchronize()
+    assert [len(x) for x in got] == [30, 30]
+    for n, idx in got[0] + got[1]:
+        assert torch.equal(idx.cpu(), want[n])
+    idx = torch.empty(3, hk, 9, dtype=torch.int32, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=torch.cuda.Stream()):
+        E.dsa_block_select(b, tab, q, [3], [lens[0]], idx)
+    for r in range(3):
+        idx.fill_(-9)
+        E.dsa_block_select(b, tab, q, [3], [lens[2]], torch.empty_like(idx))
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(idx.cpu(), want[lens[0]])
+    g.reset()
