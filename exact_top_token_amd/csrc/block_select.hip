@@ -36,6 +36,7 @@ namespace dosa {
 
 namespace {
 
+constexpr float kLargest = 0x1.fffffep127f;
 constexpr int kFew = 256;                // scores that a wavefront chooses from in registers
 constexpr int kCols = 4;                 // column tiles a wavefront has in flight, one block a lane
 
@@ -133,7 +134,10 @@ __global__ __launch_bounds__(64 * select_waves(MT)) void select_kernel(const Sel
       for (int s = 0; s < KS; ++s) {
         row16(p.f32 != 0, p.q, q_at(i, pass) + 64 * s, x[s]);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) top = fmaxf(top, fabsf(x[s][e]));
+        for (int e = 0; e < 16; ++e) {
+          x[s][e] = x[s][e] == x[s][e] ? fminf(fmaxf(x[s][e], -kLargest), kLargest) : 0.f;     // queries that are not finite
+          top = fmaxf(top, fabsf(x[s][e]));
+        }
       }
       top = max_groups(top);
       const int e = (int)((__float_as_uint(top) + (1u << 16)) >> 23) - 127 - 6;

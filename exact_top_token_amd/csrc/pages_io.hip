@@ -72,6 +72,8 @@ __global__ __launch_bounds__(256) void release_kernel(const AssignArgs p) {
   }
 }
 
+constexpr double kLargest = 0x1.fffffep127;      // fp32's
+
 // 16 bytes of a row -> its elements in 64 bits.
 template <bool F32>
 __device__ __forceinline__ void widen64(i4 a, double* x) {
@@ -162,7 +164,8 @@ __global__ __launch_bounds__(256) void rows_append_kernel(const RowsArgs p) {
     double y = 0.;
 #pragma unroll
     for (int w = 0; w < SUBS; ++w) y += sums[w][lane * E + e];
-    x[e] = y * (1.0 / p.run);          // a power of two
+    y *= 1.0 / p.run;                  // a power of two
+    x[e] = y == y ? fmin(fmax(y, -kLargest), kLargest) : 0.;     // keys that are not finite
     top = fmax(top, fabs(x[e]));
   }
 #pragma unroll

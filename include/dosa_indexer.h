@@ -480,7 +480,9 @@ typedef struct {
  *   scales [num_pages, page_size / block, Hkv] bytes: byte e scales a row by
  *          2^(e-127), the smallest e in 1..254 for which every element of the
  *          mean is below 127.5 scales in magnitude; codes are rounded to the
- *          nearest, ties to even.  The mean is summed in 64 bits. */
+ *          nearest, ties to even.  The mean is summed in 64 bits.
+ * An infinite element of a mean counts as fp32's largest number of its sign, one
+ * that is no number as 0; so do elements of dsa_block_select's queries. */
 typedef struct {
   int8_t* codes;
   uint8_t* scales;

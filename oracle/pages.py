@@ -43,12 +43,18 @@ def release(table, free, count, new_lens, kv_lens, page):
 
 def to_grid(x):
     """Row [d] -> whole numbers -127..127 and the exponent of their unit."""
-    x = np.asarray(x, np.float64)
+    most = float(np.finfo(np.float32).max)
+    x = np.nan_to_num(np.asarray(x, np.float64), nan=0.0, posinf=most, neginf=-most)
     top = float(np.abs(x).max())
     e = -126
     while e < 127 and top >= 127.5 * 2.0 ** e:
         e += 1
     return np.rint(x / 2.0 ** e).astype(np.int64), e
+
+
+def _sum(x):
+    with np.errstate(invalid="ignore"):
+        return math.fsum(x) if np.isfinite(x).all() else float(np.sum(x))
 
 
 def summaries(k_pages, table, q_lens, kv_lens, block, codes, scales):
@@ -62,7 +68,7 @@ def summaries(k_pages, table, q_lens, kv_lens, block, codes, scales):
                 continue
             rows = k_pages.reshape(-1, *k_pages.shape[2:])[at[j * block:(j + 1) * block]].astype(np.float64)
             for h in range(k_pages.shape[2]):
-                mean = np.array([math.fsum(rows[:, h, c]) / block for c in range(rows.shape[2])])
+                mean = np.array([_sum(rows[:, h, c]) / block for c in range(rows.shape[2])])
                 row, e = to_grid(mean)
                 pg, blk = divmod(int(at[j * block]) // block, page // block)
                 codes[pg, blk, h], scales[pg, blk, h] = row, e + 127

@@ -934,3 +934,41 @@ def test_select_lengths_in_two_threads_and_a_graph():
         torch.cuda.synchronize()
         assert torch.equal(idx.cpu(), want[lens[0]])
     g.reset()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_summaries_of_keys_that_are_not_finite(dtype, d):
+    """Infinite and undefined means: the largest number of their sign, and 0; other heads and blocks as ever."""
+    rng = np.random.default_rng(40 + d)
+    hk, page, block, kl = 3, 32, 16, [96]
+    say("summaries, not finite", dtype, d)
+    k = rows(rng, 96, hk, d, dtype)
+    k[3, 0, 5], k[7, 0, 5] = float("inf"), 1.0
+    k[20, 1, 0], k[21, 1, 0], k[22, 1, 7] = float("inf"), float("-inf"), float("-inf")
+    k[40, 2, 63], k[41, 2, 8] = float("nan"), 3e38
+    k[50, :, :] = float("nan")
+    k[70, 0, :], k[80, 1, ::2] = float("-inf"), float("inf")
+    p = E.Pages.empty(3, page, hk, d, ints([[2, 0, 1]]), dtype)
+    b = E.Blocks.empty(p, block)
+    E.dsa_pages_append(p, k.cuda(), k.cuda(), kl, kl, blocks=b)
+    codes, scales = P.summaries(host(p.k), np.array([[2, 0, 1]]), kl, kl, block, np.zeros(b.codes.shape), np.zeros(b.scales.shape))
+    assert np.array_equal(b.codes.cpu().numpy(), codes) and np.array_equal(b.scales.cpu().numpy(), scales)
+    assert codes.reshape(6, hk, d)[[4, 0, 2], [0, 0, 2], [5, 5, 63]].tolist()[0] == 64
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("hq", [1, 4, 20])
+def test_select_with_queries_that_are_not_finite(dtype, hq):
+    rng = np.random.default_rng(41 + hq)
+    ql, kl, d, page, block = [12], [900], 64, 32, 16
+    say("select, not finite", dtype, hq)
+    b, c, s, t = summarised(rng, kl, page, block, 1, d)
+    q = rows(rng, 12, hq, d, dtype)
+    q[0, 0, 3], q[1, 0, 5], q[2, 0, 7] = float("inf"), float("-inf"), float("nan")
+    q[3], q[4], q[5] = float("nan"), float("inf"), float("-inf")
+    q[6, hq - 1] = float("nan")
+    q[7, hq - 1, ::2], q[8, hq - 1, 1::3] = float("-inf"), float("inf")
+    q[9, 0, 0], q[9, 0, 1] = float("inf"), float("-inf")
+    got = run_select(b, t, q.cuda(), ql, kl, 6, 1, 2)
+    assert np.array_equal(got, P.select(host(q), c, s, t, ql, kl, block, page, 6, 1, 2))

@@ -55,3 +55,15 @@ def test_attention_over_pages_is_prompt_attention():
     twice = P.pages_attention(q, kp, vp, table, ql, kl, 0.3, np.broadcast_to(np.array([0, 0]), (23, hk, 2)), 16)
     once = P.pages_attention(q, kp, vp, table, ql, kl, 0.3, np.broadcast_to(np.array([0]), (23, hk, 1)), 16)
     assert np.allclose(twice[0], once[0]) and np.allclose(twice[1], once[1] + np.log(2.0))
+
+
+def test_numbers_that_are_not_finite():
+    most = float(np.finfo(np.float32).max)
+    row, e = P.to_grid([np.inf, -np.inf, np.nan, most, 0.0, 2.0 ** 122])
+    assert row.tolist() == [64, -64, 0, 64, 0, 1] and e == 122
+    k = np.zeros((1, 16, 1, 4))
+    k[0, 3, 0] = [np.inf, -np.inf, np.nan, 16.0]
+    k[0, 5, 0] = [1.0, -np.inf, 2.0, 0.0]
+    k[0, 6, 0] = [-np.inf, 5.0, 2.0, 0.0]
+    c, s = P.summaries(k, np.zeros((1, 1), int), [16], [16], 16, np.zeros((1, 1, 1, 4)), np.zeros((1, 1, 1)))
+    assert c.ravel().tolist() == [0, -64, 0, 0] and s.ravel().tolist() == [249]
