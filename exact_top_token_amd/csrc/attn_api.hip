@@ -203,7 +203,7 @@ int plan_attn(AttnChunk& ch, int src, int d, AttnClass cls, int b0, int32_t batc
   if (per > 1)
     for (int i = 0; i < a.n_seq; ++i)
       a.merged_stride = std::max(a.merged_stride, (int32_t)(unit_queries(per, (a.group + tile - 1) / tile, a.tok) *
-                                                            (a.s[i].split_len / block)) + kBlockEnds);
+                                                            (std::min(a.s[i].split_len, topk) / block)) + kBlockEnds);
   ch.parts = parts;
   return b;
 }

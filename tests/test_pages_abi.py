@@ -274,3 +274,9 @@ def test_block_workspace_of_large_groups():
     for hq in (64, 128):
         got = E.block_workspace_size([4096], [1 << 20], hq, 1, 128, "bf16", 64, 2048)
         assert got <= 16 * entries + 128 * 4096 + 512
+
+
+def test_block_workspace_of_lists_that_fill_no_whole_step():
+    """150 blocks of 16, ranges in steps of 64 keys: room for 150 entries of a list, not 152."""
+    got = E.block_workspace_size([70], [700], 512, 128, 64, "bf16", 16, 150)
+    assert 0 <= got - 3 * 128 * (32 * 150 + 8) * 16 < 512
