@@ -972,3 +972,29 @@ def test_select_with_queries_that_are_not_finite(dtype, hq):
     q[9, 0, 0], q[9, 0, 1] = float("inf"), float("-inf")
     got = run_select(b, t, q.cuda(), ql, kl, 6, 1, 2)
     assert np.array_equal(got, P.select(host(q), c, s, t, ql, kl, block, page, 6, 1, 2))
+
+
+@pytest.mark.parametrize("group,q,topn,window", [(1, 130, 40, 32), (4, 70, 150, 64), (8, 40, 300, 128)])
+@pytest.mark.parametrize("order", ["any", "ascending"])
+def test_block_attention_of_lists_longer_than_the_merge_holds(group, q, topn, window, order):
+    """The merge of a unit's lists keeps `window` entries of each at a time: so many units that every list is one
+    range, lists a few times as long, with entries twice, entries to skip and lists that end early."""
+    rng = np.random.default_rng(group)
+    hk, d, page, block, kl = 128, 64, 32, 16, 700
+    say("block lists of several windows", group, order)
+    tok = min(8, 16 // group)
+    units = -(-(-(-q // tok)) // 8) * hk
+    n = E.block_workspace_size([q], [kl], group * hk, hk, d, "bf16", block, topn)
+    assert topn > window and 0 <= n - units * (8 * tok * topn + 8) * 16 < 512        # one range
+    p, kp, vp, t = filled(rng, [kl], page, hk, d, "bf16")
+    x = rows(rng, q, group * hk, d, "bf16").cuda()
+    idx = rng.integers(-3, kl // block + 4, (q, hk, topn)).astype(np.int32)
+    if order == "ascending":
+        idx = np.sort(np.where(idx < 0, 1 << 20, idx), -1).astype(np.int32)
+        idx[idx == 1 << 20] = -1
+    idx[3, :, 5:], idx[7] = -1, -1
+    out, lse = run_pages(p, x, [q], [kl], idx=ints(idx), block=block)
+    for h in (0, 57, 127):
+        g, one = slice(h * group, (h + 1) * group), slice(h, h + 1)
+        ref = P.pages_attention(host(x[:, g]), kp[:, :, one], vp[:, :, one], t, [q], [kl], d ** -0.5, idx[:, one], block)
+        check_attention(out[:, g], lse[:, g], ref, d, topn * block, True)
