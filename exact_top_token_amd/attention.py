@@ -57,17 +57,22 @@ def declare(L) -> None:
         fn.argtypes, fn.restype = args, res
 
 
-_loaded = _torch = None
+_loaded = _torch = _device = _stream = None
 
 
 def _lib():
-    global _loaded, _torch
+    global _loaded, _torch, _device, _stream
     if _loaded is None:
         import torch
 
         from . import lib
 
         _loaded, _torch = lib(), torch
+        # the current device, and the handle of torch.cuda.current_stream(): without the objects where torch has
+        # such functions (they are not among its public ones)
+        _device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+        _stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda index: torch.cuda.current_stream(index).cuda_stream)
     return _loaded
 
 
@@ -167,11 +172,11 @@ class _On:
             _bad(f"tensors are on {self.device}, not on a GPU")
         if getattr(self.stream, "device", self.device) != self.device:
             _bad(f"stream is of {self.stream.device}, the tensors are on {self.device}")
-        if torch._C._cuda_getDevice() != self.device.index:
+        if _device() != self.device.index:
             self.back = torch.cuda.device(self.device)
             self.back.__enter__()
-        if self.stream is None:     # the handle of torch.cuda.current_stream(), without the object
-            return torch._C._cuda_getCurrentRawStream(self.device.index)
+        if self.stream is None:
+            return _stream(self.device.index)
         return int(getattr(self.stream, "cuda_stream", self.stream))
 
     def __exit__(self, *exc):

@@ -356,3 +356,18 @@ def test_attention_launches_next_to_2_32_threads_are_accepted():
         one = AT._lens([n])
         assert L.dsa_prompt_attention(at, 1024 * 128, at, 128, at, 128, 0, one, one, 1, 1024, 1, 128, 0.1, at, None, None, 0,
                                       None) == status
+
+
+def test_streams_where_torch_has_no_function_for_their_handles(monkeypatch):
+    """The current stream's handle comes from torch's public objects where its shorter way is missing."""
+    with monkeypatch.context() as m:
+        m.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+        m.delattr(torch._C, "_cuda_getDevice", raising=False)
+        m.setattr(torch.cuda, "current_device", lambda: 0)
+        m.setattr(torch.cuda, "current_stream", lambda index=None: SimpleNamespace(cuda_stream=77 + index))
+        for name in ("_loaded", "_device", "_stream"):
+            m.setattr(AT, name, None)
+        AT._lib()
+        with AT._On(torch.device("cuda", 0), None) as st:
+            assert st == 77
+    AT._lib()
