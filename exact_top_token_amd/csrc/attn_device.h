@@ -24,7 +24,12 @@ constexpr float kLn2 = 0.69314718055994530942f;
 // place; the other weights kernels always subtract first.
 constexpr float kFar = 1024.f;
 
+typedef __attribute__((address_space(4))) const int32_t scalar_i32;      // read through the scalar cache
+
 __device__ __forceinline__ int lane64() { return (int)__lane_id(); }
+__device__ __forceinline__ int below(uint64_t mask) {        // lanes of the mask in front of this one
+  return __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0u));
+}
 
 // The record of the launch that unit `u` belongs to: `first` of the records
 // ascends.  Uniform.
@@ -88,6 +93,13 @@ __device__ __forceinline__ void split3(float x, float* t) {
 // a row that gives nothing.
 __device__ __forceinline__ float weight_of(float s, float scale, float lse) {
   return __builtin_amdgcn_exp2f(fmaf(s, scale, -lse) * kLog2e);
+}
+
+// 16-byte chunk of a key tile's row `r` in LDS that holds logical chunk c: 16
+// lanes read one chunk of 16 rows.
+template <int D>
+__device__ __forceinline__ int k_chunk(int r, int c) {
+  return D == 128 ? c ^ (r & 15) : c ^ ((r >> 1) & 7);
 }
 
 // Maximum / sum over the four 16-lane groups (lanes l, l^16, l^32, l^48).

@@ -55,12 +55,8 @@ __device__ __forceinline__ f16v mfma32(b8 a, b8 b, f16v c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
 
-// 16-byte chunk of row `r` that holds logical chunk c.  Key tiles: 16 lanes
-// read one chunk of 16 rows; value tiles: 16 lanes read 32 bytes of 4 rows.
-template <int D>
-__device__ __forceinline__ int k_chunk(int r, int c) {
-  return D == 128 ? c ^ (r & 15) : c ^ ((r >> 1) & 7);
-}
+// 16-byte chunk of a value tile's row `r` that holds logical chunk c: 16 lanes
+// read 32 bytes of 4 rows.
 template <int D>
 __device__ __forceinline__ int v_chunk(int r, int c) {
   return D == 128 ? c ^ ((r & 3) << 2) : c ^ (((r >> 1) & 1) << 2);
@@ -163,7 +159,6 @@ __global__ __launch_bounds__(64 * NW, 2) void prompt_kernel(const AttnArgs p) {
   // rows, `part`; those past the last visible key repeat it.  Rows without a page
   // are read from page 0: their scores are masked, and their values, which a
   // weight of 0 is still multiplied by, become zeros in LDS.
-  typedef __attribute__((address_space(4))) const int32_t scalar_i32;
   struct Pages {
     i4 page;                            // the first alone where a tile lies in one page
     int32_t off;                        // of this wavefront's rows in their page

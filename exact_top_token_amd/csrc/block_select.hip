@@ -44,9 +44,6 @@ __device__ __forceinline__ uint32_t ordered(float x) {
   const uint32_t b = __float_as_uint(x);
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
-__device__ __forceinline__ int below(uint64_t mask) {        // lanes of the mask in front of this one
-  return __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0u));
-}
 
 // The value of lane l^16 (l^32).
 __device__ __forceinline__ float other_half16(float x) {

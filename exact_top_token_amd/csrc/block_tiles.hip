@@ -44,7 +44,6 @@ typedef short s4v __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) uint8_t lbyte;
 typedef __attribute__((address_space(3))) b8 lds_b8;
 typedef __attribute__((address_space(3))) s4v lds_s4;
-typedef __attribute__((address_space(4))) const int32_t scalar_i32;
 typedef __attribute__((address_space(4))) const i4 scalar_i4;
 
 constexpr int NW = kBlockTileWaves;
@@ -81,9 +80,6 @@ __device__ __forceinline__ uint32_t least64(uint32_t x) {
   const uint32_t a = min((uint32_t)__builtin_amdgcn_readlane((int)x, 0), (uint32_t)__builtin_amdgcn_readlane((int)x, 16));
   const uint32_t b = min((uint32_t)__builtin_amdgcn_readlane((int)x, 32), (uint32_t)__builtin_amdgcn_readlane((int)x, 48));
   return min(a, b);
-}
-__device__ __forceinline__ int below(uint64_t mask) {        // lanes of the mask in front of this one
-  return __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0u));
 }
 
 constexpr int kMergeWaves = 4;
@@ -177,12 +173,8 @@ __global__ __launch_bounds__(64 * kMergeWaves) void block_merge_kernel(const Att
   if (lane < kBlockEnds) out[lane] = i4{0, -1, 0, 0};
 }
 
-// 16-byte chunk of row `r` that holds logical chunk c.  Key tiles: 16 lanes
-// read one chunk of 16 rows; value tiles: 32 lanes read 32 bytes of 8 rows.
-template <int D>
-__device__ __forceinline__ int k_chunk(int r, int c) {
-  return D == 128 ? c ^ (r & 15) : c ^ ((r >> 1) & 7);
-}
+// 16-byte chunk of a value tile's row `r` that holds logical chunk c: 32 lanes
+// read 32 bytes of 8 rows.
 template <int D>
 __device__ __forceinline__ int v_chunk(int r, int c) {
   return D == 128 ? c ^ ((r & 7) << 1) : c ^ (((r >> 1) & 3) << 1);
@@ -280,7 +272,7 @@ __global__ __launch_bounds__(64 * NW, 4) void block_tiles_kernel(const AttnArgs 
     }
     if (rec[0][1] >= 0) {
       sub += kKeys;
-      if (RUNS > 1 || sub == p.block || sub > p.block) {
+      if (RUNS > 1 || sub >= p.block) {
         sub = 0;
         list += RUNS;
 #pragma unroll

@@ -267,7 +267,6 @@ int dsa_block_select(const dsa_blocks* blocks, const int32_t* page_table, int32_
     a.max_pages = max_pages;
     a.num_pages = blocks->num_pages;
     a.Hkv = blocks->Hkv;
-    a.Hq = Hq;
     a.group = Hq / blocks->Hkv;
     a.lb = __builtin_ctz((unsigned)blocks->block);
     a.topn = topn;

@@ -69,7 +69,7 @@ struct SelectArgs {
   int32_t* idx;       // [total_q, Hkv, topn]
   int64_t q_stride;   // elements
   Div div;            // by the blocks of a page
-  int32_t max_pages, num_pages, Hkv, Hq, group;
+  int32_t max_pages, num_pages, Hkv, group;
   int32_t lb;         // log2 of the block
   int32_t f32;        // queries' type
   int32_t topn, sinks, local;

@@ -59,7 +59,6 @@ typedef __amdgpu_buffer_rsrc_t Rows;
 __device__ __forceinline__ Rows rows_at(const uint8_t* p, int bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0, bytes, 0x00027000);
 }
-typedef __attribute__((address_space(4))) const int32_t scalar_i32;
 
 template <bool F32, int D, int RT, bool SEL>
 __global__ __launch_bounds__(64 * kWaves) void pages_kernel(const AttnArgs p) {
