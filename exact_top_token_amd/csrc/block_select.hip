@@ -126,15 +126,22 @@ __global__ __launch_bounds__(64 * select_waves(MT)) void select_kernel(const Sel
     };
     // exponent of row n of tile i, its elements
     auto exponent = [&](int i, int pass, float x[KS][16]) -> int {
-      float top = 0.f;
+      float top = 0.f;                   // a maximum that a NaN goes through, two elements an instruction
 #pragma unroll
       for (int s = 0; s < KS; ++s) {
         row16(p.f32 != 0, p.q, q_at(i, pass) + 64 * s, x[s]);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          x[s][e] = x[s][e] == x[s][e] ? fminf(fmaxf(x[s][e], -kLargest), kLargest) : 0.f;     // queries that are not finite
-          top = fmaxf(top, fabsf(x[s][e]));
-        }
+        for (int e = 0; e < 16; ++e) top = __builtin_elementwise_maximum(top, fabsf(x[s][e]));
+      }
+      if (!(top <= kLargest)) {          // some element is not finite
+        top = 0.f;
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            x[s][e] = x[s][e] == x[s][e] ? fminf(fmaxf(x[s][e], -kLargest), kLargest) : 0.f;
+            top = fmaxf(top, fabsf(x[s][e]));
+          }
       }
       top = max_groups(top);
       const int e = (int)((__float_as_uint(top) + (1u << 16)) >> 23) - 127 - 6;
