@@ -55,7 +55,16 @@ constexpr int64_t kTiledPageRows = 32;   // over pages of rows: the wavefront ke
 constexpr int64_t kTiledResident = 256;  // workgroups of the tiled kernel: one a CU
 constexpr int64_t kTiledMinKeys = 512;
 
-constexpr int64_t kTiledBlockRows = 64;  // over listed blocks: half a workgroup's rows
+// Over listed blocks: half a workgroup's rows.  The tiled kernel shares what its
+// queries have in common, but waits some 65 us for a unit's 66 merged blocks one
+// after the other; the wavefront kernel reads every list, and takes as long as the
+// caches for that.  Wavefront and tiled kernel, 16 of about 130 blocks, d = 128, groups
+// of 8: one sequence of 64 rows 18 and 47 us, of 256 24 and 65; 8 of 64 38 and 50, of
+// 256 113 and 78; 32 of 64 145 and 99, of 256 433 and 176 (groups of 2: 8 of 64
+// 112 and 82; d = 64 with 32 blocks of 16: 32 of 256 115 and 125).  Which is faster
+// goes by all that the call reads; the choice goes by the sequence alone, so that
+// its weights are rounded alike in any company.
+constexpr int64_t kTiledBlockRows = 64;
 
 // Sequences that share launches.  Over bf16 pages the wavefront kernel's row
 // tiles decide how softmax weights are rounded, so sequences of one tile and of
@@ -87,6 +96,8 @@ AttnClass class_of(int src, int64_t rows, bool sel) {
 // keys takes a workgroup 1.8 us, as long as 9 MB of memory, and a unit about four
 // tiles to begin and end.  A scheduler's step of chunks of 1024 and 700 queries
 // over 9216 and 700 keys: 128 long units alone take 256 us, as two ranges each 150.
+// (d = 64 takes 1.3 us a tile and joins half the bytes, but numbers of its own choose
+// no better: of 21 batches two took 17 and 23% longer and the rest the same.)
 int64_t balanced_len(const AttnArgs& a, int64_t len, int64_t tile) {
   int64_t most = 0;
   for (int i = 0; i < a.n_seq; ++i) most = std::max<int64_t>(most, a.s[i].kv_len);

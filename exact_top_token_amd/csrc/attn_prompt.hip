@@ -32,7 +32,12 @@
 // bf16 for the second product, since two terms of them would double it in a
 // kernel that it bounds: outputs are off by 0.19% of their size (root mean
 // square) where fp32 weights and one rounding at the end leave 0.14%.  The
-// weights' sum is taken before the rounding.
+// weights' sum is taken before the rounding.  (Both sides over pages, d = 128:
+// one term 0.23% and 4.09 ms for 4096 queries over 65536 keys, two terms 0.17%,
+// all of it the result's own rounding, and 5.71 ms; chunks of 1024 and 700 next to
+// single tokens 0.31 and 0.37 ms; 4096 over 32768 with d = 64 2.58 and 3.59 ms.  A
+// third off what the result's type costs anyway does not pay for two fifths more
+// time.)
 #include <type_traits>
 
 #include "attn_device.h"
@@ -152,8 +157,8 @@ __global__ __launch_bounds__(64 * NW, 2) void prompt_kernel(const AttnArgs p) {
   };
 
   // The same over pages (4096 queries over 65536 keys, 32 heads on 8, d = 128:
-  // 3.85 to 3.97 ms, 1070 to 1110 TFLOP/s; 1024 over 16384 0.28 ms, in pages of 16
-  // with four look-ups a tile 0.34 ms).  A tile's page numbers (one of 64 rows, or of each 16)
+  // 3.83 to 4.17 ms on different boards, 1020 to 1110 TFLOP/s; 1024 over 16384 0.27
+  // to 0.28 ms, in pages of 16 with four look-ups a tile 0.34 ms).  A tile's page numbers (one of 64 rows, or of each 16)
   // are looked up through the scalar cache a turn before its keys are fetched and
   // kept until its values have been.  A wavefront's rows of a tile lie in 16
   // rows, `part`; those past the last visible key repeat it.  Rows without a page
@@ -307,7 +312,7 @@ __global__ __launch_bounds__(64 * NW, 2) void prompt_kernel(const AttnArgs p) {
       __builtin_amdgcn_sched_group_barrier(0x402, 112 / (2 * NS), 0);
     }
     if constexpr (PAGED && D == 64) {
-      // (4096 queries over 32768 keys, groups of 8: 2.47 against 2.67 ms; with d = 128, whose products hide
+      // (4096 queries over 32768 keys, groups of 8: 2.47 against 2.67 ms on one board; with d = 128, whose products hide
       // more, 2% slower)
       auto values = [&](auto sel) {
         constexpr int S = decltype(sel)::value;

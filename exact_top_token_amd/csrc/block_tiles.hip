@@ -23,8 +23,9 @@
 //
 // 4096 and 1500 queries, 64 heads on 8, d = 128, each 16 blocks of 64 of up to
 // 32768 keys, of which neighbours share half (66 different ones of 16 queries):
-// 0.54 ms and 31 us of merging; a wavefront a query takes 1.94 ms, merging two
-// queries in a wavefront without LDS 1.36.  Reading the blocks alone took 0.46 ms
+// 0.56 to 0.59 ms on different boards, of which 30 us the merge (under a trace 0.58
+// to 0.62 ms and 31 us); a wavefront a query takes 1.94 ms, merging two queries in
+// a wavefront without LDS 1.36.  Reading the blocks alone took 0.46 ms
 // (6.2 GB, two thirds from the dies' caches): a workgroup waits for its slowest
 // wavefront at every block, and the CU holds two.  Addresses worked out anew for
 // every load and scores masked one by one, not rows, cost 0.05 ms.
@@ -32,6 +33,13 @@
 // barrier for each half, took 0.62 ms, in four slots 0.63 (against 0.56, merging
 // included); tiles of 32 keys with three under way 0.70, sixteen wavefronts of 32
 // queries 0.92, the merge by one of the eight wavefronts 1.24.
+//
+// Weights are rounded to bf16 once for their product with v, their sum is taken
+// before: outputs are off by 0.23% of their size (root mean square) where fp32
+// weights and the result's rounding leave 0.17%.  Two terms leave 0.17% too, in 0.72
+// instead of 0.59 ms (groups of 4, 16 of 512 blocks: 0.48 and 0.41; d = 64, 64 of
+// 2048 blocks of 16: 0.72 and 0.59): a third off what the result's type costs anyway
+// does not pay for a fifth more time.
 #include <type_traits>
 
 #include "attn_device.h"

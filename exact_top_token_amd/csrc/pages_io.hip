@@ -100,8 +100,9 @@ __device__ __forceinline__ void widen64(i4 a, double* x) {
 // summed, those that are not the call's read from the page.
 //
 // The mean is summed in 64 bits: keys of 8 or 24 significant bits add up without
-// rounding unless their exponents lie 38 (23) apart, so the codes do not depend
-// on the order.  The scale 2^e is the smallest power of two with max |mean| <
+// rounding, and so in any order, unless their exponents lie 38 (23) apart; the order
+// goes by the positions in the block, so the codes do not depend on which calls
+// wrote its keys either way.  The scale 2^e is the smallest power of two with max |mean| <
 // 127.5 2^e: 127.5 = 2^6 (2 - 2^-7), so adding 2^-7 to the significand carries
 // into the exponent exactly where e has to be one more.
 template <bool F32, int D>

@@ -295,8 +295,8 @@ __global__ __launch_bounds__(64 * kWaves) void pages_kernel(const AttnArgs p) {
     } else {
       // one row tile: weights as two bf16 terms, 16 significant bits.  The matrix unit waits for memory here, and
       // the result's rounding stays the only one that shows.  Two row tiles have no registers for that (32
-      // sequences x 4 queries in groups of 8 over 871K keys 811 against 746 us): weights rounded to bf16, off by
-      // 2^-9 at most, their sum taken before
+      // sequences x 4 queries in groups of 8 over 871K keys 814 against 744 us): weights rounded to bf16, their
+      // sum taken before, and outputs off by 0.23% of their size (root mean square) instead of 0.17%
       constexpr int TERMS = RT == 1 ? 2 : 1;
       b8 pf[RT][TERMS];
 #pragma unroll
